@@ -249,11 +249,12 @@ def _plain(s):
         codes, scales = _quantise(_act(g, case["act"]) * u, case["qtype"], case["mode"])
         return {"codes": codes, "scales": scales}
     W, e, counts = case["W"], case["e"], s["counts"]
-    xs = _segments(s["x"].float(), counts, W, e)
-    if op == "gmm_grad":
-        w, dys = s["weight"].float(), torch.split(s["dout"].float(), _expert_sizes(counts, W, e))
+    if op == "gmm_grad":  # the forward call's permuted rows: expert after expert
+        sizes = _expert_sizes(counts, W, e)
+        xs, w, dys = torch.split(s["x"].float(), sizes), s["weight"].float(), torch.split(s["dout"].float(), sizes)
         dx = _to_arrival([dy @ w[j].t() for j, dy in enumerate(dys)], counts, W, e)
         return {"dx": dx.to(dt), "dweight": torch.stack([x.t() @ dy for x, dy in zip(xs, dys)]).to(dt)}
+    xs = _segments(s["x"].float(), counts, W, e)
     wg, wu = s["gate"].float(), s["up"].float()
     gs = [x @ wg[j] for j, x in enumerate(xs)]
     us = [x @ wu[j] for j, x in enumerate(xs)]
@@ -357,7 +358,8 @@ def exact(case, seed):
         a = g * torch.sigmoid(g) if case["act"] == "silu" else torch.nn.functional.gelu(g, approximate="tanh")
         codes, scales = _exact_codes(a * u, case["qtype"], case["mode"])
         return {"codes": codes, "scales": scales}
-    # Each arrival row's expert; an expert's rows keep their order of arrival.
+    # Each arrival row's expert; an expert's rows keep their order of arrival.  (The grouped product's gradient has its
+    # rows in expert order already.)
     e, dev = case["e"], d["x"].device
     owner = torch.repeat_interleave(torch.arange(case["W"] * e, device=dev) % e, s["recvCounts"].long())
     x, at = d["x"], 0
@@ -366,7 +368,7 @@ def exact(case, seed):
     for j in range(e):
         rows = torch.nonzero(owner == j).flatten()
         n = rows.numel()
-        xj = x[rows].requires_grad_(True)
+        xj = (x[at:at + n] if op == "gmm_grad" else x[rows]).requires_grad_(True)
         if op == "gmm_grad":
             wj = [d["weight"][j].requires_grad_(True)]
             hj = xj @ wj[0]
