@@ -1,6 +1,6 @@
 """ctypes binding of liba2av_gmm.so: argument marshalling only.
 
-Same names as the C ABI in include/a2av_gmm.h.  Every step of the hot path
+Same names as the C ABI in include/*.h.  Every step of the hot path
 runs in the library's CUDA kernels; this module only checks tensors, sizes the
 outputs and workspace with torch, and passes raw device pointers and the
 current CUDA stream.  There is no CPU fallback: without the built library
@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,11 +31,15 @@ EXPORTS = ("a2av_gmm_workspace_size", "a2av_gmm_run", "a2av_gmm_read_device_stat
            "a2av_gmm_status_string", "a2av_gmm_launch_count", "a2av_gmm_run_static_scratch",
            "a2av_gmm_run_profiled", "a2av_gmm_run_arrivals",
            "a2av_amp_update_scale", "a2av_found_nonfinite", "a2av_quant_reduce",
-           "a2av_gmm_mx_workspace_size", "a2av_gmm_mx_run", "a2av_gmm_mx_run_profiled")
+           "a2av_gmm_mx_workspace_size", "a2av_gmm_mx_run", "a2av_gmm_mx_run_profiled",
+           "a2av_rms_norm", "a2av_rms_norm_backward", "a2av_rms_norm_backward_workspace_size", "a2av_glu_quant",
+           "a2av_gated_workspace_size", "a2av_gated_run", "a2av_gated_backward",
+           "a2av_gmm_backward_workspace_size", "a2av_gmm_backward")
 
 # a2av_qtype / a2av_qmode of include/a2av_quant_reduce.h.
 QTYPES = {"e4m3fn": 0, "e5m2": 1, "int8": 2}
 QMODES = {"mx": 0, "group128": 1}
+ACTS = {"silu": 0, "gelu_tanh": 1}  # a2av_act of include/a2av_ffn.h
 
 
 class A2avError(RuntimeError):
@@ -57,6 +62,25 @@ class MxDesc(ctypes.Structure):
                 ("A", ctypes.c_int64), ("H1", ctypes.c_int64), ("N1", ctypes.c_int64),
                 ("BS", ctypes.c_int64), ("H2", ctypes.c_int64), ("N2", ctypes.c_int64),
                 ("qtype", ctypes.c_int32), ("want_permute_out", ctypes.c_int32), ("tiles", ctypes.c_int32)]
+
+
+class RmsNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("qtype", ctypes.c_int32),
+                ("qmode", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class GluDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("N", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("qtype", ctypes.c_int32),
+                ("qmode", ctypes.c_int32)]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [("W", ctypes.c_int32), ("e", ctypes.c_int32),
+                ("A", ctypes.c_int64), ("H1", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("want_permute_out", ctypes.c_int32),
+                ("save", ctypes.c_int32)]
 
 
 _lib = None
@@ -115,6 +139,18 @@ def load_library(path: str):
     L.a2av_gmm_mx_run.restype = ctypes.c_int
     L.a2av_gmm_mx_run_profiled.argtypes = [ctypes.POINTER(MxDesc)] + [p] * 14 + [sz, p, p, p]
     L.a2av_gmm_mx_run_profiled.restype = ctypes.c_int
+    i64, psz = ctypes.c_int64, ctypes.POINTER(sz)
+    L.a2av_rms_norm.argtypes = [ctypes.POINTER(RmsNormDesc)] + [p] * 9
+    L.a2av_rms_norm_backward_workspace_size.argtypes = [i64, i64, i32, psz]
+    L.a2av_rms_norm_backward.argtypes = [i64, i64, i32] + [p] * 8 + [sz, p]
+    L.a2av_glu_quant.argtypes = [ctypes.POINTER(GluDesc)] + [p] * 6
+    L.a2av_gated_workspace_size.argtypes = [ctypes.POINTER(GatedDesc), psz]
+    L.a2av_gated_run.argtypes = [ctypes.POINTER(GatedDesc)] + [p] * 8 + [sz, p]
+    L.a2av_gated_backward.argtypes = [ctypes.POINTER(GatedDesc)] + [p] * 10 + [sz, p]
+    L.a2av_gmm_backward_workspace_size.argtypes = [ctypes.POINTER(Desc), psz]
+    L.a2av_gmm_backward.argtypes = [ctypes.POINTER(Desc)] + [p] * 7 + [sz, p]
+    for name in EXPORTS[-9:]:
+        getattr(L, name).restype = ctypes.c_int
     return L
 
 
@@ -391,3 +427,286 @@ class MxPlan:
         if st != A2AV_OK:
             raise A2avError(st, name)
         return gmmY, mmY, permuteOut_q, permuteOut_s
+
+
+# ---- the operators around the grouped product (include/a2av_ffn.h)
+
+
+def _call(name, *args):
+    st = getattr(load(), name)(*args)
+    if st != A2AV_OK:
+        raise A2avError(st, name)
+
+
+def _size(name, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _call(name, *args, ctypes.byref(n))
+    return n.value
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream, device):
+    """Handle of the stream to enqueue on: the given one, or the device's current one."""
+    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _rows_of(t, name, dtype=None):
+    """A 2-D CUDA tensor whose rows are contiguous; returns the elements from one row to the next."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _out(t, name, shape, dtype, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _dtype16(t, name):
+    if t.dtype not in DTYPES:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _named(table, key, what):
+    if key not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, got {key!r}")
+    return table[key]
+
+
+def _code_outputs(out, rows, cols, qtype, mode, device):
+    """(codes, scales) to write: those of an earlier result, or new ones; (None, None) without a qtype."""
+    if qtype is None:
+        return None, None
+    block = 32 if mode == "mx" else 128
+    return (_out(out.codes if out else None, "codes", (rows, cols), torch.uint8, device),
+            _out(out.scales if out else None, "scales", (rows, cols // block),
+                 torch.uint8 if mode == "mx" else torch.float32, device))
+
+
+class RmsNormOut(NamedTuple):
+    h: Optional[torch.Tensor]       # x + residual, element type (None without a residual)
+    y: Optional[torch.Tensor]       # normed rows, element type
+    codes: Optional[torch.Tensor]   # uint8 codes of the normed rows
+    scales: Optional[torch.Tensor]  # uint8 E8M0 per 32 (mx) or float32 per 128 (group128)
+    rstd: Optional[torch.Tensor]    # float32 [rows]
+
+
+def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want_y=None, want_rstd=False,
+                  out: Optional[RmsNormOut] = None, stream=None) -> RmsNormOut:
+    """RMS norm of x [rows, H] (+ residual), times gamma [H]: the normed rows as codes and scales (qtype "e4m3fn",
+    "e5m2" or "int8"; mode "mx" or "group128") and / or in the element type (want_y; by default without a qtype).
+    Rows of x and residual may be strided; residual may be one row expanded to all.  `out`: an earlier result of the
+    same call, whose tensors are written again."""
+    code = _dtype16(x, "x")
+    rows, H = x.shape if x.dim() == 2 else (0, 0)
+    xs = _rows_of(x, "x")
+    _check(gamma, "gamma", x.dtype, 1)
+    if gamma.shape[0] != H:
+        raise ValueError(f"gamma must be [{H}]")
+    rs = 0
+    if residual is not None:
+        rs = _rows_of(residual, "residual", x.dtype)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have the shape of x")
+    if want_y is None:
+        want_y = qtype is None
+    q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
+    m = _named(QMODES, mode, "mode")
+    dev = x.device
+    h = None if residual is None else _out(out.h if out else None, "h", (rows, H), x.dtype, dev)
+    y = _out(out.y if out else None, "y", (rows, H), x.dtype, dev) if want_y else None
+    rstd = _out(out.rstd if out else None, "rstd", (rows,), torch.float32, dev) if want_rstd else None
+    codes, scales = _code_outputs(out, rows, H, qtype, mode, dev)
+    desc = RmsNormDesc(rows, H, xs, rs, code, q, m, eps)
+    _call("a2av_rms_norm", ctypes.byref(desc), _at(x), _at(residual), _at(gamma), _at(h), _at(y), _at(codes),
+          _at(scales), _at(rstd), _on(stream, dev))
+    return RmsNormOut(h, y, codes, scales, rstd)
+
+
+def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, workspace=None, stream=None):
+    """(dx [rows, H], dgamma float32 [H]) from the gradient dy of the normed rows and, optionally, the gradient dh
+    that reaches h directly.  dx is the gradient of x and of the residual."""
+    code = _dtype16(dy, "dy")
+    _check(dy, "dy", None, 2)
+    rows, H = dy.shape
+    for t, name in ((h, "h"), (dh, "dh")):
+        if t is not None:
+            _check(t, name, dy.dtype, 2)
+            if t.shape != dy.shape:
+                raise ValueError(f"{name} must be [{rows}, {H}]")
+    _check(gamma, "gamma", dy.dtype, 1)
+    _check(rstd, "rstd", torch.float32, 1)
+    if gamma.shape[0] != H or rstd.shape[0] != rows:
+        raise ValueError(f"gamma must be [{H}] and rstd [{rows}]")
+    dx = _out(dx, "dx", (rows, H), dy.dtype, dy.device)
+    dgamma = _out(dgamma, "dgamma", (H,), torch.float32, dy.device)
+    if workspace is None:
+        workspace = torch.empty(_size("a2av_rms_norm_backward_workspace_size", rows, H, code), dtype=torch.uint8,
+                                device=dy.device)
+    _call("a2av_rms_norm_backward", rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd), _at(dx),
+          _at(dgamma), _at(workspace), workspace.numel(), _on(stream, dy.device))
+    return dx, dgamma
+
+
+class GluQuantOut(NamedTuple):
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+
+
+def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, out: Optional[GluQuantOut] = None,
+                   stream=None) -> GluQuantOut:
+    """act(gate) * up of gate_up [rows, 2N] (gate columns, then up columns) as codes and scales and / or in the
+    element type (want_h; by default without a qtype)."""
+    code = _dtype16(gate_up, "gate_up")
+    stride = _rows_of(gate_up, "gate_up")
+    rows, N = gate_up.shape[0], gate_up.shape[1] // 2
+    if gate_up.shape[1] != 2 * N:
+        raise ValueError("gate_up must have an even number of columns")
+    if want_h is None:
+        want_h = qtype is None
+    q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
+    desc = GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode"))
+    dev = gate_up.device
+    codes, scales = _code_outputs(out, rows, N, qtype, mode, dev)
+    h = _out(out.h if out else None, "h", (rows, N), gate_up.dtype, dev) if want_h else None
+    gate = _at(gate_up)
+    _call("a2av_glu_quant", ctypes.byref(desc), gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
+          _on(stream, dev))
+    return GluQuantOut(codes, scales, h)
+
+
+def _rank_rows(t, name, rows, cols, dtype):
+    if rows:
+        _check(t, name, dtype, 2)
+        if tuple(t.shape) != (rows, cols):
+            raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+
+
+def _counts(t, n):
+    _check(t, "recvCounts", torch.int32, 1)
+    if t.numel() != n:
+        raise ValueError(f"recvCounts must have {n} entries")
+
+
+def _weights(t, name, shape, dtype):
+    _check(t, name, dtype, 3)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+class GatedOut(NamedTuple):
+    h: torch.Tensor                     # [A, N], expert-major
+    saved: Optional[torch.Tensor]       # float32 [2, A, N]: gate and up before the activation
+    permuteOut: Optional[torch.Tensor]  # expert-major rows (W = 1: ataOut itself)
+
+
+class GatedGrads(NamedTuple):
+    dAtaOut: Optional[torch.Tensor]  # [A, H1], rank-major
+    dGate: Optional[torch.Tensor]    # [e, H1, N]
+    dUp: Optional[torch.Tensor]      # [e, H1, N]
+
+
+class GatedPlan:
+    """Descriptor + workspace of the gated block h = act(X Wg) * (X Wu) over ragged experts, and its backward pass,
+    for one shape.  save: keep what the backward pass needs (with several sources that includes permuteOut)."""
+
+    def __init__(self, W, e, A, H1, N, dtype=torch.bfloat16, act="silu", save=False, want_permute_out=None,
+                 device=None):
+        if want_permute_out is None:
+            want_permute_out = save and W > 1
+        if dtype not in DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+        self.desc = GatedDesc(W, e, A, H1, N, DTYPES[dtype], _named(ACTS, act, "act"), int(bool(want_permute_out)),
+                              int(bool(save)))
+        self.dtype = dtype
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.workspace = torch.empty(_size("a2av_gated_workspace_size", ctypes.byref(self.desc)), dtype=torch.uint8,
+                                     device=self.device)
+
+    def _check_weights(self, gateWeight, upWeight):
+        d = self.desc
+        _weights(gateWeight, "gateWeight", (d.e, d.H1, d.N), self.dtype)
+        _weights(upWeight, "upWeight", (d.e, d.H1, d.N), self.dtype)
+
+    def run(self, ataOut, recvCounts, gateWeight, upWeight, h=None, saved=None, permuteOut=None,
+            stream=None) -> GatedOut:
+        d = self.desc
+        _rank_rows(ataOut, "ataOut", d.A, d.H1, self.dtype)
+        _counts(recvCounts, d.W * d.e)
+        self._check_weights(gateWeight, upWeight)
+        h = _out(h, "h", (d.A, d.N), self.dtype, self.device)
+        if d.save:
+            saved = _out(saved, "saved", (2, d.A, d.N), torch.float32, self.device)
+        if d.want_permute_out:
+            permuteOut = _out(permuteOut, "permuteOut", (d.A, d.H1), self.dtype, self.device)
+        _call("a2av_gated_run", ctypes.byref(d), _at(ataOut), _at(recvCounts), _at(gateWeight), _at(upWeight),
+              _at(permuteOut) if d.want_permute_out else None, _at(h), _at(saved) if d.save else None,
+              self.workspace.data_ptr(), self.workspace.numel(), _on(stream, self.device))
+        return GatedOut(h, saved if d.save else None,
+                        permuteOut if d.want_permute_out else (ataOut if d.W == 1 else None))
+
+    def backward(self, dh, permuteOut, recvCounts, gateWeight, upWeight, saved, want_rows=True, want_weights=True,
+                 dAtaOut=None, dGate=None, dUp=None, stream=None) -> GatedGrads:
+        d = self.desc
+        _rank_rows(dh, "dh", d.A, d.N, self.dtype)
+        _rank_rows(permuteOut, "permuteOut", d.A, d.H1, self.dtype)
+        _counts(recvCounts, d.W * d.e)
+        self._check_weights(gateWeight, upWeight)
+        _check(saved, "saved", torch.float32, 3)
+        if tuple(saved.shape) != (2, d.A, d.N):
+            raise ValueError(f"saved must be {[2, d.A, d.N]}")
+        if want_rows:
+            dAtaOut = _out(dAtaOut, "dAtaOut", (d.A, d.H1), self.dtype, self.device)
+        if want_weights:
+            dGate = _out(dGate, "dGate", (d.e, d.H1, d.N), self.dtype, self.device)
+            dUp = _out(dUp, "dUp", (d.e, d.H1, d.N), self.dtype, self.device)
+        _call("a2av_gated_backward", ctypes.byref(d), _at(dh), _at(permuteOut), _at(recvCounts), _at(gateWeight),
+              _at(upWeight), _at(saved), _at(dAtaOut) if want_rows else None, _at(dGate) if want_weights else None,
+              _at(dUp) if want_weights else None, self.workspace.data_ptr(), self.workspace.numel(),
+              _on(stream, self.device))
+        return GatedGrads(dAtaOut if want_rows else None, dGate if want_weights else None,
+                          dUp if want_weights else None)
+
+
+class GmmBackwardPlan:
+    """Descriptor + workspace of the grouped product's gradients for one shape (a2av_gmm_backward)."""
+
+    def __init__(self, W, e, A, H1, N1, dtype=torch.bfloat16, device=None):
+        self.desc = make_desc(W, e, A, H1, N1, dtype=dtype)
+        self.dtype = dtype
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.workspace = torch.empty(_size("a2av_gmm_backward_workspace_size", ctypes.byref(self.desc)),
+                                     dtype=torch.uint8, device=self.device)
+
+    def run(self, dY, permuteOut, recvCounts, gmmWeight, want_rows=True, want_weights=True, dAtaOut=None,
+            dWeight=None, stream=None):
+        """(dAtaOut [A, H1] rank-major, dWeight [e, H1, N1]); either may be left out (None)."""
+        d = self.desc
+        _rank_rows(dY, "dY", d.A, d.N1, self.dtype)
+        _rank_rows(permuteOut, "permuteOut", d.A, d.H1, self.dtype)
+        _counts(recvCounts, d.W * d.e)
+        _weights(gmmWeight, "gmmWeight", (d.e, d.H1, d.N1), self.dtype)
+        if want_rows:
+            dAtaOut = _out(dAtaOut, "dAtaOut", (d.A, d.H1), self.dtype, self.device)
+        if want_weights:
+            dWeight = _out(dWeight, "dWeight", (d.e, d.H1, d.N1), self.dtype, self.device)
+        _call("a2av_gmm_backward", ctypes.byref(d), _at(dY), _at(permuteOut), _at(recvCounts), _at(gmmWeight),
+              _at(dAtaOut) if want_rows else None, _at(dWeight) if want_weights else None,
+              self.workspace.data_ptr(), self.workspace.numel(), _on(stream, self.device))
+        return dAtaOut if want_rows else None, dWeight if want_weights else None

@@ -1,0 +1,557 @@
+// Persistent ragged GEMMs of an expert layer's gated block and gradients, on
+// tcgen05 tensor cores (sm_103a), for the experts j of a rank:
+//
+//   gated            h = act(X Wg_j) * (X Wu_j)
+//   rows' gradient   dX = D_0 W_0j^T (+ D_1 W_1j^T)
+//   weights' gradient  dW_j = X_j^T D_j
+//
+// One kernel, three ways of walking the operands.  A cluster of two CTAs
+// computes a tile of 256 rows x 256 accumulator columns with one cta_group::2
+// MMA: each CTA stages 128 of the rows of A and half of the columns of B.  The
+// even CTA issues the MMAs; each CTA holds its 128 rows of the accumulator.
+//
+// The gated tile is 128 output columns: the even CTA stages them from Wg, the
+// odd one from Wu, so the accumulator's first half is G and its second U for
+// the same rows and columns, and the epilogue forms act(G) * U lane by lane
+// before anything is written.  The same split gives both weights' gradients
+// of a gated block from one read of X.
+//
+// Every operand tile has one shape in shared memory: 128 rows of 128 elements,
+// as two 64-element atoms of 128-byte swizzled rows (32 KB), loaded by one
+// TMA box (two where the width is no multiple of 64; columns and rows past
+// the tensor's end arrive as zeros).  What differs is how the tensor core
+// reads it: with the contraction along the elements (K-major) or along the
+// rows (MN-major), a bit in the instruction descriptor and two strides.
+//
+//   form              A tile (rows x elements)   B tile (rows x elements)
+//   gated             X: rows x K    K-major     W: K x columns        MN-major
+//   rows' gradient    D: rows x K    K-major     W: out columns x K    K-major
+//   weights' gradient X: K x M       MN-major    D: K x columns        MN-major
+//
+// In the weights' gradient K runs over an expert's rows, whose last block is
+// ragged, and the rows behind it belong to the next expert.  That block goes
+// first in each tile, is multiplied only up to its last 16 rows, and the rows
+// of those that are not the expert's are overwritten with zeros in both
+// operands by a warp of each CTA before the MMA may read them: multiplying by
+// zero on one side alone would let another expert's infinities through.
+//
+// Per CTA: warp 0 loads, warp 1 clears ragged rows (weights' gradient), warp 4
+// allocates TMEM and (even CTA) issues, warps 5-8 are the epilogue.  Two
+// accumulators let a tile's epilogue overlap the next tile's main loop.  Every
+// wait is bounded: on expiry the kernel records kStatusTimeout and winds down.
+#include "activation.cuh"
+#include "ffn.h"
+#include "pair.cuh"
+
+namespace a2av {
+
+namespace {
+
+constexpr int BM = 128;        // rows a CTA stages
+constexpr int TILE_M = 256;    // rows of a pair's tile
+constexpr int BK = 128;        // contraction elements a stage
+constexpr int kStages = 3;
+constexpr uint32_t kAtomBytes = 128 * 128;     // 128 rows x 64 elements
+constexpr uint32_t kTileBytes = 2 * kAtomBytes;
+constexpr uint32_t kStageBytes = 2 * kTileBytes;  // A and B
+constexpr int kClearWarp = 1;
+constexpr int kMmaWarp = 4;
+constexpr int kThreads = 9 * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccCols = 256;
+constexpr uint32_t kEpiBufBytes = 32 * 64;  // 32 rows x 32 columns of 16 bits
+constexpr uint32_t kEpiWarpBytes = 2 * kEpiBufBytes;
+
+struct GroupInfo {
+    int32_t row0;        // first expert-major row
+    int32_t rows;
+    int32_t tile_start;  // first linear tile
+};
+
+struct Control {
+    uint64_t full[kStages];    // even CTA: a stage has landed in both CTAs
+    uint64_t empty[kStages];   // the MMAs that read a stage have completed
+    uint64_t ragged[kStages];  // this CTA's part of a ragged block has landed
+    uint64_t cleared[kStages]; // even CTA: both CTAs have cleared a ragged block's rows
+    uint64_t tfull[2];         // accumulator ready for the epilogue
+    uint64_t tempty[2];        // even CTA: both epilogues have drained it
+    uint32_t tmem_base;
+    int32_t abort;
+    int32_t total_tiles;
+    GroupInfo g[kMaxExperts + 1];
+    SegmentTable seg;
+};
+
+constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
+constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kControlBytes + 4 * kEpiWarpBytes;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+struct Tile {
+    int g, m, n;
+};
+
+// Tiles of a group: row tiles in order, column tiles innermost.
+__device__ __forceinline__ Tile tile_at(const Control &c, int t, int tn) {
+    int g = 0;
+    while (t >= c.g[g + 1].tile_start) ++g;
+    const int local = t - c.g[g].tile_start;
+    return {g, local / tn, local % tn};
+}
+
+__device__ __forceinline__ void st_global_f32x8(float *ptr, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Instruction descriptor for kind::f16 with an fp32 accumulator and the
+// operands' majors, M = N = 256.
+template <bool BF16, int FORM>
+__device__ __forceinline__ constexpr uint32_t instr_desc() {
+    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) |
+           ((FORM == kFormGradWeight ? 1u : 0u) << 15) | ((FORM == kFormGradRows ? 0u : 1u) << 16) |
+           ((256u >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Contraction block kb of a tile: its first element and how many of its 128
+// elements count.  The weights' gradient takes the ragged last block first.
+struct Block {
+    int first, len;
+};
+template <int FORM>
+__device__ __forceinline__ Block block_of(int K, int kb) {
+    if constexpr (FORM == kFormGradWeight) {
+        const int rem = K % BK, whole = K / BK;
+        if (rem == 0) return {kb * BK, BK};
+        return kb == 0 ? Block{whole * BK, rem} : Block{(kb - 1) * BK, BK};
+    }
+    return {kb * BK, min(BK, K - kb * BK)};
+}
+
+template <bool BF16, int FORM, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertGemmLaunch p) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+    Control &C = *reinterpret_cast<Control *>(base_ptr + kStages * kStageBytes);
+    const uint32_t epi0 = base + kStages * kStageBytes + kControlBytes;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = pair::cluster_rank();
+    const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
+    // Columns of the output one tile covers.
+    const int tile_n = FORM == kFormGradRows || p.half_step ? 256 : 128;
+    const int tn = (p.N + tile_n - 1) / tile_n;
+
+    // ---- prologue: groups and tiles (warp 0), barriers (warp 1), TMEM (MMA warp)
+    if (warp == 0) {
+        const bool good = build_segment_table(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
+        int row0 = 0, rows = 0, tiles = 0;
+        if (lane < p.e) {
+            row0 = C.seg.dst[lane * p.W];
+            rows = C.seg.dst[(lane + 1) * p.W] - row0;
+            const int tm = FORM == kFormGradWeight ? (p.M + TILE_M - 1) / TILE_M : (rows + TILE_M - 1) / TILE_M;
+            tiles = good ? tm * tn : 0;
+        }
+        int inc = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane < p.e) C.g[lane] = GroupInfo{row0, rows, inc - tiles};
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
+        if (lane == 0) {
+            C.g[p.e] = GroupInfo{0, 0, total};
+            C.total_tiles = total;
+            C.abort = 0;
+            if (blockIdx.x == 0) {
+                if (p.write_status) *p.status = good ? 0 : kStatusBadCounts;
+                else if (!good) atomicOr(p.status, kStatusBadCounts);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(smem_u32(&C.full[s]), 1);
+                mbar_init(smem_u32(&C.empty[s]), 1);
+                mbar_init(smem_u32(&C.ragged[s]), 1);
+                mbar_init(smem_u32(&C.cleared[s]), 2);
+            }
+            for (int a = 0; a < 2; ++a) {
+                mbar_init(smem_u32(&C.tfull[a]), 1);
+                mbar_init(smem_u32(&C.tempty[a]), 8);
+            }
+            fence_barrier_init();
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            prefetch_tensormap(&p.tmA[0]);
+            prefetch_tensormap(&p.tmB[FORM == kFormGradRows ? 0 : rank]);
+            prefetch_tensormap(&p.tmY[0]);
+        }
+    } else if (warp == kMmaWarp) {
+        pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
+    }
+    tc_fence_before_sync();
+    pair::sync_all();
+    tc_fence_after_sync();
+
+    const int total = C.total_tiles;
+    const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
+    const uint32_t ragged0 = smem_u32(&C.ragged[0]), cleared0 = smem_u32(&C.cleared[0]);
+    const auto contraction = [&](const Tile &w) { return FORM == kFormGradWeight ? C.g[w.g].rows : p.K; };
+    const auto is_ragged = [&](const Block &b) { return FORM == kFormGradWeight && (b.len & 15) != 0; };
+
+    if (warp == 0) {
+        // =========================================================== producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            bool ready = !p.after;  // what the kernel before this one writes is visible
+            for (int t = unit; t < total && ok; t += nunits) {
+                const Tile w = tile_at(C, t, tn);
+                const int K = contraction(w);
+                const int kblocks = (K + BK - 1) / BK;
+                const int row = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM;  // this CTA's first row
+                // Gated, rows taken in place: a half whose rows of this group
+                // lie in one (source, expert) run is contiguous in ataOut; the
+                // permute kernel staged only the others.
+                const CUtensorMap *ta = &p.tmA[0];
+                int arow = row;
+                if (FORM == kFormGated && p.direct_halves) {
+                    const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
+                    if (row < g_end && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
+                        ta = &p.tmDirect;
+                        arow = source_row(C.seg, p.W, p.e, row);
+                    }
+                }
+                if (!ready && ta != &p.tmDirect) {
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    ready = true;
+                }
+                const int steps = FORM == kFormGradRows ? p.phases * kblocks : kblocks;
+                for (int i = 0; i < steps; ++i, ++it) {
+                    const int s = it % kStages;
+                    const int phase = FORM == kFormGradRows && i >= kblocks ? 1 : 0;
+                    const Block b = block_of<FORM>(K, i - phase * kblocks);
+                    if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.status,
+                                          p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a_st = base + s * kStageBytes, b_st = a_st + kTileBytes;
+                    // Where the loads complete: the even CTA's barrier for
+                    // both CTAs' parts; a ragged block on each CTA's own.
+                    uint32_t bar;
+                    if (is_ragged(b)) {
+                        bar = ragged0 + 8 * s;
+                        mbar_arrive_expect_tx(bar, kStageBytes);
+                    } else {
+                        if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStageBytes);
+                        bar = pair::map_to_rank(full0 + 8 * s, 0);
+                    }
+                    int ax, ay, bx, by, bz;
+                    const CUtensorMap *a_map, *b_map;
+                    if constexpr (FORM == kFormGated) {
+                        a_map = ta, ax = b.first, ay = arow;
+                        b_map = &p.tmB[rank], bx = w.n * 128, by = b.first, bz = w.g;
+                    } else if constexpr (FORM == kFormGradRows) {
+                        a_map = &p.tmA[phase], ax = b.first, ay = row;
+                        b_map = &p.tmB[phase], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128, bz = w.g;
+                    } else {
+                        const int k_row = C.g[w.g].row0 + b.first;
+                        a_map = &p.tmA[0], ax = w.m * TILE_M + static_cast<int>(rank) * BM, ay = k_row;
+                        b_map = &p.tmB[rank], bx = w.n * tile_n + static_cast<int>(rank) * p.half_step, by = k_row, bz = 0;
+                    }
+                    if (p.one_a) {
+                        pair::load_4d(a_st, a_map, bar, 0, ay, ax / 64, 0);
+                    } else {
+                        pair::load_3d(a_st, a_map, bar, ax, ay, 0);
+                        pair::load_3d(a_st + kAtomBytes, a_map, bar, ax + 64, ay, 0);
+                    }
+                    if (p.one_b) {
+                        pair::load_4d(b_st, b_map, bar, 0, by, bx / 64, bz);
+                    } else {
+                        pair::load_3d(b_st, b_map, bar, bx, by, bz);
+                        pair::load_3d(b_st + kAtomBytes, b_map, bar, bx + 64, by, bz);
+                    }
+                }
+            }
+            // Tail: every stage filled has been released (no copy in flight).
+            for (int i = 0; i < kStages && ok; ++i, ++it)
+                ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % kStages), ((it / kStages) & 1) ^ 1, p.status,
+                                      p.wait_limit_ns);
+        }
+    } else if (warp == kClearWarp && FORM == kFormGradWeight) {
+        // ============================================= ragged rows of the block
+        uint32_t it = 0;
+        uint32_t used = 0;  // parity, by stage, of the ragged blocks seen
+        for (int t = unit; t < total; t += nunits) {
+            const Tile w = tile_at(C, t, tn);
+            const int K = contraction(w);
+            const int kblocks = (K + BK - 1) / BK;
+            const Block b = kblocks ? block_of<FORM>(K, 0) : Block{0, 0};
+            if (is_ragged(b)) {
+                const int s = it % kStages;
+                if (!pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns)) break;
+                used ^= 1u << s;
+                __syncwarp();
+                // Rows len .. the next multiple of 16, 128 bytes in each of
+                // the four atoms (the swizzle stays within a row).
+                const int rows = 16 - (b.len & 15);
+                const uint32_t st = base + s * kStageBytes + b.len * 128;
+                for (int i = lane; i < rows * 32; i += 32)  // atom i / (8 rows), 16-byte piece of its rows
+                    st_shared_v4(st + (i / (rows * 8)) * kAtomBytes + (i % (rows * 8)) * 16, make_uint4(0, 0, 0, 0));
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    pair::arrive_cluster(pair::map_to_rank(cleared0 + 8 * s, 0));
+                    if (rank == 0) mbar_arrive(full0 + 8 * s);  // the stage's phase, in place of the loads' bytes
+                }
+            }
+            it += kblocks;
+        }
+    } else if (warp == kMmaWarp) {
+        // =========================================================== MMA issuer
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = instr_desc<BF16, FORM>();
+            // K-major: 8-row groups 1024 B apart; a K step of 16 elements is
+            //    32 B along the row, the second atom 16 KB on.
+            // MN-major: atoms of 64 columns 16 KB apart (leading offset), 8-row
+            //    K groups 1024 B apart; a K step of 16 rows is 2 KB.
+            constexpr bool kAkm = FORM != kFormGradWeight, kBkm = FORM == kFormGradRows;
+            const uint64_t a_desc0 = smem_desc(base, kAkm ? 16 : kAtomBytes, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(base + kTileBytes, kBkm ? 16 : kAtomBytes, 1024, kSwizzle128B);
+            uint32_t it = 0, tl = 0, used = 0;
+            bool ok = true;
+            for (int t = unit; t < total && ok; t += nunits, ++tl) {
+                const Tile w = tile_at(C, t, tn);
+                const int K = contraction(w);
+                const int kblocks = (K + BK - 1) / BK;
+                const int steps = FORM == kFormGradRows ? p.phases * kblocks : kblocks;
+                const int acc = tl & 1;
+                if (!pair::wait_phase(&C.abort, smem_u32(&C.tempty[acc]), ((tl >> 1) & 1) ^ 1, p.status,
+                                      p.wait_limit_ns))
+                    break;
+                tc_fence_after_sync();
+                const uint32_t d_tmem = C.tmem_base + acc * kAccCols;
+                for (int i = 0; i < steps; ++i, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t par = (it / kStages) & 1;
+                    if (!mbar_try_wait(full0 + 8 * s, par) &&
+                        !pair::wait_phase(&C.abort, full0 + 8 * s, par, p.status, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const Block b = block_of<FORM>(K, FORM == kFormGradRows && i >= kblocks ? i - kblocks : i);
+                    if (is_ragged(b)) {
+                        if (!pair::wait_phase(&C.abort, cleared0 + 8 * s, (used >> s) & 1, p.status,
+                                              p.wait_limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        used ^= 1u << s;
+                        tc_fence_after_sync();
+                    }
+                    const uint64_t ad0 = a_desc0 + ((s * kStageBytes) >> 4);
+                    const uint64_t bd0 = b_desc0 + ((s * kStageBytes) >> 4);
+                    const int ksteps = (b.len + 15) / 16;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        if (kk < ksteps) {
+                            const uint32_t km = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4, mn = 128 * kk;
+                            pair::mma(d_tmem, ad0 + (kAkm ? km : mn), bd0 + (kBkm ? km : mn), idesc, (i | kk) != 0);
+                        }
+                    }
+                    pair::commit(empty0 + 8 * s);
+                }
+                if (ok) pair::commit(smem_u32(&C.tfull[acc]));
+            }
+        }
+    } else if (warp > kMmaWarp) {
+        // =========================================================== epilogue
+        const int q = warp & 3;  // TMEM lane quarter this warp may read
+        const uint32_t stage = epi0 + static_cast<uint32_t>(warp - kMmaWarp - 1) * kEpiWarpBytes;
+        const uint32_t tempty0 = pair::map_to_rank(smem_u32(&C.tempty[0]), 0);
+        uint32_t tl = 0, nblk = 0;
+        for (int t = unit; t < total; t += nunits, ++tl) {
+            const Tile w = tile_at(C, t, tn);
+            const int acc = tl & 1;
+            if (!pair::wait_phase(&C.abort, smem_u32(&C.tfull[acc]), (tl >> 1) & 1, p.status, p.wait_limit_ns)) break;
+            __syncwarp();
+            tc_fence_after_sync();
+            const GroupInfo gi = C.g[w.g];
+            const int row0w = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;  // this warp's first row
+            const int rows = FORM == kFormGradWeight ? p.M : gi.rows;
+            const bool valid = row0w + lane < rows;
+            const bool all_rows = row0w + 32 <= rows;
+            // Output row of this lane's row, and whether the warp's 32 rows are
+            // consecutive there.
+            int64_t orow = 0;
+            bool together = all_rows;
+            if constexpr (FORM == kFormGradWeight) {
+                orow = static_cast<int64_t>(w.g) * p.M + row0w + lane;
+            } else if constexpr (FORM == kFormGated) {
+                orow = gi.row0 + row0w + lane;
+            } else {  // the gradient's rows go back to their order of arrival
+                int seg = 0;
+                if (valid) {
+                    seg = segment_of(C.seg, p.W, p.e, gi.row0 + row0w + lane);
+                    orow = source_row_in(C.seg, p.W, p.e, seg, gi.row0 + row0w + lane);
+                }
+                together = all_rows && __shfl_sync(0xffffffffu, seg, 0) == __shfl_sync(0xffffffffu, seg, 31);
+            }
+            const bool zero = FORM == kFormGradWeight && gi.rows == 0;  // nothing was accumulated
+            const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kAccCols;
+            constexpr int kChunks = FORM == kFormGated ? 4 : 8;
+            for (int c = 0; c < kChunks; ++c) {
+                const int half = FORM == kFormGated ? 0 : c >> 2;
+                const int col = (FORM == kFormGradRows ? w.n * 256 + c * 32
+                                                       : w.n * tile_n + half * p.half_step + (c & 3) * 32);
+                if (col >= p.N) continue;  // uniform
+                const uint32_t buf = stage + (nblk++ & 1u) * kEpiBufBytes;
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t_base + c * 32, r);
+                if constexpr (FORM == kFormGated) {
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(t_base + 128 + c * 32, u);
+                    tmem_ld_wait();
+                    if (p.saved[0] && valid) {
+                        float *g_out = p.saved[0] + orow * p.N + col, *u_out = p.saved[1] + orow * p.N + col;
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            if (col + v * 8 < p.N) {
+                                st_global_f32x8(g_out + v * 8, r + v * 8);
+                                st_global_f32x8(u_out + v * 8, u + v * 8);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        r[i] = __float_as_uint(act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]));
+                } else {
+                    tmem_ld_wait();
+                    if (zero) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = 0;
+                    }
+                }
+                // The store that read this buffer two blocks ago is done when at
+                // most one bulk group (every block commits one) is pending.
+                if (lane == 0) bulk_wait_read_1();
+                __syncwarp();
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    uint4 pk;
+                    pk.x = pack2f<BF16>(__uint_as_float(r[v * 8 + 0]), __uint_as_float(r[v * 8 + 1]));
+                    pk.y = pack2f<BF16>(__uint_as_float(r[v * 8 + 2]), __uint_as_float(r[v * 8 + 3]));
+                    pk.z = pack2f<BF16>(__uint_as_float(r[v * 8 + 4]), __uint_as_float(r[v * 8 + 5]));
+                    pk.w = pack2f<BF16>(__uint_as_float(r[v * 8 + 6]), __uint_as_float(r[v * 8 + 7]));
+                    st_shared_v4(buf + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), pk);
+                }
+                if (together) {  // one TMA store; columns past N are clipped
+                    const int y = static_cast<int>(__shfl_sync(0xffffffffu, orow, 0));
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&p.tmY[half], buf, col, y);
+                        bulk_commit_group();
+                    }
+                } else {
+                    if (lane == 0) bulk_commit_group();  // an empty group keeps the count
+                    __syncwarp();
+                    const int v = lane & 3;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int rr = 8 * k + (lane >> 2);
+                        const int64_t dst = __shfl_sync(0xffffffffu, orow, rr);
+                        const uint4 val = ld_shared_v4(buf + rr * 64 + ((v ^ ((rr >> 1) & 3)) << 4));
+                        if (row0w + rr < rows && col + v * 8 < p.N)
+                            st_stream_v4(static_cast<uint16_t *>(p.out[half]) + dst * p.N + col + v * 8, val);
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) pair::arrive_cluster(tempty0 + 8 * acc);
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+
+    __syncwarp();  // the single-lane roles are done
+    tc_fence_before_sync();
+    pair::sync_all();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        pair::tmem_free_pair(C.tmem_base, kTmemCols);
+    }
+}
+
+template <bool BF16, int FORM, int ACT>
+cudaError_t launch_form(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    auto kern = expert_gemm_kernel<BF16, FORM, ACT>;
+    cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.after ? 2 : 1;
+    err = cudaLaunchKernelEx(&cfg, kern, p);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_type(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    switch (p.form) {
+        case kFormGated:
+            return p.act == A2AV_ACT_SILU ? launch_form<BF16, kFormGated, A2AV_ACT_SILU>(p, stream)
+                                          : launch_form<BF16, kFormGated, A2AV_ACT_GELU_TANH>(p, stream);
+        case kFormGradRows: return launch_form<BF16, kFormGradRows, A2AV_ACT_SILU>(p, stream);
+        case kFormGradWeight: return launch_form<BF16, kFormGradWeight, A2AV_ACT_SILU>(p, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    return p.bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
+}
+
+// Clusters resident at once; every form has the same shared memory and at most one CTA per SM.
+int expert_gemm_max_clusters() {
+    auto kern = expert_gemm_kernel<true, kFormGated, A2AV_ACT_SILU>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
+        cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 1024, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+    return n;
+}
+
+}  // namespace a2av

@@ -1,0 +1,436 @@
+// C ABI of the expert-layer operators (declared in include/a2av_ffn.h):
+// argument checks, tensor maps and launches.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "a2av_ffn.h"
+#include "ffn.h"
+#include "kernels.h"
+#include "plan.cuh"
+
+namespace {
+
+using a2av::ExpertGemmLaunch;
+
+constexpr size_t kStatusBytes = 256;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool mult8(int64_t v) { return v % 8 == 0; }
+bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+
+int sm_count() {
+    static int cache[kMaxDevices] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+int gemm_clusters() {
+    static int cache[kMaxDevices] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    if (cache[dev] == 0) cache[dev] = a2av::expert_gemm_max_clusters();
+    return cache[dev];
+}
+
+// The 8-bit output asked for: its type and mode within the formats, and rows
+// that are whole scale blocks.
+a2av_status check_quant(int32_t qtype, int32_t qmode, int64_t cols) {
+    if (qtype == A2AV_Q_NONE) return A2AV_OK;
+    if (qtype < A2AV_Q_E4M3FN || qtype > A2AV_Q_INT8) return A2AV_ERR_INVALID;
+    if (qmode != A2AV_QMODE_MX && qmode != A2AV_QMODE_GROUP128) return A2AV_ERR_INVALID;
+    if (qmode == A2AV_QMODE_MX && qtype == A2AV_Q_INT8) return A2AV_ERR_INVALID;
+    if (cols % (qmode == A2AV_QMODE_MX ? 32 : 128) != 0) return A2AV_ERR_INVALID;
+    return A2AV_OK;
+}
+
+a2av_status check_quant_out(int32_t qtype, int32_t qmode, const void *codes, const void *scales, bool rows) {
+    if (qtype == A2AV_Q_NONE) return codes || scales ? A2AV_ERR_INVALID : A2AV_OK;
+    if (rows && (!codes || !scales)) return A2AV_ERR_NULLPTR;
+    if (!aligned(codes, 8) || (qmode == A2AV_QMODE_GROUP128 && !aligned(scales, 4))) return A2AV_ERR_UNSUPPORTED;
+    return A2AV_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Operand tiles of [groups][rows][cols] row-major: 128 rows x 128 elements as
+// two 64-element atoms, 128-byte swizzled.  `one`: the 4-D view
+// [groups][cols / 64][rows][64], both atoms in one box (cols a multiple of
+// 64); otherwise the 3-D view, one atom a box.
+bool operand_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t cols, bool bf16, bool one) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const auto type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t pitch = static_cast<cuuint64_t>(cols) * 2;
+    const cuuint64_t plane = groups > 1 ? pitch * rows : pitch;  // not used with one group
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r;
+    if (one) {
+        const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
+                                    static_cast<cuuint64_t>(groups)};
+        const cuuint64_t strides[3] = {pitch, 128, plane};
+        const cuuint32_t box[4] = {64, 128, 2, 1};
+        r = fn(m, type, 4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                                    static_cast<cuuint64_t>(groups)};
+        const cuuint64_t strides[2] = {pitch, plane};
+        const cuuint32_t box[3] = {64, 128, 1};
+        r = fn(m, type, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return r == CUDA_SUCCESS;
+}
+
+// [rows][cols] row-major output, stored in boxes of 32 x 32, 64-byte swizzled.
+bool output_map(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, bool bf16) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Persistent grid: the clusters resident at once, never more than there can be tiles.
+int gemm_grid(int64_t max_tiles) {
+    int units = gemm_clusters();
+    if (units <= 0) units = std::max(1, sm_count() / 2);
+    return static_cast<int>(2 * std::max<int64_t>(1, std::min<int64_t>(units, max_tiles)));
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, const int32_t *recvCounts, int32_t *status) {
+    ExpertGemmLaunch g;
+    std::memset(&g, 0, sizeof g);
+    g.recvCounts = recvCounts;
+    g.W = W;
+    g.e = e;
+    g.A = static_cast<int32_t>(A);
+    g.bf16 = dtype == A2AV_BF16;
+    g.status = status;
+    g.write_status = 1;
+    g.wait_limit_ns = kWaitLimitNs;
+    return g;
+}
+
+// Gradients of one or two products with the same rows: dX = sum_p D_p W_p^T,
+// dW_p = X^T D_p.  `status` is stored by the first kernel.
+a2av_status run_gradients(ExpertGemmLaunch g, int phases, int64_t H1, int64_t N, const void *const D[2],
+                          const void *X, const void *const Wt[2], void *dX, void *const dW[2], cudaStream_t stream) {
+    const bool bf16 = g.bf16 != 0;
+    const bool one_n = N % 64 == 0, one_h = H1 % 64 == 0;
+    if (dX && g.A > 0) {
+        ExpertGemmLaunch r = g;
+        r.form = a2av::kFormGradRows;
+        r.phases = phases;
+        r.K = static_cast<int32_t>(N);
+        r.N = static_cast<int32_t>(H1);
+        r.half_step = 128;
+        r.one_a = r.one_b = one_n;
+        for (int i = 0; i < 2; ++i) {
+            const int p = phases == 2 ? i : 0;
+            if (!operand_map(&r.tmA[i], D[p], 1, g.A, N, bf16, one_n) ||
+                !operand_map(&r.tmB[i], Wt[p], g.e, H1, N, bf16, one_n) ||
+                !output_map(&r.tmY[i], dX, g.A, H1, bf16))
+                return A2AV_ERR_CUDA;
+            r.out[i] = dX;
+        }
+        r.grid = gemm_grid((ceil_div(g.A, 256) + g.e) * ceil_div(H1, 256));
+        if (a2av::launch_expert_gemm(r, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        g.write_status = 0;
+    }
+    if (dW[0]) {
+        ExpertGemmLaunch w = g;
+        w.form = a2av::kFormGradWeight;
+        w.M = static_cast<int32_t>(H1);
+        w.N = static_cast<int32_t>(N);
+        w.half_step = phases == 2 ? 0 : 128;
+        w.one_a = one_h;
+        w.one_b = one_n;
+        for (int i = 0; i < 2; ++i) {
+            const int p = phases == 2 ? i : 0;
+            // Without rows nothing is loaded; the maps still have to be valid.
+            if (g.A > 0 && (!operand_map(&w.tmA[i], X, 1, g.A, H1, bf16, one_h) ||
+                            !operand_map(&w.tmB[i], D[p], 1, g.A, N, bf16, one_n)))
+                return A2AV_ERR_CUDA;
+            if (!output_map(&w.tmY[i], dW[p], g.e * H1, N, bf16)) return A2AV_ERR_CUDA;
+            w.out[i] = dW[p];
+        }
+        w.grid = gemm_grid(g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? 128 : 256));
+        if (a2av::launch_expert_gemm(w, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+    }
+    return A2AV_OK;
+}
+
+a2av_status validate(const a2av_gated_desc *d) {
+    if (!d) return A2AV_ERR_NULLPTR;
+    if (d->W < 1 || d->e < 1 || d->e > a2av::kMaxExperts) return A2AV_ERR_INVALID;
+    if (static_cast<int64_t>(d->W) * d->e > a2av::kMaxSegments) return A2AV_ERR_INVALID;
+    if (d->H1 <= 0 || d->H1 >= 65536 || d->N <= 0 || d->N >= 65536) return A2AV_ERR_INVALID;
+    if (d->A < 0 || d->A > INT32_MAX) return A2AV_ERR_INVALID;
+    if (!type16(d->dtype)) return A2AV_ERR_INVALID;
+    if (d->act != A2AV_ACT_SILU && d->act != A2AV_ACT_GELU_TANH) return A2AV_ERR_INVALID;
+    // One source: the rows are expert-major already.  Several: the backward
+    // pass reads permuteOut, so a call that saves for it writes it too.
+    if (d->W == 1 ? d->want_permute_out != 0 : d->save && !d->want_permute_out) return A2AV_ERR_INVALID;
+    if (!mult8(d->H1) || !mult8(d->N)) return A2AV_ERR_UNSUPPORTED;
+    return A2AV_OK;
+}
+
+size_t staged_bytes(const a2av_gated_desc *d) {
+    return d->W > 1 && !d->want_permute_out ? round256(static_cast<size_t>(d->A) * d->H1 * 2) : 0;
+}
+size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
+    return d->save ? round256(static_cast<size_t>(d->A) * d->N * 2) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const void *residual, const void *gamma,
+                          void *h, void *y, void *codes, void *scales, float *rstd, a2av_stream_t stream) {
+    if (!desc) return A2AV_ERR_NULLPTR;
+    const a2av_rms_norm_desc &d = *desc;
+    if (d.rows < 0 || d.rows > INT32_MAX || d.H <= 0 || d.H >= 65536 || !type16(d.dtype)) return A2AV_ERR_INVALID;
+    if (!(d.eps >= 0.0f)) return A2AV_ERR_INVALID;
+    if (d.x_stride < d.H || (residual && d.residual_stride != 0 && d.residual_stride < d.H)) return A2AV_ERR_INVALID;
+    const a2av_status q = check_quant(d.qtype, d.qmode, d.H);
+    if (q != A2AV_OK) return q;
+    if (!mult8(d.H) || !mult8(d.x_stride) || (residual && !mult8(d.residual_stride))) return A2AV_ERR_UNSUPPORTED;
+    if (!gamma || (d.rows > 0 && !x)) return A2AV_ERR_NULLPTR;
+    if (d.rows > 0 && !h && !y && !codes && !rstd) return A2AV_ERR_NULLPTR;
+    const a2av_status qo = check_quant_out(d.qtype, d.qmode, codes, scales, d.rows > 0);
+    if (qo != A2AV_OK) return qo;
+    for (const void *p : {x, residual, gamma, static_cast<const void *>(h), static_cast<const void *>(y)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (d.rows == 0) return A2AV_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return A2AV_ERR_CUDA;
+    a2av::RmsNormLaunch p{static_cast<int32_t>(d.rows), static_cast<int32_t>(d.H), d.x_stride, d.residual_stride, x,
+                          residual, gamma, h, y, static_cast<uint8_t *>(codes), scales, rstd, d.eps, d.qtype};
+    return a2av::launch_rms_norm(p, d.dtype == A2AV_BF16, d.qtype == A2AV_Q_NONE ? A2AV_Q_NONE : d.qmode, sms,
+                                 reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? A2AV_OK
+               : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_rms_norm_backward_workspace_size(int64_t rows, int64_t H, int32_t dtype, size_t *bytes) {
+    if (!bytes) return A2AV_ERR_NULLPTR;
+    if (rows < 0 || rows > INT32_MAX || H <= 0 || H >= 65536 || !type16(dtype)) return A2AV_ERR_INVALID;
+    if (!mult8(H)) return A2AV_ERR_UNSUPPORTED;
+    *bytes = round256(std::max<size_t>(1, static_cast<size_t>(a2av::rms_norm_grad_blocks(rows, H)) * H * 4));
+    return A2AV_OK;
+}
+
+a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const void *dy, const void *dh,
+                                   const void *h, const void *gamma, const float *rstd, void *dx, float *dgamma,
+                                   void *workspace, size_t workspace_bytes, a2av_stream_t stream) {
+    size_t need = 0;
+    const a2av_status s = a2av_rms_norm_backward_workspace_size(rows, H, dtype, &need);
+    if (s != A2AV_OK) return s;
+    if (rows > 0 && (!dy || !h || !gamma || !rstd || !dx)) return A2AV_ERR_NULLPTR;
+    for (const void *p : {dy, dh, h, gamma, static_cast<const void *>(dx), static_cast<const void *>(dgamma)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (dgamma && rows > 0) {
+        if (!workspace) return A2AV_ERR_NULLPTR;
+        if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    }
+    if (rows == 0 && !dgamma) return A2AV_OK;
+    a2av::RmsNormGradLaunch p{static_cast<int32_t>(rows), static_cast<int32_t>(H), dy, dh, h, gamma, rstd, dx, dgamma,
+                              static_cast<float *>(workspace), a2av::rms_norm_grad_blocks(rows, H)};
+    return a2av::launch_rms_norm_grad(p, dtype == A2AV_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? A2AV_OK
+               : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const void *up, void *h, void *codes,
+                           void *scales, a2av_stream_t stream) {
+    if (!desc) return A2AV_ERR_NULLPTR;
+    const a2av_glu_desc &d = *desc;
+    if (d.rows < 0 || d.rows > INT32_MAX || d.N <= 0 || d.N >= 65536 || !type16(d.dtype)) return A2AV_ERR_INVALID;
+    if (d.act != A2AV_ACT_SILU && d.act != A2AV_ACT_GELU_TANH) return A2AV_ERR_INVALID;
+    if (d.stride < d.N) return A2AV_ERR_INVALID;
+    const a2av_status q = check_quant(d.qtype, d.qmode, d.N);
+    if (q != A2AV_OK) return q;
+    if (!mult8(d.N) || !mult8(d.stride)) return A2AV_ERR_UNSUPPORTED;
+    if (d.rows > 0 && (!gate || !up || (!h && !codes))) return A2AV_ERR_NULLPTR;
+    const a2av_status qo = check_quant_out(d.qtype, d.qmode, codes, scales, d.rows > 0);
+    if (qo != A2AV_OK) return qo;
+    if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(h, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (d.rows == 0) return A2AV_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return A2AV_ERR_CUDA;
+    a2av::GluLaunch p{d.rows, static_cast<int32_t>(d.N), d.stride, gate, up, h, static_cast<uint8_t *>(codes), scales,
+                      d.qtype};
+    return a2av::launch_glu_quant(p, d.dtype == A2AV_BF16, d.act, d.qtype == A2AV_Q_NONE ? A2AV_Q_NONE : d.qmode, sms,
+                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? A2AV_OK
+               : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_gated_workspace_size(const a2av_gated_desc *desc, size_t *bytes) {
+    if (!desc || !bytes) return A2AV_ERR_NULLPTR;
+    const a2av_status s = validate(desc);
+    if (s != A2AV_OK) return s;
+    *bytes = kStatusBytes + std::max(staged_bytes(desc), 2 * slope_bytes(desc));
+    return A2AV_OK;
+}
+
+a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, const int32_t *recvCounts,
+                           const void *gateWeight, const void *upWeight, void *permuteOut, void *h, float *saved,
+                           void *workspace, size_t workspace_bytes, a2av_stream_t stream_handle) {
+    const a2av_status vs = validate(desc);
+    if (vs != A2AV_OK) return vs;
+    const a2av_gated_desc &d = *desc;
+    if (!recvCounts || !gateWeight || !upWeight || !workspace) return A2AV_ERR_NULLPTR;
+    if (d.A > 0 && (!ataOut || !h || (d.want_permute_out && !permuteOut) || (d.save && !saved)))
+        return A2AV_ERR_NULLPTR;
+    for (const void *p : {ataOut, gateWeight, upWeight, static_cast<const void *>(h),
+                          static_cast<const void *>(d.want_permute_out ? permuteOut : nullptr)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(recvCounts, 4) || (d.save && !aligned(saved, 32))) return A2AV_ERR_UNSUPPORTED;
+    size_t need = 0;
+    a2av_gated_workspace_size(desc, &need);
+    if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const int sms = sm_count();
+    if (sms <= 0) return A2AV_ERR_CUDA;
+
+    ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
+    const bool bf16 = g.bf16 != 0;
+    g.form = a2av::kFormGated;
+    g.act = d.act;
+    g.K = static_cast<int32_t>(d.H1);
+    g.N = static_cast<int32_t>(d.N);
+    g.one_a = d.H1 % 64 == 0;
+    g.one_b = d.N % 64 == 0;
+    const void *rows = ataOut;
+    if (d.W > 1 && d.A > 0) {
+        // Expert-major rows: all of them in permuteOut, or in the workspace
+        // those 128-row halves of a tile that straddle a (source, expert) run
+        // boundary, the others being read in place.
+        void *dst = d.want_permute_out ? permuteOut : static_cast<uint8_t *>(workspace) + kStatusBytes;
+        g.direct_halves = d.want_permute_out ? 0 : 1;
+        a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, g.direct_halves, 8};
+        if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        g.write_status = 0;
+        g.after = 1;
+        rows = dst;
+        if (g.direct_halves && !operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
+    }
+    if (d.A > 0) {
+        if (!operand_map(&g.tmA[0], rows, 1, d.A, d.H1, bf16, g.one_a) ||
+            !operand_map(&g.tmB[0], gateWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
+            !operand_map(&g.tmB[1], upWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
+            !output_map(&g.tmY[0], h, d.A, d.N, bf16))
+            return A2AV_ERR_CUDA;
+        g.out[0] = h;
+        if (d.save) {
+            g.saved[0] = saved;
+            g.saved[1] = saved + static_cast<size_t>(d.A) * d.N;
+        }
+    }
+    g.grid = gemm_grid((ceil_div(d.A, 256) + d.e) * ceil_div(d.N, 128));
+    return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, const void *permuteOut,
+                                const int32_t *recvCounts, const void *gateWeight, const void *upWeight,
+                                const float *saved, void *dAtaOut, void *dGate, void *dUp, void *workspace,
+                                size_t workspace_bytes, a2av_stream_t stream_handle) {
+    const a2av_status vs = validate(desc);
+    if (vs != A2AV_OK) return vs;
+    const a2av_gated_desc &d = *desc;
+    if (!d.save) return A2AV_ERR_INVALID;
+    if (!recvCounts || !gateWeight || !upWeight || !workspace) return A2AV_ERR_NULLPTR;
+    if (d.A > 0 && (!dh || !permuteOut || !saved)) return A2AV_ERR_NULLPTR;
+    if ((dGate == nullptr) != (dUp == nullptr) || (!dAtaOut && !dGate)) return A2AV_ERR_NULLPTR;
+    for (const void *p : {dh, permuteOut, gateWeight, upWeight, static_cast<const void *>(dAtaOut),
+                          static_cast<const void *>(dGate), static_cast<const void *>(dUp)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(recvCounts, 4) || !aligned(saved, 32)) return A2AV_ERR_UNSUPPORTED;
+    size_t need = 0;
+    a2av_gated_workspace_size(desc, &need);
+    if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const int sms = sm_count();
+    if (sms <= 0) return A2AV_ERR_CUDA;
+
+    ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
+    uint8_t *slopes = static_cast<uint8_t *>(workspace) + kStatusBytes;
+    void *const dG = slopes, *const dU = slopes + slope_bytes(desc);
+    const int64_t n = d.A * d.N;
+    if (n > 0) {
+        a2av::GluGradLaunch s{n, dh, saved, saved + n, dG, dU};
+        if (a2av::launch_glu_grad(s, g.bf16, d.act, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+    }
+    const void *const D[2] = {dG, dU}, *const Wt[2] = {gateWeight, upWeight};
+    void *const dW[2] = {dGate, dUp};
+    return run_gradients(g, 2, d.H1, d.N, D, permuteOut, Wt, dAtaOut, dW, stream);
+}
+
+a2av_status a2av_gmm_backward_workspace_size(const a2av_gmm_desc *desc, size_t *bytes) {
+    if (!desc || !bytes) return A2AV_ERR_NULLPTR;
+    size_t unused = 0;
+    const a2av_status s = a2av_gmm_workspace_size(desc, &unused);  // the shapes' limits
+    if (s != A2AV_OK) return s;
+    if (desc->BS != 0) return A2AV_ERR_INVALID;
+    *bytes = kStatusBytes;
+    return A2AV_OK;
+}
+
+a2av_status a2av_gmm_backward(const a2av_gmm_desc *desc, const void *dY, const void *permuteOut,
+                              const int32_t *recvCounts, const void *gmmWeight, void *dAtaOut, void *dWeight,
+                              void *workspace, size_t workspace_bytes, a2av_stream_t stream_handle) {
+    size_t need = 0;
+    const a2av_status s = a2av_gmm_backward_workspace_size(desc, &need);
+    if (s != A2AV_OK) return s;
+    const a2av_gmm_desc &d = *desc;
+    if (!recvCounts || !workspace || (!dAtaOut && !dWeight)) return A2AV_ERR_NULLPTR;
+    if (d.A > 0 && (!dY || (dWeight && !permuteOut))) return A2AV_ERR_NULLPTR;
+    if (dAtaOut && !gmmWeight) return A2AV_ERR_NULLPTR;
+    for (const void *p : {dY, permuteOut, gmmWeight, static_cast<const void *>(dAtaOut),
+                          static_cast<const void *>(dWeight)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(recvCounts, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    const ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
+    const void *const D[2] = {dY, nullptr}, *const Wt[2] = {gmmWeight, nullptr};
+    void *const dW[2] = {dWeight, nullptr};
+    return run_gradients(g, 1, d.H1, d.N1, D, permuteOut, Wt, dAtaOut, dW,
+                         reinterpret_cast<cudaStream_t>(stream_handle));
+}
+
+}  // extern "C"
