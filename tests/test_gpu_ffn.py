@@ -285,6 +285,28 @@ def test_gmm_backward(W, H1, N, sizes, dt):
     R.assert_rounded(dw, rw, ew, "dWeight")
 
 
+@pytest.mark.parametrize("W,H1,N,sizes", [
+    (1, 4096, 1024, [1]), (8, 4096, 1024, [3, 0, 4, 1]), (2, 8, 8, [1, 1]), (1, 1000, 72, [7]), (4, 520, 200, [0, 0, 0, 9]),
+    (3, 2048, 136, [16]), (8, 264, 64, [1, 0, 2, 0, 1, 5, 3, 4]), (16, 7168, 320, [2] * 6), (1, 40, 1408, [8, 8]),
+])
+@pytest.mark.parametrize("name", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_gated_few_rows(W, H1, N, sizes, name, dt):
+    dtype = DT[dt]
+    e, A, counts, x, wg, wu = _inputs(W, H1, N, sizes, dtype, seed=120)
+    f = R.gated(x, counts, W, e, wg, wu, name)
+    rc = torch.from_numpy(counts).cuda()
+    guard = torch.full((A * N + 512,), 5.0, dtype=dtype, device="cuda")
+    plan = binding.GatedPlan(W, e, A, H1, N, dtype, name, save=W == 1)
+    r = plan.run(dev(x), rc, *dev(wg, wu), h=guard[:A * N].view(A, N))
+    assert _status(plan) == (0, 0)
+    R.assert_rounded(r.h, f["h"], f["eh"], "h")
+    assert bool((guard[A * N:] == 5.0).all())
+    if W == 1:
+        for got, ref, err in ((r.saved[0], f["G"], f["eg"]), (r.saved[1], f["U"], f["eu"])):
+            assert bool(((got.cpu().double() - ref).abs() <= err).all())
+
+
 def test_gated_gradient_against_differences():
     """<gradient, direction> against central differences of the float64 forward."""
     W, H1, N, sizes, name = 2, 136, 72, [40, 0, 23], "silu"

@@ -432,8 +432,11 @@ class MxPlan:
 # ---- the operators around the grouped product (include/a2av_ffn.h)
 
 
+# These calls are a few microseconds on the GPU for a single token, so their checks are kept to the fewest steps.
+
+
 def _call(name, *args):
-    st = getattr(load(), name)(*args)
+    st = getattr(_lib or load(), name)(*args)
     if st != A2AV_OK:
         raise A2avError(st, name)
 
@@ -448,38 +451,46 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, device):
-    """Handle of the stream to enqueue on: the given one, or the device's current one."""
-    return stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+def _on(stream, t):
+    """Handle of the stream to enqueue on: the given one, or the current one of t's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _rows_of(t, name, dtype=None):
-    """A 2-D CUDA tensor whose rows are contiguous; returns the elements from one row to the next."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+def _is(t, name, dtype, shape):
+    """t is a contiguous CUDA tensor of this type and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows_of(t, name):
+    """A 2-D CUDA tensor of 16-bit floats whose rows are contiguous; returns (type code, elements from one row to the
+    next)."""
+    code = DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError(f"{name} must be a bfloat16 or float16 tensor, got {getattr(t, 'dtype', type(t))}")
+    if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    step, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return code, step if rows > 1 else cols
 
 
-def _out(t, name, shape, dtype, device):
-    """The caller's output tensor, checked, or a new one."""
+def _out(t, name, dtype, shape, like):
+    """The caller's output tensor, checked, or a new one on `like`'s device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _is(t, name, dtype, shape)
     return t
-
-
-def _dtype16(t, name):
-    if t.dtype not in DTYPES:
-        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    return DTYPES[t.dtype]
 
 
 def _named(table, key, what):
@@ -488,14 +499,12 @@ def _named(table, key, what):
     return table[key]
 
 
-def _code_outputs(out, rows, cols, qtype, mode, device):
-    """(codes, scales) to write: those of an earlier result, or new ones; (None, None) without a qtype."""
-    if qtype is None:
-        return None, None
-    block = 32 if mode == "mx" else 128
-    return (_out(out.codes if out else None, "codes", (rows, cols), torch.uint8, device),
-            _out(out.scales if out else None, "scales", (rows, cols // block),
-                 torch.uint8 if mode == "mx" else torch.float32, device))
+def _code_outputs(out, rows, cols, mode, like):
+    """(codes, scales) to write: those of an earlier result, or new ones."""
+    mx = mode == "mx"
+    return (_out(out.codes if out else None, "codes", torch.uint8, (rows, cols), like),
+            _out(out.scales if out else None, "scales", torch.uint8 if mx else torch.float32,
+                 (rows, cols // (32 if mx else 128)), like))
 
 
 class RmsNormOut(NamedTuple):
@@ -512,54 +521,49 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
     "e5m2" or "int8"; mode "mx" or "group128") and / or in the element type (want_y; by default without a qtype).
     Rows of x and residual may be strided; residual may be one row expanded to all.  `out`: an earlier result of the
     same call, whose tensors are written again."""
-    code = _dtype16(x, "x")
-    rows, H = x.shape if x.dim() == 2 else (0, 0)
-    xs = _rows_of(x, "x")
-    _check(gamma, "gamma", x.dtype, 1)
-    if gamma.shape[0] != H:
-        raise ValueError(f"gamma must be [{H}]")
-    rs = 0
+    code, xs = _rows_of(x, "x")
+    shape, dtype = x.shape, x.dtype
+    rows, H = shape
+    _is(gamma, "gamma", dtype, (H,))
+    q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
+    rs, h = 0, None
     if residual is not None:
-        rs = _rows_of(residual, "residual", x.dtype)
-        if residual.shape != x.shape:
-            raise ValueError("residual must have the shape of x")
-    if want_y is None:
-        want_y = qtype is None
-    q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
-    m = _named(QMODES, mode, "mode")
-    dev = x.device
-    h = None if residual is None else _out(out.h if out else None, "h", (rows, H), x.dtype, dev)
-    y = _out(out.y if out else None, "y", (rows, H), x.dtype, dev) if want_y else None
-    rstd = _out(out.rstd if out else None, "rstd", (rows,), torch.float32, dev) if want_rstd else None
-    codes, scales = _code_outputs(out, rows, H, qtype, mode, dev)
+        _, rs = _rows_of(residual, "residual")
+        if residual.shape != shape or residual.dtype != dtype:
+            raise ValueError("residual must have the shape and type of x")
+        h = _out(out.h if out else None, "h", dtype, shape, x)
+    y = codes = scales = rstd = None
+    if want_y or (want_y is None and qtype is None):
+        y = _out(out.y if out else None, "y", dtype, shape, x)
+    if want_rstd:
+        rstd = _out(out.rstd if out else None, "rstd", torch.float32, (rows,), x)
+    if qtype is not None:
+        codes, scales = _code_outputs(out, rows, H, mode, x)
     desc = RmsNormDesc(rows, H, xs, rs, code, q, m, eps)
-    _call("a2av_rms_norm", ctypes.byref(desc), _at(x), _at(residual), _at(gamma), _at(h), _at(y), _at(codes),
-          _at(scales), _at(rstd), _on(stream, dev))
+    _call("a2av_rms_norm", ctypes.byref(desc), x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
+          _at(codes), _at(scales), _at(rstd), _on(stream, x))
     return RmsNormOut(h, y, codes, scales, rstd)
 
 
 def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, workspace=None, stream=None):
     """(dx [rows, H], dgamma float32 [H]) from the gradient dy of the normed rows and, optionally, the gradient dh
     that reaches h directly.  dx is the gradient of x and of the residual."""
-    code = _dtype16(dy, "dy")
-    _check(dy, "dy", None, 2)
-    rows, H = dy.shape
-    for t, name in ((h, "h"), (dh, "dh")):
-        if t is not None:
-            _check(t, name, dy.dtype, 2)
-            if t.shape != dy.shape:
-                raise ValueError(f"{name} must be [{rows}, {H}]")
-    _check(gamma, "gamma", dy.dtype, 1)
-    _check(rstd, "rstd", torch.float32, 1)
-    if gamma.shape[0] != H or rstd.shape[0] != rows:
-        raise ValueError(f"gamma must be [{H}] and rstd [{rows}]")
-    dx = _out(dx, "dx", (rows, H), dy.dtype, dy.device)
-    dgamma = _out(dgamma, "dgamma", (H,), torch.float32, dy.device)
+    code, _ = _rows_of(dy, "dy")
+    shape, dtype = dy.shape, dy.dtype
+    rows, H = shape
+    _is(dy, "dy", dtype, shape)
+    _is(h, "h", dtype, shape)
+    if dh is not None:
+        _is(dh, "dh", dtype, shape)
+    _is(gamma, "gamma", dtype, (H,))
+    _is(rstd, "rstd", torch.float32, (rows,))
+    dx = _out(dx, "dx", dtype, shape, dy)
+    dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy)
     if workspace is None:
         workspace = torch.empty(_size("a2av_rms_norm_backward_workspace_size", rows, H, code), dtype=torch.uint8,
                                 device=dy.device)
     _call("a2av_rms_norm_backward", rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd), _at(dx),
-          _at(dgamma), _at(workspace), workspace.numel(), _on(stream, dy.device))
+          _at(dgamma), _at(workspace), workspace.numel(), _on(stream, dy))
     return dx, dgamma
 
 
@@ -573,41 +577,22 @@ def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, 
                    stream=None) -> GluQuantOut:
     """act(gate) * up of gate_up [rows, 2N] (gate columns, then up columns) as codes and scales and / or in the
     element type (want_h; by default without a qtype)."""
-    code = _dtype16(gate_up, "gate_up")
-    stride = _rows_of(gate_up, "gate_up")
-    rows, N = gate_up.shape[0], gate_up.shape[1] // 2
-    if gate_up.shape[1] != 2 * N:
+    code, stride = _rows_of(gate_up, "gate_up")
+    rows, cols = gate_up.shape
+    N = cols // 2
+    if cols != 2 * N:
         raise ValueError("gate_up must have an even number of columns")
-    if want_h is None:
-        want_h = qtype is None
     q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
     desc = GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode"))
-    dev = gate_up.device
-    codes, scales = _code_outputs(out, rows, N, qtype, mode, dev)
-    h = _out(out.h if out else None, "h", (rows, N), gate_up.dtype, dev) if want_h else None
-    gate = _at(gate_up)
+    codes = scales = h = None
+    if qtype is not None:
+        codes, scales = _code_outputs(out, rows, N, mode, gate_up)
+    if want_h or (want_h is None and qtype is None):
+        h = _out(out.h if out else None, "h", gate_up.dtype, (rows, N), gate_up)
+    gate = gate_up.data_ptr()
     _call("a2av_glu_quant", ctypes.byref(desc), gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
-          _on(stream, dev))
+          _on(stream, gate_up))
     return GluQuantOut(codes, scales, h)
-
-
-def _rank_rows(t, name, rows, cols, dtype):
-    if rows:
-        _check(t, name, dtype, 2)
-        if tuple(t.shape) != (rows, cols):
-            raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
-
-
-def _counts(t, n):
-    _check(t, "recvCounts", torch.int32, 1)
-    if t.numel() != n:
-        raise ValueError(f"recvCounts must have {n} entries")
-
-
-def _weights(t, name, shape, dtype):
-    _check(t, name, dtype, 3)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 class GatedOut(NamedTuple):
@@ -639,49 +624,41 @@ class GatedPlan:
         self.workspace = torch.empty(_size("a2av_gated_workspace_size", ctypes.byref(self.desc)), dtype=torch.uint8,
                                      device=self.device)
 
-    def _check_weights(self, gateWeight, upWeight):
+    def _check_shared(self, recvCounts, gateWeight, upWeight):
         d = self.desc
-        _weights(gateWeight, "gateWeight", (d.e, d.H1, d.N), self.dtype)
-        _weights(upWeight, "upWeight", (d.e, d.H1, d.N), self.dtype)
+        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
+        _is(gateWeight, "gateWeight", self.dtype, (d.e, d.H1, d.N))
+        _is(upWeight, "upWeight", self.dtype, (d.e, d.H1, d.N))
 
     def run(self, ataOut, recvCounts, gateWeight, upWeight, h=None, saved=None, permuteOut=None,
             stream=None) -> GatedOut:
-        d = self.desc
-        _rank_rows(ataOut, "ataOut", d.A, d.H1, self.dtype)
-        _counts(recvCounts, d.W * d.e)
-        self._check_weights(gateWeight, upWeight)
-        h = _out(h, "h", (d.A, d.N), self.dtype, self.device)
-        if d.save:
-            saved = _out(saved, "saved", (2, d.A, d.N), torch.float32, self.device)
-        if d.want_permute_out:
-            permuteOut = _out(permuteOut, "permuteOut", (d.A, d.H1), self.dtype, self.device)
-        _call("a2av_gated_run", ctypes.byref(d), _at(ataOut), _at(recvCounts), _at(gateWeight), _at(upWeight),
-              _at(permuteOut) if d.want_permute_out else None, _at(h), _at(saved) if d.save else None,
-              self.workspace.data_ptr(), self.workspace.numel(), _on(stream, self.device))
-        return GatedOut(h, saved if d.save else None,
-                        permuteOut if d.want_permute_out else (ataOut if d.W == 1 else None))
+        d, dtype, ws = self.desc, self.dtype, self.workspace
+        A, H1, N = d.A, d.H1, d.N
+        _is(ataOut, "ataOut", dtype, (A, H1))
+        self._check_shared(recvCounts, gateWeight, upWeight)
+        h = _out(h, "h", dtype, (A, N), ws)
+        saved = _out(saved, "saved", torch.float32, (2, A, N), ws) if d.save else None
+        permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ws) if d.want_permute_out else None
+        _call("a2av_gated_run", ctypes.byref(d), ataOut.data_ptr(), recvCounts.data_ptr(), gateWeight.data_ptr(),
+              upWeight.data_ptr(), _at(permuted), h.data_ptr(), _at(saved), ws.data_ptr(), ws.numel(),
+              _on(stream, ws))
+        return GatedOut(h, saved, ataOut if d.W == 1 else permuted)
 
     def backward(self, dh, permuteOut, recvCounts, gateWeight, upWeight, saved, want_rows=True, want_weights=True,
                  dAtaOut=None, dGate=None, dUp=None, stream=None) -> GatedGrads:
-        d = self.desc
-        _rank_rows(dh, "dh", d.A, d.N, self.dtype)
-        _rank_rows(permuteOut, "permuteOut", d.A, d.H1, self.dtype)
-        _counts(recvCounts, d.W * d.e)
-        self._check_weights(gateWeight, upWeight)
-        _check(saved, "saved", torch.float32, 3)
-        if tuple(saved.shape) != (2, d.A, d.N):
-            raise ValueError(f"saved must be {[2, d.A, d.N]}")
-        if want_rows:
-            dAtaOut = _out(dAtaOut, "dAtaOut", (d.A, d.H1), self.dtype, self.device)
-        if want_weights:
-            dGate = _out(dGate, "dGate", (d.e, d.H1, d.N), self.dtype, self.device)
-            dUp = _out(dUp, "dUp", (d.e, d.H1, d.N), self.dtype, self.device)
-        _call("a2av_gated_backward", ctypes.byref(d), _at(dh), _at(permuteOut), _at(recvCounts), _at(gateWeight),
-              _at(upWeight), _at(saved), _at(dAtaOut) if want_rows else None, _at(dGate) if want_weights else None,
-              _at(dUp) if want_weights else None, self.workspace.data_ptr(), self.workspace.numel(),
-              _on(stream, self.device))
-        return GatedGrads(dAtaOut if want_rows else None, dGate if want_weights else None,
-                          dUp if want_weights else None)
+        d, dtype, ws = self.desc, self.dtype, self.workspace
+        A, H1, N = d.A, d.H1, d.N
+        _is(dh, "dh", dtype, (A, N))
+        _is(permuteOut, "permuteOut", dtype, (A, H1))
+        self._check_shared(recvCounts, gateWeight, upWeight)
+        _is(saved, "saved", torch.float32, (2, A, N))
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), ws) if want_rows else None
+        gate = _out(dGate, "dGate", dtype, (d.e, H1, N), ws) if want_weights else None
+        up = _out(dUp, "dUp", dtype, (d.e, H1, N), ws) if want_weights else None
+        _call("a2av_gated_backward", ctypes.byref(d), dh.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
+              gateWeight.data_ptr(), upWeight.data_ptr(), saved.data_ptr(), _at(rows), _at(gate), _at(up),
+              ws.data_ptr(), ws.numel(), _on(stream, ws))
+        return GatedGrads(rows, gate, up)
 
 
 class GmmBackwardPlan:
@@ -697,16 +674,14 @@ class GmmBackwardPlan:
     def run(self, dY, permuteOut, recvCounts, gmmWeight, want_rows=True, want_weights=True, dAtaOut=None,
             dWeight=None, stream=None):
         """(dAtaOut [A, H1] rank-major, dWeight [e, H1, N1]); either may be left out (None)."""
-        d = self.desc
-        _rank_rows(dY, "dY", d.A, d.N1, self.dtype)
-        _rank_rows(permuteOut, "permuteOut", d.A, d.H1, self.dtype)
-        _counts(recvCounts, d.W * d.e)
-        _weights(gmmWeight, "gmmWeight", (d.e, d.H1, d.N1), self.dtype)
-        if want_rows:
-            dAtaOut = _out(dAtaOut, "dAtaOut", (d.A, d.H1), self.dtype, self.device)
-        if want_weights:
-            dWeight = _out(dWeight, "dWeight", (d.e, d.H1, d.N1), self.dtype, self.device)
-        _call("a2av_gmm_backward", ctypes.byref(d), _at(dY), _at(permuteOut), _at(recvCounts), _at(gmmWeight),
-              _at(dAtaOut) if want_rows else None, _at(dWeight) if want_weights else None,
-              self.workspace.data_ptr(), self.workspace.numel(), _on(stream, self.device))
-        return dAtaOut if want_rows else None, dWeight if want_weights else None
+        d, dtype, ws = self.desc, self.dtype, self.workspace
+        A, H1, N1 = d.A, d.H1, d.N1
+        _is(dY, "dY", dtype, (A, N1))
+        _is(permuteOut, "permuteOut", dtype, (A, H1))
+        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
+        _is(gmmWeight, "gmmWeight", dtype, (d.e, H1, N1))
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), ws) if want_rows else None
+        weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), ws) if want_weights else None
+        _call("a2av_gmm_backward", ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
+              gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel(), _on(stream, ws))
+        return rows, weights

@@ -1,11 +1,11 @@
 // Persistent ragged GEMMs of an expert layer's gated block and gradients, on
 // tcgen05 tensor cores (sm_103a), for the experts j of a rank:
 //
-//   gated            h = act(X Wg_j) * (X Wu_j)
-//   rows' gradient   dX = D_0 W_0j^T (+ D_1 W_1j^T)
-//   weights' gradient  dW_j = X_j^T D_j
+//   gated      h = act(X Wg_j) * (X Wu_j)
+//   gradients  dX = D_0 W_0j^T (+ D_1 W_1j^T)  and  dW_j = X_j^T D_j
 //
-// One kernel, three ways of walking the operands.  A cluster of two CTAs
+// Three ways of walking the operands, two kernels: both gradients' tiles are
+// one list, so that they share a launch and its tail.  A cluster of two CTAs
 // computes a tile of 256 rows x 256 accumulator columns with one cta_group::2
 // MMA: each CTA stages 128 of the rows of A and half of the columns of B.  The
 // even CTA issues the MMAs; each CTA holds its 128 rows of the accumulator.
@@ -23,7 +23,7 @@
 // reads it: with the contraction along the elements (K-major) or along the
 // rows (MN-major), a bit in the instruction descriptor and two strides.
 //
-//   form              A tile (rows x elements)   B tile (rows x elements)
+//   tile              A (rows x elements)        B (rows x elements)
 //   gated             X: rows x K    K-major     W: K x columns        MN-major
 //   rows' gradient    D: rows x K    K-major     W: out columns x K    K-major
 //   weights' gradient X: K x M       MN-major    D: K x columns        MN-major
@@ -35,6 +35,11 @@
 // operands by a warp of each CTA before the MMA may read them: multiplying by
 // zero on one side alone would let another expert's infinities through.
 //
+// The rows of A may still be in the making when this kernel starts: the kernel
+// before it in the stream (stage.cu) writes them in the order the tiles go and
+// counts the finished pieces of each 128 rows, and the producer waits for a
+// tile's counts.  That kernel is small enough to share the SMs with this one.
+//
 // Per CTA: warp 0 loads, warp 1 clears ragged rows (weights' gradient), warp 4
 // allocates TMEM and (even CTA) issues, warps 5-8 are the epilogue.  Two
 // accumulators let a tile's epilogue overlap the next tile's main loop.  Every
@@ -42,6 +47,7 @@
 #include "activation.cuh"
 #include "ffn.h"
 #include "pair.cuh"
+#include "pdl.cuh"
 
 namespace a2av {
 
@@ -63,9 +69,10 @@ constexpr uint32_t kEpiBufBytes = 32 * 64;  // 32 rows x 32 columns of 16 bits
 constexpr uint32_t kEpiWarpBytes = 2 * kEpiBufBytes;
 
 struct GroupInfo {
-    int32_t row0;        // first expert-major row
+    int32_t row0;   // first expert-major row
     int32_t rows;
-    int32_t tile_start;  // first linear tile
+    int32_t tile0;  // first tile over its rows
+    int32_t half0;  // first 128-row half
 };
 
 struct Control {
@@ -77,7 +84,7 @@ struct Control {
     uint64_t tempty[2];        // even CTA: both epilogues have drained it
     uint32_t tmem_base;
     int32_t abort;
-    int32_t total_tiles;
+    int32_t row_tiles, total_tiles;
     GroupInfo g[kMaxExperts + 1];
     SegmentTable seg;
 };
@@ -88,14 +95,26 @@ static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 struct Tile {
     int g, m, n;
+    bool weights;  // of the weights' gradient
 };
 
-// Tiles of a group: row tiles in order, column tiles innermost.
-__device__ __forceinline__ Tile tile_at(const Control &c, int t, int tn) {
+// What a launch's tiles cover.
+struct Walk {
+    int tn;       // column tiles of a tile over rows
+    int wm, wn;   // row and column tiles of an expert's weights' gradient
+};
+
+// The tiles over the experts' rows, then those of the weights' gradients; of
+// each expert the row tiles in order, column tiles innermost.
+__device__ __forceinline__ Tile tile_at(const Control &c, int t, const Walk &k) {
+    if (t >= c.row_tiles) {
+        const int u = t - c.row_tiles, per = k.wm * k.wn, local = u % per;
+        return {u / per, local / k.wn, local % k.wn, true};
+    }
     int g = 0;
-    while (t >= c.g[g + 1].tile_start) ++g;
-    const int local = t - c.g[g].tile_start;
-    return {g, local / tn, local % tn};
+    while (t >= c.g[g + 1].tile0) ++g;
+    const int local = t - c.g[g].tile0;
+    return {g, local / k.tn, local % k.tn, false};
 }
 
 __device__ __forceinline__ void st_global_f32x8(float *ptr, const uint32_t *r) {
@@ -106,11 +125,10 @@ __device__ __forceinline__ void st_global_f32x8(float *ptr, const uint32_t *r) {
 
 // Instruction descriptor for kind::f16 with an fp32 accumulator and the
 // operands' majors, M = N = 256.
-template <bool BF16, int FORM>
-__device__ __forceinline__ constexpr uint32_t instr_desc() {
-    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) |
-           ((FORM == kFormGradWeight ? 1u : 0u) << 15) | ((FORM == kFormGradRows ? 0u : 1u) << 16) |
-           ((256u >> 3) << 17) | ((256u >> 4) << 24);
+template <bool BF16>
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool a_mn, bool b_mn) {
+    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 // Contraction block kb of a tile: its first element and how many of its 128
@@ -118,17 +136,41 @@ __device__ __forceinline__ constexpr uint32_t instr_desc() {
 struct Block {
     int first, len;
 };
-template <int FORM>
-__device__ __forceinline__ Block block_of(int K, int kb) {
-    if constexpr (FORM == kFormGradWeight) {
-        const int rem = K % BK, whole = K / BK;
-        if (rem == 0) return {kb * BK, BK};
-        return kb == 0 ? Block{whole * BK, rem} : Block{(kb - 1) * BK, BK};
+__device__ __forceinline__ Block block_of(bool weights, int K, int kb) {
+    if (weights && K % BK != 0) {
+        if (kb == 0) return {K / BK * BK, K % BK};
+        return {(kb - 1) * BK, BK};
     }
     return {kb * BK, min(BK, K - kb * BK)};
 }
 
-template <bool BF16, int FORM, int ACT>
+// Until the count of finished pieces reaches `want`, by one thread; then the
+// rows may be read by TMA.  False: gave up.
+__device__ __noinline__ bool wait_pieces(int32_t *abort_flag, const int32_t *count, int32_t want, int32_t *status,
+                                         uint64_t limit_ns) {
+    const auto done = [&]() {
+        int32_t v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        return v >= want;
+    };
+    if (!done()) {
+        const uint64_t t0 = global_timer_ns();
+        while (!done()) {
+            __nanosleep(100);
+            if (*reinterpret_cast<volatile int32_t *>(abort_flag)) return false;
+            if (global_timer_ns() - t0 > limit_ns) {
+                *reinterpret_cast<volatile int32_t *>(abort_flag) = 1;
+                atomicOr(status, kStatusTimeout);
+                return false;
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return true;
+}
+
+// GRAD: the gradients' tiles (both kinds); otherwise the gated block's.
+template <bool BF16, bool GRAD, int ACT>
 __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertGemmLaunch p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -140,31 +182,35 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = pair::cluster_rank();
     const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
-    // Columns of the output one tile covers.
-    const int tile_n = FORM == kFormGradRows || p.half_step ? 256 : 128;
-    const int tn = (p.N + tile_n - 1) / tile_n;
+    // Columns of the output one tile covers; the tiles of a launch.
+    const int row_n = GRAD ? 256 : 128, w_n = p.half_step ? 256 : 128;
+    const Walk walk{(p.N + row_n - 1) / row_n, (p.wM + TILE_M - 1) / TILE_M, (p.wN + w_n - 1) / w_n};
 
     // ---- prologue: groups and tiles (warp 0), barriers (warp 1), TMEM (MMA warp)
     if (warp == 0) {
+        // (With rows in the making, the kernel that makes them has waited for
+        // all before it, and recvCounts was there for it too.)
+        if (!p.pieces) pdl_wait();
         const bool good = build_segment_table(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int row0 = 0, rows = 0, tiles = 0;
         if (lane < p.e) {
             row0 = C.seg.dst[lane * p.W];
             rows = C.seg.dst[(lane + 1) * p.W] - row0;
-            const int tm = FORM == kFormGradWeight ? (p.M + TILE_M - 1) / TILE_M : (rows + TILE_M - 1) / TILE_M;
-            tiles = good ? tm * tn : 0;
+            tiles = good ? (rows + TILE_M - 1) / TILE_M * walk.tn : 0;
         }
-        int inc = tiles;
+        const int halves = (rows + BM - 1) / BM;
+        int inc = tiles, hinc = halves;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += v;
+            const int v = __shfl_up_sync(0xffffffffu, inc, off), h = __shfl_up_sync(0xffffffffu, hinc, off);
+            if (lane >= off) inc += v, hinc += h;
         }
-        if (lane < p.e) C.g[lane] = GroupInfo{row0, rows, inc - tiles};
+        if (lane < p.e) C.g[lane] = GroupInfo{row0, rows, inc - tiles, hinc - halves};
         const int total = __shfl_sync(0xffffffffu, inc, 31);
         if (lane == 0) {
-            C.g[p.e] = GroupInfo{0, 0, total};
-            C.total_tiles = total;
+            C.g[p.e] = GroupInfo{0, 0, total, 0};
+            C.row_tiles = total;
+            C.total_tiles = total + (good ? p.e * walk.wm * walk.wn : 0);
             C.abort = 0;
             if (blockIdx.x == 0) {
                 if (p.write_status) *p.status = good ? 0 : kStatusBadCounts;
@@ -187,9 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         }
     } else if (warp == 2) {
         if (lane == 0) {
-            prefetch_tensormap(&p.tmA[0]);
-            prefetch_tensormap(&p.tmB[FORM == kFormGradRows ? 0 : rank]);
-            prefetch_tensormap(&p.tmY[0]);
+            if (walk.tn > 0) {
+                prefetch_tensormap(&p.tmA[0]);
+                prefetch_tensormap(&p.tmB[GRAD ? 0 : rank]);
+            } else {
+                prefetch_tensormap(&p.tmX);
+            }
         }
     } else if (warp == kMmaWarp) {
         pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
@@ -201,41 +250,47 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     const int total = C.total_tiles;
     const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
     const uint32_t ragged0 = smem_u32(&C.ragged[0]), cleared0 = smem_u32(&C.cleared[0]);
-    const auto contraction = [&](const Tile &w) { return FORM == kFormGradWeight ? C.g[w.g].rows : p.K; };
-    const auto is_ragged = [&](const Block &b) { return FORM == kFormGradWeight && (b.len & 15) != 0; };
+    const auto contraction = [&](const Tile &w) { return w.weights ? C.g[w.g].rows : p.K; };
+    const auto is_ragged = [&](const Tile &w, const Block &b) { return w.weights && (b.len & 15) != 0; };
+    const auto steps_of = [&](const Tile &w, int kblocks) { return GRAD && !w.weights ? p.phases * kblocks : kblocks; };
 
     if (warp == 0) {
         // =========================================================== producer
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            bool ready = !p.after;  // what the kernel before this one writes is visible
+            bool all_there = !p.pieces;  // the kernel before this one has completed
             for (int t = unit; t < total && ok; t += nunits) {
-                const Tile w = tile_at(C, t, tn);
+                const Tile w = tile_at(C, t, walk);
                 const int K = contraction(w);
-                const int kblocks = (K + BK - 1) / BK;
+                const int kblocks = (K + BK - 1) / BK, steps = steps_of(w, kblocks);
+                const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
                 const int row = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM;  // this CTA's first row
-                // Gated, rows taken in place: a half whose rows of this group
-                // lie in one (source, expert) run is contiguous in ataOut; the
-                // permute kernel staged only the others.
                 const CUtensorMap *ta = &p.tmA[0];
                 int arow = row;
-                if (FORM == kFormGated && p.direct_halves) {
-                    const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
-                    if (row < g_end && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
-                        ta = &p.tmDirect;
-                        arow = source_row(C.seg, p.W, p.e, row);
+                if (!GRAD && p.direct_halves && row < g_end && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
+                    // A half whose rows of this group lie in one (source, expert)
+                    // run is read where it arrived.
+                    ta = &p.tmDirect;
+                    arow = source_row(C.seg, p.W, p.e, row);
+                } else if (!all_there) {
+                    if (w.weights) {  // all of the rows are contracted
+                        pdl_wait();
+                        all_there = true;
+                    } else if (row < g_end) {
+                        // Staged halves are counted by half, the gradients' rows by blocks of 128 rows.
+                        const int c0 = GRAD ? row / BM : C.g[w.g].half0 + 2 * w.m + static_cast<int>(rank);
+                        const int c1 = GRAD ? (min(row + BM, g_end) - 1) / BM : c0;
+                        for (int c = c0; c <= c1 && ok; ++c)
+                            ok = wait_pieces(&C.abort, p.pieces + c, GRAD && c == p.A / BM ? p.last_pieces : p.row_pieces,
+                                             p.status, p.wait_limit_ns);
+                        if (!ok) break;
                     }
                 }
-                if (!ready && ta != &p.tmDirect) {
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    ready = true;
-                }
-                const int steps = FORM == kFormGradRows ? p.phases * kblocks : kblocks;
                 for (int i = 0; i < steps; ++i, ++it) {
                     const int s = it % kStages;
-                    const int phase = FORM == kFormGradRows && i >= kblocks ? 1 : 0;
-                    const Block b = block_of<FORM>(K, i - phase * kblocks);
+                    const int phase = GRAD && !w.weights && i >= kblocks ? 1 : 0;
+                    const Block b = block_of(w.weights, K, i - phase * kblocks);
                     if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.status,
                                           p.wait_limit_ns)) {
                         ok = false;
@@ -245,33 +300,36 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     // Where the loads complete: the even CTA's barrier for
                     // both CTAs' parts; a ragged block on each CTA's own.
                     uint32_t bar;
-                    if (is_ragged(b)) {
+                    if (is_ragged(w, b)) {
                         bar = ragged0 + 8 * s;
                         mbar_arrive_expect_tx(bar, kStageBytes);
                     } else {
                         if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStageBytes);
                         bar = pair::map_to_rank(full0 + 8 * s, 0);
                     }
-                    int ax, ay, bx, by, bz;
+                    int ax, ay, bx, by, bz = w.g;
                     const CUtensorMap *a_map, *b_map;
-                    if constexpr (FORM == kFormGated) {
+                    bool one_a = p.one_a, one_b = p.one_b;
+                    if constexpr (!GRAD) {
                         a_map = ta, ax = b.first, ay = arow;
-                        b_map = &p.tmB[rank], bx = w.n * 128, by = b.first, bz = w.g;
-                    } else if constexpr (FORM == kFormGradRows) {
+                        b_map = &p.tmB[rank], bx = w.n * 128, by = b.first;
+                    } else if (!w.weights) {
                         a_map = &p.tmA[phase], ax = b.first, ay = row;
-                        b_map = &p.tmB[phase], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128, bz = w.g;
+                        b_map = &p.tmB[phase], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128;
                     } else {
-                        const int k_row = C.g[w.g].row0 + b.first;
-                        a_map = &p.tmA[0], ax = w.m * TILE_M + static_cast<int>(rank) * BM, ay = k_row;
-                        b_map = &p.tmB[rank], bx = w.n * tile_n + static_cast<int>(rank) * p.half_step, by = k_row, bz = 0;
+                        ay = by = C.g[w.g].row0 + b.first;
+                        a_map = &p.tmX, ax = w.m * TILE_M + static_cast<int>(rank) * BM;
+                        b_map = &p.tmA[p.half_step ? 0 : rank], bx = w.n * w_n + static_cast<int>(rank) * p.half_step;
+                        bz = 0;
+                        one_a = p.one_x, one_b = p.one_a;
                     }
-                    if (p.one_a) {
+                    if (one_a) {
                         pair::load_4d(a_st, a_map, bar, 0, ay, ax / 64, 0);
                     } else {
                         pair::load_3d(a_st, a_map, bar, ax, ay, 0);
                         pair::load_3d(a_st + kAtomBytes, a_map, bar, ax + 64, ay, 0);
                     }
-                    if (p.one_b) {
+                    if (one_b) {
                         pair::load_4d(b_st, b_map, bar, 0, by, bx / 64, bz);
                     } else {
                         pair::load_3d(b_st, b_map, bar, bx, by, bz);
@@ -279,21 +337,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     }
                 }
             }
+            pdl_trigger();
+            if (!all_there) pdl_wait();  // (a kernel's end implies that of all before it)
             // Tail: every stage filled has been released (no copy in flight).
             for (int i = 0; i < kStages && ok; ++i, ++it)
                 ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % kStages), ((it / kStages) & 1) ^ 1, p.status,
                                       p.wait_limit_ns);
         }
-    } else if (warp == kClearWarp && FORM == kFormGradWeight) {
+    } else if (warp == kClearWarp && GRAD) {
         // ============================================= ragged rows of the block
         uint32_t it = 0;
         uint32_t used = 0;  // parity, by stage, of the ragged blocks seen
         for (int t = unit; t < total; t += nunits) {
-            const Tile w = tile_at(C, t, tn);
+            const Tile w = tile_at(C, t, walk);
             const int K = contraction(w);
             const int kblocks = (K + BK - 1) / BK;
-            const Block b = kblocks ? block_of<FORM>(K, 0) : Block{0, 0};
-            if (is_ragged(b)) {
+            const Block b = kblocks ? block_of(w.weights, K, 0) : Block{0, 0};
+            if (is_ragged(w, b)) {
                 const int s = it % kStages;
                 if (!pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns)) break;
                 used ^= 1u << s;
@@ -311,27 +371,29 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     if (rank == 0) mbar_arrive(full0 + 8 * s);  // the stage's phase, in place of the loads' bytes
                 }
             }
-            it += kblocks;
+            it += steps_of(w, kblocks);
         }
     } else if (warp == kMmaWarp) {
         // =========================================================== MMA issuer
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = instr_desc<BF16, FORM>();
             // K-major: 8-row groups 1024 B apart; a K step of 16 elements is
             //    32 B along the row, the second atom 16 KB on.
             // MN-major: atoms of 64 columns 16 KB apart (leading offset), 8-row
             //    K groups 1024 B apart; a K step of 16 rows is 2 KB.
-            constexpr bool kAkm = FORM != kFormGradWeight, kBkm = FORM == kFormGradRows;
-            const uint64_t a_desc0 = smem_desc(base, kAkm ? 16 : kAtomBytes, 1024, kSwizzle128B);
-            const uint64_t b_desc0 = smem_desc(base + kTileBytes, kBkm ? 16 : kAtomBytes, 1024, kSwizzle128B);
+            const uint64_t a_km = smem_desc(base, 16, 1024, kSwizzle128B);
+            const uint64_t a_mn = smem_desc(base, kAtomBytes, 1024, kSwizzle128B);
+            const uint64_t to_b = kTileBytes >> 4;
             uint32_t it = 0, tl = 0, used = 0;
             bool ok = true;
             for (int t = unit; t < total && ok; t += nunits, ++tl) {
-                const Tile w = tile_at(C, t, tn);
+                const Tile w = tile_at(C, t, walk);
                 const int K = contraction(w);
-                const int kblocks = (K + BK - 1) / BK;
-                const int steps = FORM == kFormGradRows ? p.phases * kblocks : kblocks;
+                const int kblocks = (K + BK - 1) / BK, steps = steps_of(w, kblocks);
                 const int acc = tl & 1;
+                // A: MN-major for the weights' gradient only; B: K-major for the rows' gradient only.
+                const bool a_is_mn = GRAD && w.weights, b_is_mn = !GRAD || w.weights;
+                const uint32_t idesc = instr_desc<BF16>(a_is_mn, b_is_mn);
+                const uint64_t a_desc0 = a_is_mn ? a_mn : a_km, b_desc0 = (b_is_mn ? a_mn : a_km) + to_b;
                 if (!pair::wait_phase(&C.abort, smem_u32(&C.tempty[acc]), ((tl >> 1) & 1) ^ 1, p.status,
                                       p.wait_limit_ns))
                     break;
@@ -345,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    const Block b = block_of<FORM>(K, FORM == kFormGradRows && i >= kblocks ? i - kblocks : i);
-                    if (is_ragged(b)) {
+                    const Block b = block_of(w.weights, K, i >= kblocks ? i - kblocks : i);
+                    if (is_ragged(w, b)) {
                         if (!pair::wait_phase(&C.abort, cleared0 + 8 * s, (used >> s) & 1, p.status,
                                               p.wait_limit_ns)) {
                             ok = false;
@@ -362,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     for (int kk = 0; kk < BK / 16; ++kk) {
                         if (kk < ksteps) {
                             const uint32_t km = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4, mn = 128 * kk;
-                            pair::mma(d_tmem, ad0 + (kAkm ? km : mn), bd0 + (kBkm ? km : mn), idesc, (i | kk) != 0);
+                            pair::mma(d_tmem, ad0 + (a_is_mn ? mn : km), bd0 + (b_is_mn ? mn : km), idesc,
+                                      (i | kk) != 0);
                         }
                     }
                     pair::commit(empty0 + 8 * s);
@@ -377,23 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         const uint32_t tempty0 = pair::map_to_rank(smem_u32(&C.tempty[0]), 0);
         uint32_t tl = 0, nblk = 0;
         for (int t = unit; t < total; t += nunits, ++tl) {
-            const Tile w = tile_at(C, t, tn);
+            const Tile w = tile_at(C, t, walk);
             const int acc = tl & 1;
             if (!pair::wait_phase(&C.abort, smem_u32(&C.tfull[acc]), (tl >> 1) & 1, p.status, p.wait_limit_ns)) break;
             __syncwarp();
             tc_fence_after_sync();
             const GroupInfo gi = C.g[w.g];
             const int row0w = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;  // this warp's first row
-            const int rows = FORM == kFormGradWeight ? p.M : gi.rows;
+            const int rows = w.weights ? p.wM : gi.rows, N = w.weights ? p.wN : p.N;
             const bool valid = row0w + lane < rows;
             const bool all_rows = row0w + 32 <= rows;
             // Output row of this lane's row, and whether the warp's 32 rows are
             // consecutive there.
             int64_t orow = 0;
             bool together = all_rows;
-            if constexpr (FORM == kFormGradWeight) {
-                orow = static_cast<int64_t>(w.g) * p.M + row0w + lane;
-            } else if constexpr (FORM == kFormGated) {
+            if (w.weights) {
+                orow = static_cast<int64_t>(w.g) * p.wM + row0w + lane;
+            } else if constexpr (!GRAD) {
                 orow = gi.row0 + row0w + lane;
             } else {  // the gradient's rows go back to their order of arrival
                 int seg = 0;
@@ -403,18 +466,18 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 }
                 together = all_rows && __shfl_sync(0xffffffffu, seg, 0) == __shfl_sync(0xffffffffu, seg, 31);
             }
-            const bool zero = FORM == kFormGradWeight && gi.rows == 0;  // nothing was accumulated
+            const bool zero = w.weights && gi.rows == 0;  // nothing was accumulated
             const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kAccCols;
-            constexpr int kChunks = FORM == kFormGated ? 4 : 8;
+            constexpr int kChunks = GRAD ? 8 : 4;
             for (int c = 0; c < kChunks; ++c) {
-                const int half = FORM == kFormGated ? 0 : c >> 2;
-                const int col = (FORM == kFormGradRows ? w.n * 256 + c * 32
-                                                       : w.n * tile_n + half * p.half_step + (c & 3) * 32);
-                if (col >= p.N) continue;  // uniform
+                const int half = c >> 2;
+                const int col = !GRAD ? w.n * 128 + c * 32
+                                      : !w.weights ? w.n * 256 + c * 32 : w.n * w_n + half * p.half_step + (c & 3) * 32;
+                if (col >= N) continue;  // uniform
                 const uint32_t buf = stage + (nblk++ & 1u) * kEpiBufBytes;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_base + c * 32, r);
-                if constexpr (FORM == kFormGated) {
+                if constexpr (!GRAD) {
                     uint32_t u[32];
                     tmem_ld_32x32b_x32(t_base + 128 + c * 32, u);
                     tmem_ld_wait();
@@ -429,8 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        r[i] = __float_as_uint(act_value<ACT>(__uint_as_float(r[i])) * __uint_as_float(u[i]));
+                    for (int i = 0; i < 32; i += 2) {
+                        float a, b;
+                        split(mul2(act_value<ACT>(pair_of(__uint_as_float(r[i]), __uint_as_float(r[i + 1]))),
+                                   pair_of(__uint_as_float(u[i]), __uint_as_float(u[i + 1]))),
+                              a, b);
+                        r[i] = __float_as_uint(a);
+                        r[i + 1] = __float_as_uint(b);
+                    }
                 } else {
                     tmem_ld_wait();
                     if (zero) {
@@ -445,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     uint4 pk;
-                    pk.x = pack2f<BF16>(__uint_as_float(r[v * 8 + 0]), __uint_as_float(r[v * 8 + 1]));
-                    pk.y = pack2f<BF16>(__uint_as_float(r[v * 8 + 2]), __uint_as_float(r[v * 8 + 3]));
-                    pk.z = pack2f<BF16>(__uint_as_float(r[v * 8 + 4]), __uint_as_float(r[v * 8 + 5]));
-                    pk.w = pack2f<BF16>(__uint_as_float(r[v * 8 + 6]), __uint_as_float(r[v * 8 + 7]));
+                    pk.x = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 0]), __uint_as_float(r[v * 8 + 1])));
+                    pk.y = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 2]), __uint_as_float(r[v * 8 + 3])));
+                    pk.z = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 4]), __uint_as_float(r[v * 8 + 5])));
+                    pk.w = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 6]), __uint_as_float(r[v * 8 + 7])));
                     st_shared_v4(buf + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), pk);
                 }
                 if (together) {  // one TMA store; columns past N are clipped
@@ -456,20 +525,20 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&p.tmY[half], buf, col, y);
+                        tma_store_2d(w.weights ? &p.tmW[half] : &p.tmY, buf, col, y);
                         bulk_commit_group();
                     }
                 } else {
                     if (lane == 0) bulk_commit_group();  // an empty group keeps the count
                     __syncwarp();
                     const int v = lane & 3;
+                    uint16_t *out = static_cast<uint16_t *>(w.weights ? p.out_w[half] : p.out);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int rr = 8 * k + (lane >> 2);
                         const int64_t dst = __shfl_sync(0xffffffffu, orow, rr);
                         const uint4 val = ld_shared_v4(buf + rr * 64 + ((v ^ ((rr >> 1) & 3)) << 4));
-                        if (row0w + rr < rows && col + v * 8 < p.N)
-                            st_stream_v4(static_cast<uint16_t *>(p.out[half]) + dst * p.N + col + v * 8, val);
+                        if (row0w + rr < rows && col + v * 8 < N) st_stream_v4(out + dst * N + col + v * 8, val);
                     }
                 }
                 __syncwarp();
@@ -490,40 +559,20 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     }
 }
 
-template <bool BF16, int FORM, int ACT>
-cudaError_t launch_form(const ExpertGemmLaunch &p, cudaStream_t stream) {
-    auto kern = expert_gemm_kernel<BF16, FORM, ACT>;
-    cudaError_t err =
+template <bool BF16, bool GRAD, int ACT>
+cudaError_t launch_kind(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    auto kern = expert_gemm_kernel<BF16, GRAD, ACT>;
+    const cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
     if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.after ? 2 : 1;
-    err = cudaLaunchKernelEx(&cfg, kern, p);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    return launch_pdl(kern, p.grid, kThreads, kSmemBytes, 2, stream, p);
 }
 
 template <bool BF16>
 cudaError_t launch_type(const ExpertGemmLaunch &p, cudaStream_t stream) {
-    switch (p.form) {
-        case kFormGated:
-            return p.act == A2AV_ACT_SILU ? launch_form<BF16, kFormGated, A2AV_ACT_SILU>(p, stream)
-                                          : launch_form<BF16, kFormGated, A2AV_ACT_GELU_TANH>(p, stream);
-        case kFormGradRows: return launch_form<BF16, kFormGradRows, A2AV_ACT_SILU>(p, stream);
-        case kFormGradWeight: return launch_form<BF16, kFormGradWeight, A2AV_ACT_SILU>(p, stream);
-    }
-    return cudaErrorInvalidValue;
+    if (p.grad) return launch_kind<BF16, true, A2AV_ACT_SILU>(p, stream);
+    return p.act == A2AV_ACT_SILU ? launch_kind<BF16, false, A2AV_ACT_SILU>(p, stream)
+                                  : launch_kind<BF16, false, A2AV_ACT_GELU_TANH>(p, stream);
 }
 
 }  // namespace
@@ -532,26 +581,9 @@ cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream) {
     return p.bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
 }
 
-// Clusters resident at once; every form has the same shared memory and at most one CTA per SM.
+// Every kind has the same shared memory and at most one CTA an SM.
 int expert_gemm_max_clusters() {
-    auto kern = expert_gemm_kernel<true, kFormGated, A2AV_ACT_SILU>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes)) !=
-        cudaSuccess)
-        return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * 1024, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
-    return n;
+    return max_clusters(expert_gemm_kernel<true, false, A2AV_ACT_SILU>, kThreads, kSmemBytes, 2);
 }
 
 }  // namespace a2av

@@ -20,9 +20,9 @@ struct RmsNormLaunch {
     void *scales;
     float *rstd;
     float eps;
-    int32_t qtype;
 };
-cudaError_t launch_rms_norm(const RmsNormLaunch &p, bool bf16, int qmode, int sms, cudaStream_t stream);
+// kind: quant_kind() of the 8-bit output, or -1.
+cudaError_t launch_rms_norm(const RmsNormLaunch &p, bool bf16, int kind, int sms, cudaStream_t stream);
 
 struct RmsNormGradLaunch {
     int32_t rows, H;
@@ -45,49 +45,85 @@ struct GluLaunch {
     void *h;
     uint8_t *codes;
     void *scales;
-    int32_t qtype;
+    uint64_t inv64;  // set by the launch: 2^64 and 2^32 over N / 8, rounded up
+    uint32_t inv32;
 };
-cudaError_t launch_glu_quant(const GluLaunch &p, bool bf16, int act, int qmode, int sms, cudaStream_t stream);
+cudaError_t launch_glu_quant(GluLaunch p, bool bf16, int act, int kind, cudaStream_t stream);
 
-// dG = dh U act'(G), dU = dh act(G), element by element over n values.
+// Rows in the making for a GEMM that may run beside their kernel (stage.cu).
+// `pieces`: counts of finished pieces by 128 rows, zero at the start; NULL: not
+// counted (the GEMM waits for the whole kernel).
+
+// Expert-major copy of rank-major rows, in the order of the GEMM's 128-row
+// halves (counted from each expert's first row).
+struct StageRowsLaunch {
+    const int32_t *recvCounts;
+    int32_t W, e, A, H1;
+    const void *src;
+    void *dst;
+    int32_t *status;         // stored (0 or kStatusBadCounts)
+    int32_t only_straddling; // copy only the halves that straddle a run boundary
+    int32_t *pieces;         // by half; only halves that straddle are counted
+};
+int stage_rows_pieces(int64_t H1);  // pieces of a half
+cudaError_t launch_stage_rows(const StageRowsLaunch &p, int sms, cudaStream_t stream);
+
+// dG = dh U act'(G), dU = dh act(G) for [rows, N] values.
 struct GluGradLaunch {
-    int64_t n;  // multiple of 8
+    int32_t rows, N;
     const void *dh;
     const float *gate, *up;
     void *dgate, *dup;
+    int32_t *pieces;  // by block of 128 rows
 };
+int glu_grad_pieces(int64_t rows, int64_t N);  // pieces of a block of this many (up to 128) rows
 cudaError_t launch_glu_grad(const GluGradLaunch &p, bool bf16, int act, int sms, cudaStream_t stream);
 
-// The three products of a gated block or of a grouped product's gradient, as
-// one kernel over ragged expert groups (expert_gemm.cu).
-enum ExpertForm {
-    kFormGated = 0,      // h = act(X Wg) * (X Wu)
-    kFormGradRows = 1,   // dX = sum over p of D_p W_p^T
-    kFormGradWeight = 2  // dW = X^T D, contracted over an expert's rows
-};
-
+// The products of a gated block (grad 0) or the gradients of one or two
+// products over the same rows (grad 1), over ragged expert groups
+// (expert_gemm.cu).
 struct ExpertGemmLaunch {
     const int32_t *recvCounts;
     int32_t W, e, A;
-    int32_t K;           // contraction length (rows' gradient: of one phase; weights' gradient: unused)
-    int32_t phases;      // rows' gradient: products added into one accumulator (gated 2, plain 1)
-    int32_t M, N;        // weights' gradient: rows of dW; N: output columns
-    int32_t half_step;   // columns from a tile's first accumulator half to its second: 128 where both
-                         // halves belong to one matrix, 0 where the second half is another matrix
-    int32_t one_a, one_b;  // 1: a stage's operand is one TMA load (4-D map), 0: two (3-D map)
-    int32_t bf16, form, act;
+    int32_t bf16, grad, act;
+    // Tiles over the experts' rows: gated [A, N] = [A, K] x [K, N] twice;
+    // gradient [A, N] = sum over phases of [A, K] x [N, K]^T.  N 0: none.
+    int32_t K, N, phases;
+    int32_t one_a, one_b;   // 1: a stage's operand is one TMA load (4-D map), 0: two (3-D map)
+    int32_t direct_halves;  // gated: halves inside one segment are read in place from ataOut
+    // Tiles of the weights' gradients, [wM, wN] an expert = X^T D.  wM 0: none.
+    int32_t wM, wN;
+    int32_t one_x;
+    int32_t half_step;      // columns from a tile's first accumulator half to its second: 128 where both
+                            // halves belong to one matrix, 0 where the second half is another matrix
+    const int32_t *pieces;  // rows of A in the making beside this kernel, by 128 (NULL: all there)
+    int32_t row_pieces, last_pieces;  // of 128 rows; of the last block of A (gradient)
     int32_t *status;
     int32_t write_status;
-    int32_t direct_halves;  // gated: halves inside one segment are read in place from ataOut
-    int32_t after;          // launched beside the kernel before it (programmatic dependent launch)
     int32_t grid;           // CTAs, two a cluster
     uint64_t wait_limit_ns;
-    void *out[2];           // by accumulator half
+    void *out, *out_w[2];   // over the rows; weights' gradients by accumulator half
     float *saved[2];        // gated: unrounded G and U, or NULL
-    CUtensorMap tmA[2], tmB[2], tmY[2];
+    CUtensorMap tmA[2], tmB[2], tmX, tmY, tmW[2];
     CUtensorMap tmDirect;
 };
 cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream);
 int expert_gemm_max_clusters();
+
+// The gated block for a few rows (gated_rows.cu).
+struct GatedRowsLaunch {
+    const int32_t *recvCounts;
+    int32_t W, e, A, K, N;
+    void *h;
+    float *saved[2];
+    int32_t *status;
+    uint64_t wait_limit_ns;
+    int32_t split, grid;  // set by the launch: CTAs of a cluster, CTAs
+    const void *x;            // ataOut
+    CUtensorMap tmGate, tmUp; // [e][K][N], box 64 columns x 128 k
+};
+// Rows the fullest of e experts is expected to have when A rows spread at random.
+double gated_rows_most(int64_t A, int32_t e);
+cudaError_t launch_gated_rows(GatedRowsLaunch p, bool bf16, int act, cudaStream_t stream);
 
 }  // namespace a2av

@@ -8,8 +8,8 @@
 
 #include "a2av_ffn.h"
 #include "ffn.h"
-#include "kernels.h"
 #include "plan.cuh"
+#include "quantise.cuh"
 
 namespace {
 
@@ -18,7 +18,6 @@ using a2av::ExpertGemmLaunch;
 constexpr size_t kStatusBytes = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
 constexpr int kMaxDevices = 64;
-
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
@@ -53,6 +52,10 @@ a2av_status check_quant(int32_t qtype, int32_t qmode, int64_t cols) {
     if (qmode == A2AV_QMODE_MX && qtype == A2AV_Q_INT8) return A2AV_ERR_INVALID;
     if (cols % (qmode == A2AV_QMODE_MX ? 32 : 128) != 0) return A2AV_ERR_INVALID;
     return A2AV_OK;
+}
+
+int kind_of(int32_t qtype, int32_t qmode) {
+    return qtype == A2AV_Q_NONE ? a2av::kQuantNone : a2av::quant_kind(qmode, qtype);
 }
 
 a2av_status check_quant_out(int32_t qtype, int32_t qmode, const void *codes, const void *scales, bool rows) {
@@ -142,53 +145,41 @@ ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, con
     return g;
 }
 
-// Gradients of one or two products with the same rows: dX = sum_p D_p W_p^T,
-// dW_p = X^T D_p.  `status` is stored by the first kernel.
+// Gradients of one or two products with the same rows, in one launch:
+// dX = sum_p D_p W_p^T, dW_p = X^T D_p.
 a2av_status run_gradients(ExpertGemmLaunch g, int phases, int64_t H1, int64_t N, const void *const D[2],
                           const void *X, const void *const Wt[2], void *dX, void *const dW[2], cudaStream_t stream) {
     const bool bf16 = g.bf16 != 0;
-    const bool one_n = N % 64 == 0, one_h = H1 % 64 == 0;
+    g.grad = 1;
+    g.phases = phases;
+    g.half_step = phases == 2 ? 0 : 128;
+    g.one_a = g.one_b = N % 64 == 0;
+    g.one_x = H1 % 64 == 0;
+    for (int p = 0; p < phases && g.A > 0; ++p)
+        if (!operand_map(&g.tmA[p], D[p], 1, g.A, N, bf16, g.one_a)) return A2AV_ERR_CUDA;
+    int64_t tiles = 0;
     if (dX && g.A > 0) {
-        ExpertGemmLaunch r = g;
-        r.form = a2av::kFormGradRows;
-        r.phases = phases;
-        r.K = static_cast<int32_t>(N);
-        r.N = static_cast<int32_t>(H1);
-        r.half_step = 128;
-        r.one_a = r.one_b = one_n;
-        for (int i = 0; i < 2; ++i) {
-            const int p = phases == 2 ? i : 0;
-            if (!operand_map(&r.tmA[i], D[p], 1, g.A, N, bf16, one_n) ||
-                !operand_map(&r.tmB[i], Wt[p], g.e, H1, N, bf16, one_n) ||
-                !output_map(&r.tmY[i], dX, g.A, H1, bf16))
-                return A2AV_ERR_CUDA;
-            r.out[i] = dX;
-        }
-        r.grid = gemm_grid((ceil_div(g.A, 256) + g.e) * ceil_div(H1, 256));
-        if (a2av::launch_expert_gemm(r, stream) != cudaSuccess) return A2AV_ERR_CUDA;
-        g.write_status = 0;
+        g.K = static_cast<int32_t>(N);
+        g.N = static_cast<int32_t>(H1);
+        g.out = dX;
+        for (int p = 0; p < phases; ++p)
+            if (!operand_map(&g.tmB[p], Wt[p], g.e, H1, N, bf16, g.one_b)) return A2AV_ERR_CUDA;
+        if (!output_map(&g.tmY, dX, g.A, H1, bf16)) return A2AV_ERR_CUDA;
+        tiles += (ceil_div(g.A, 256) + g.e) * ceil_div(H1, 256);
     }
     if (dW[0]) {
-        ExpertGemmLaunch w = g;
-        w.form = a2av::kFormGradWeight;
-        w.M = static_cast<int32_t>(H1);
-        w.N = static_cast<int32_t>(N);
-        w.half_step = phases == 2 ? 0 : 128;
-        w.one_a = one_h;
-        w.one_b = one_n;
-        for (int i = 0; i < 2; ++i) {
-            const int p = phases == 2 ? i : 0;
-            // Without rows nothing is loaded; the maps still have to be valid.
-            if (g.A > 0 && (!operand_map(&w.tmA[i], X, 1, g.A, H1, bf16, one_h) ||
-                            !operand_map(&w.tmB[i], D[p], 1, g.A, N, bf16, one_n)))
-                return A2AV_ERR_CUDA;
-            if (!output_map(&w.tmY[i], dW[p], g.e * H1, N, bf16)) return A2AV_ERR_CUDA;
-            w.out[i] = dW[p];
+        g.wM = static_cast<int32_t>(H1);
+        g.wN = static_cast<int32_t>(N);
+        for (int i = 0; i < 2; ++i) {  // by accumulator half
+            g.out_w[i] = dW[phases == 2 ? i : 0];
+            if (!output_map(&g.tmW[i], g.out_w[i], g.e * H1, N, bf16)) return A2AV_ERR_CUDA;
         }
-        w.grid = gemm_grid(g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? 128 : 256));
-        if (a2av::launch_expert_gemm(w, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        if (g.A > 0 && !operand_map(&g.tmX, X, 1, g.A, H1, bf16, g.one_x)) return A2AV_ERR_CUDA;
+        tiles += g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? 128 : 256);
     }
-    return A2AV_OK;
+    if (tiles == 0) return A2AV_OK;
+    g.grid = gemm_grid(tiles);
+    return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 
 a2av_status validate(const a2av_gated_desc *d) {
@@ -206,8 +197,25 @@ a2av_status validate(const a2av_gated_desc *d) {
     return A2AV_OK;
 }
 
+// Whether the weight-streaming kernel (gated_rows.cu) takes a forward call: the
+// rows its fullest expert is expected to have fit one pass over the weights, or
+// two where the tile kernel would leave half of the SMs without a tile.
+// Measured (us, streaming / tiles), rows an expert: 4 experts of 4096 x 1024,
+// 16: 21 / 42, 32: 24 / 39, 64 (two passes): 31 / 38, 128: 42 / 39; one expert
+// of 7168 x 2048, 16: 17 / 43, 64: 20 / 43, 128: 28 / 43, 256: 45 / 43; 16
+// experts of 2048 x 1408, 32: 51 / 59, 64: 69 / 55.
+bool few_rows(const a2av_gated_desc &d) {
+    if (d.A == 0 || d.want_permute_out) return false;
+    const double most = a2av::gated_rows_most(d.A, d.e);
+    return most <= 64.0 || (most <= 128.0 && d.H1 >= 4096 && d.e * ((d.N + 127) / 128) < 40);
+}
+
 size_t staged_bytes(const a2av_gated_desc *d) {
     return d->W > 1 && !d->want_permute_out ? round256(static_cast<size_t>(d->A) * d->H1 * 2) : 0;
+}
+// Counts of finished pieces, by 128 rows of each expert or of all.
+size_t pieces_bytes(const a2av_gated_desc *d) {
+    return (d->W > 1 || d->save) && d->A > 0 ? round256((static_cast<size_t>(d->A) / 128 + d->e + 1) * 4) : 0;
 }
 size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
     return d->save ? round256(static_cast<size_t>(d->A) * d->N * 2) : 0;
@@ -238,8 +246,8 @@ a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const v
     const int sms = sm_count();
     if (sms <= 0) return A2AV_ERR_CUDA;
     a2av::RmsNormLaunch p{static_cast<int32_t>(d.rows), static_cast<int32_t>(d.H), d.x_stride, d.residual_stride, x,
-                          residual, gamma, h, y, static_cast<uint8_t *>(codes), scales, rstd, d.eps, d.qtype};
-    return a2av::launch_rms_norm(p, d.dtype == A2AV_BF16, d.qtype == A2AV_Q_NONE ? A2AV_Q_NONE : d.qmode, sms,
+                          residual, gamma, h, y, static_cast<uint8_t *>(codes), scales, rstd, d.eps};
+    return a2av::launch_rms_norm(p, d.dtype == A2AV_BF16, kind_of(d.qtype, d.qmode), sms,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? A2AV_OK
                : A2AV_ERR_CUDA;
@@ -290,11 +298,9 @@ a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const vo
     if (qo != A2AV_OK) return qo;
     if (!aligned(gate, 16) || !aligned(up, 16) || !aligned(h, 16)) return A2AV_ERR_UNSUPPORTED;
     if (d.rows == 0) return A2AV_OK;
-    const int sms = sm_count();
-    if (sms <= 0) return A2AV_ERR_CUDA;
     a2av::GluLaunch p{d.rows, static_cast<int32_t>(d.N), d.stride, gate, up, h, static_cast<uint8_t *>(codes), scales,
-                      d.qtype};
-    return a2av::launch_glu_quant(p, d.dtype == A2AV_BF16, d.act, d.qtype == A2AV_Q_NONE ? A2AV_Q_NONE : d.qmode, sms,
+                      0, 0};
+    return a2av::launch_glu_quant(p, d.dtype == A2AV_BF16, d.act, kind_of(d.qtype, d.qmode),
                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? A2AV_OK
                : A2AV_ERR_CUDA;
@@ -304,7 +310,7 @@ a2av_status a2av_gated_workspace_size(const a2av_gated_desc *desc, size_t *bytes
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + std::max(staged_bytes(desc), 2 * slope_bytes(desc));
+    *bytes = kStatusBytes + pieces_bytes(desc) + std::max(staged_bytes(desc), 2 * slope_bytes(desc));
     return A2AV_OK;
 }
 
@@ -328,9 +334,31 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     const int sms = sm_count();
     if (sms <= 0) return A2AV_ERR_CUDA;
 
+    if (few_rows(d)) {
+        const bool bf16 = d.dtype == A2AV_BF16;
+        a2av::GatedRowsLaunch r;
+        std::memset(&r, 0, sizeof r);
+        r.recvCounts = recvCounts;
+        r.W = d.W;
+        r.e = d.e;
+        r.A = static_cast<int32_t>(d.A);
+        r.K = static_cast<int32_t>(d.H1);
+        r.N = static_cast<int32_t>(d.N);
+        r.h = h;
+        if (d.save) {
+            r.saved[0] = saved;
+            r.saved[1] = saved + d.A * d.N;
+        }
+        r.status = static_cast<int32_t *>(workspace);
+        r.wait_limit_ns = kWaitLimitNs;
+        r.x = ataOut;
+        if (!operand_map(&r.tmGate, gateWeight, d.e, d.H1, d.N, bf16, false) ||
+            !operand_map(&r.tmUp, upWeight, d.e, d.H1, d.N, bf16, false))
+            return A2AV_ERR_CUDA;
+        return a2av::launch_gated_rows(r, bf16, d.act, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
+    }
     ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
     const bool bf16 = g.bf16 != 0;
-    g.form = a2av::kFormGated;
     g.act = d.act;
     g.K = static_cast<int32_t>(d.H1);
     g.N = static_cast<int32_t>(d.N);
@@ -340,23 +368,28 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     if (d.W > 1 && d.A > 0) {
         // Expert-major rows: all of them in permuteOut, or in the workspace
         // those 128-row halves of a tile that straddle a (source, expert) run
-        // boundary, the others being read in place.
-        void *dst = d.want_permute_out ? permuteOut : static_cast<uint8_t *>(workspace) + kStatusBytes;
-        g.direct_halves = d.want_permute_out ? 0 : 1;
-        a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, g.direct_halves, 8};
-        if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        // boundary; the GEMM reads the other halves in place either way.
+        uint8_t *ws = static_cast<uint8_t *>(workspace) + kStatusBytes;
+        void *dst = d.want_permute_out ? permuteOut : ws + pieces_bytes(desc);
+        int32_t *pieces = reinterpret_cast<int32_t *>(ws);
+        if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        a2av::StageRowsLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status,
+                                 d.want_permute_out ? 0 : 1, pieces};
+        if (a2av::launch_stage_rows(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        g.pieces = pieces;
+        g.row_pieces = a2av::stage_rows_pieces(d.H1);
+        g.direct_halves = 1;
         g.write_status = 0;
-        g.after = 1;
         rows = dst;
-        if (g.direct_halves && !operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
+        if (!operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
     }
     if (d.A > 0) {
         if (!operand_map(&g.tmA[0], rows, 1, d.A, d.H1, bf16, g.one_a) ||
             !operand_map(&g.tmB[0], gateWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
             !operand_map(&g.tmB[1], upWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
-            !output_map(&g.tmY[0], h, d.A, d.N, bf16))
+            !output_map(&g.tmY, h, d.A, d.N, bf16))
             return A2AV_ERR_CUDA;
-        g.out[0] = h;
+        g.out = h;
         if (d.save) {
             g.saved[0] = saved;
             g.saved[1] = saved + static_cast<size_t>(d.A) * d.N;
@@ -389,12 +422,16 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
     if (sms <= 0) return A2AV_ERR_CUDA;
 
     ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
-    uint8_t *slopes = static_cast<uint8_t *>(workspace) + kStatusBytes;
+    uint8_t *slopes = static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
     void *const dG = slopes, *const dU = slopes + slope_bytes(desc);
-    const int64_t n = d.A * d.N;
-    if (n > 0) {
-        a2av::GluGradLaunch s{n, dh, saved, saved + n, dG, dU};
+    if (d.A > 0) {
+        int32_t *pieces = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+        if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        a2av::GluGradLaunch s{g.A, static_cast<int32_t>(d.N), dh, saved, saved + d.A * d.N, dG, dU, pieces};
         if (a2av::launch_glu_grad(s, g.bf16, d.act, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        g.pieces = pieces;
+        g.row_pieces = a2av::glu_grad_pieces(128, d.N);
+        g.last_pieces = a2av::glu_grad_pieces(d.A % 128, d.N);
     }
     const void *const D[2] = {dG, dU}, *const Wt[2] = {gateWeight, upWeight};
     void *const dW[2] = {dGate, dUp};

@@ -47,7 +47,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
 // Bounded wait on an mbarrier phase, acquiring at cluster scope (arrivals may
 // come from the peer CTA).  False: gave up, or another role did; the abort
 // flag and the status word are set.
-__device__ __noinline__ bool wait_phase(int32_t *abort_flag, uint32_t bar, uint32_t parity, int32_t *status,
+static __device__ __noinline__ bool wait_phase(int32_t *abort_flag, uint32_t bar, uint32_t parity, int32_t *status,
                                         uint64_t limit_ns) {
     if (try_wait_cluster(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();

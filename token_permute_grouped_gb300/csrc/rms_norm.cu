@@ -11,6 +11,7 @@
 
 #include "activation.cuh"
 #include "ffn.h"
+#include "pdl.cuh"
 #include "quantise.cuh"
 
 namespace a2av {
@@ -26,176 +27,293 @@ __device__ __forceinline__ uint4 ld_once(const uint4 *p) {
     return v;
 }
 
-// Sum over the block, the same in every thread.  `slots` alternates between
-// two sets of 32 floats so that one barrier a sum is enough.
-__device__ __forceinline__ float block_sum(float v, float *slots) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
-    if (warps == 1) return v;
-    if (lane == 0) slots[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = lane < warps ? slots[lane] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+// Sum over a row's threads, the same in every thread.  `slots` alternates
+// between two sets so that one barrier a sum is enough; `bar` is the named
+// barrier of the row's threads.  Partial sums are added with the rounding
+// error carried along (two-sum), which leaves the error of the threads' own
+// short sums, averaged over the row.
+__device__ __forceinline__ void two_sum(float &hi, float &lo, float b_hi, float b_lo) {
+    const float s = hi + b_hi, z = s - hi;
+    lo += b_lo + ((hi - (s - z)) + (b_hi - z));
+    hi = s;
 }
 
-// VPT: vectors of 8 values a thread holds.  MODE: a2av_qmode or kQuantNone.
-template <bool BF16, int VPT, int MODE>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const RmsNormLaunch p) {
-    __shared__ float slots[2][32];
+__device__ __forceinline__ float2 row_sum(float v, float2 *slots, int t, int threads, int bar) {
+    float lo = 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        two_sum(v, lo, __shfl_xor_sync(0xffffffffu, v, off), __shfl_xor_sync(0xffffffffu, lo, off));
+    const int warps = threads / 32, lane = t % 32;
+    if (warps > 1) {
+        if (lane == 0) slots[t / 32] = make_float2(v, lo);
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+        const float2 w = lane < warps ? slots[lane] : make_float2(0.0f, 0.0f);
+        v = w.x;
+        lo = w.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            two_sum(v, lo, __shfl_xor_sync(0xffffffffu, v, off), __shfl_xor_sync(0xffffffffu, lo, off));
+    }
+    return make_float2(v, fabsf(v) < __uint_as_float(0x7f800000u) ? lo : 0.0f);  // (an infinite sum's error is a NaN)
+}
+
+// 1 / sqrt(v): one Newton step on the hardware's reciprocal root, and in `lo`
+// what the next step would add.
+__device__ __forceinline__ float inv_sqrt(float v, float &lo) {
+    float r = rsqrtf(v);
+    lo = 0.0f;
+    if (v > 0.0f && v < __uint_as_float(0x7f800000u)) {
+        r = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+        const float q = v * r, e = fmaf(v, r, -q);  // v r^2 = (q + e) r
+        lo = -0.5f * r * (fmaf(q, r, -1.0f) + e * r);
+    }
+    return r;
+}
+
+// VPT: vectors of 8 values a thread holds.  KIND: the 8-bit output.  MAXT:
+// threads at most.  A block that walks several rows requests the next one's
+// values before it reduces the current row (up to two vectors a thread; more
+// would not leave registers for it).
+template <bool BF16, int VPT, int KIND, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_kernel(const RmsNormLaunch p) {
+    using Q = Quant<KIND>;
+    constexpr bool PRE = VPT <= 2;
+    __shared__ float2 slots[2][32];
     const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x;
     const uint4 *gamma = static_cast<const uint4 *>(p.gamma);
-    int flip = 0;
-    for (int row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    uint4 raw[VPT], res[VPT];
+    const auto load = [&](int row) {
         const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + row * p.x_stride);
-        const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + row * p.r_stride);
-        const size_t out0 = static_cast<size_t>(row) * vecs;
-        uint4 raw[VPT], res[VPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
             if (t + k * T < vecs) raw[k] = ld_once(x + t + k * T);
         if (p.residual) {
+            const uint4 *r =
+                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + row * p.r_stride);
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
                 if (t + k * T < vecs) res[k] = ld_once(r + t + k * T);
         }
-        float s[VPT][8];
-        float sum = 0.0f;
+    };
+    int flip = 0;
+    pdl_trigger();
+    pdl_wait();
+    if (PRE) load(blockIdx.x);
+    for (int row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+        const size_t out0 = static_cast<size_t>(row) * vecs;
+        if (!PRE) load(row);
+        f32x2 s[VPT][4];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[k][i] = 0;
             if (t + k * T < vecs) {
                 unpack8<BF16>(raw[k], s[k]);
                 if (p.residual) {
-                    float f[8];
+                    f32x2 f[4];
                     unpack8<BF16>(res[k], f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[k][i] += f[i];
+                    for (int i = 0; i < 4; ++i) s[k][i] = add2(s[k][i], f[i]);
                 }
-                if (p.h) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[k][i] = 0.0f;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += s[k][i] * s[k][i];
         }
-        sum = block_sum(sum, slots[flip]);
-        const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+        if (PRE && row + static_cast<int>(gridDim.x) < p.rows) load(row + gridDim.x);
+        f32x2 sum2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (p.h && t + k * T < vecs) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum2 = fma2(s[k][i], s[k][i], sum2);
+        }
+        float sum, odd;
+        split(sum2, sum, odd);
+        const float2 total = row_sum(sum + odd, slots[flip], t, T, 0);
+        const float mean = (total.x + total.y) / static_cast<float>(p.H) + p.eps;
+        float rstd_lo;
+        const float rstd = inv_sqrt(mean, rstd_lo);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
-        if (MODE == kQuantNone && !p.y) continue;
+        if (!Q::kAny && !p.y) continue;
+        f32x2 y[VPT][4];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = t + k * T;
-            float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[k][i] = 0;
             if (v < vecs) {
-                float g[8];
+                f32x2 g[4];
                 unpack8<BF16>(__ldg(gamma + v), g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = s[k][i] * rstd * g[i];
-                if (p.y) static_cast<uint4 *>(p.y)[out0 + v] = pack8<BF16>(y);
+                for (int i = 0; i < 4; ++i) y[k][i] = mul2(mul2(s[k][i], both(rstd)), g[i]);
+                if (p.y) static_cast<uint4 *>(p.y)[out0 + v] = pack8<BF16>(y[k]);
             }
-            if constexpr (MODE != kQuantNone) {
-                uint8_t e8m0 = 0;
-                float scale = 0.0f;
-                const uint2 c = quantise8<MODE>(y, p.qtype, &e8m0, &scale);
-                if (v < vecs) {
-                    reinterpret_cast<uint2 *>(p.codes)[out0 + v] = c;
-                    constexpr int kLanes = MODE == A2AV_QMODE_MX ? 4 : 16;
-                    if (v % kLanes == 0) {
-                        if constexpr (MODE == A2AV_QMODE_MX)
-                            static_cast<uint8_t *>(p.scales)[(out0 + v) / kLanes] = e8m0;
-                        else
-                            static_cast<float *>(p.scales)[(out0 + v) / kLanes] = scale;
+        }
+        if constexpr (Q::kAny) {
+            // y's two roundings and rstd's, each with its error: |y| - pw is
+            // exact for the values in question.
+            const auto reaches = [&](int k, float pw) {
+                const int v = t + k * T;
+                if (v >= vecs) return false;
+                f32x2 g2[4];
+                unpack8<BF16>(__ldg(gamma + v), g2);
+                bool hit = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a[2], g[2], z[2];
+                    split(s[k][i], a[0], a[1]);
+                    split(g2[i], g[0], g[1]);
+                    split(y[k][i], z[0], z[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float q = a[j] * rstd, r = fmaf(a[j], rstd, -q);
+                        const float err = fmaf(q, g[j], -z[j]) + (r + a[j] * rstd_lo) * g[j];
+                        hit |= fabsf(z[j]) - pw + copysignf(1.0f, z[j]) * err >= 0.0f;
                     }
                 }
-            }
+                return hit;
+            };
+            quantise<KIND, VPT>(y, reaches, [&](int k, uint2 codes, uint8_t e8m0, float scale) {
+                const int v = t + k * T;
+                if (v >= vecs) return;
+                reinterpret_cast<uint2 *>(p.codes)[out0 + v] = codes;
+                if (v % Q::kLanes == 0) {
+                    if constexpr (Q::kMx) static_cast<uint8_t *>(p.scales)[(out0 + v) / Q::kLanes] = e8m0;
+                    else static_cast<float *>(p.scales)[(out0 + v) / Q::kLanes] = scale;
+                }
+            });
         }
     }
 }
 
-template <bool BF16, int VPT>
-cudaError_t launch_norm_vpt(const RmsNormLaunch &p, int qmode, int threads, int grid, cudaStream_t stream) {
-    if (qmode == kQuantNone) rms_norm_kernel<BF16, VPT, kQuantNone><<<grid, threads, 0, stream>>>(p);
-    else if (qmode == A2AV_QMODE_MX) rms_norm_kernel<BF16, VPT, A2AV_QMODE_MX><<<grid, threads, 0, stream>>>(p);
-    else rms_norm_kernel<BF16, VPT, A2AV_QMODE_GROUP128><<<grid, threads, 0, stream>>>(p);
-    return cudaGetLastError();
+template <bool BF16, int VPT, int MAXT>
+cudaError_t launch_norm_vpt(const RmsNormLaunch &p, int kind, int threads, int grid, cudaStream_t stream) {
+    switch (kind) {
+#define A2AV_KIND(...)                                                                             \
+    case __VA_ARGS__:                                                                              \
+        return launch_pdl(rms_norm_kernel<BF16, VPT, __VA_ARGS__, MAXT>, grid, threads, 0, 0, stream, p)
+        A2AV_KIND(kQuantNone);
+        A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E4M3FN));
+        A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E5M2));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_E4M3FN));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_E5M2));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_INT8));
+#undef A2AV_KIND
+    }
+    return cudaErrorInvalidValue;
 }
 
 // Threads for `vecs` vectors at VPT each: whole warps.
 int threads_for(int vecs, int vpt) { return ((vecs + vpt - 1) / vpt + 31) / 32 * 32; }
 
-// A block walks rows, keeping its share of dgamma in registers; the shares go
-// to partial[block] and a second kernel adds them in block order.
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(1024) rms_norm_grad_kernel(const RmsNormGradLaunch p) {
-    __shared__ float slots[2][32];
-    const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x;
+// A block holds R rows at a time (blockDim = T x R), each walked on by its own
+// T threads, which keep their share of dgamma in registers; at the end the
+// block adds its rows' shares in order and stores one row of partial sums, and
+// a second kernel adds those in block order.
+template <bool BF16, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLaunch p) {
+    constexpr bool PRE = VPT <= 2;
+    __shared__ float2 slots[2][32];
+    extern __shared__ float4 share[];
+    const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x, R = blockDim.y, g = threadIdx.y;
     const uint4 *gamma = static_cast<const uint4 *>(p.gamma);
-    float dg[VPT][8];
+    f32x2 dg[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[k][i] = 0.0f;
-    int flip = 0;
-    for (int row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+        for (int i = 0; i < 4; ++i) dg[k][i] = 0;
+    uint4 a[VPT], n[VPT], d[VPT], na[VPT], nn[VPT], nd[VPT];  // dy, h, dh of this row and of the next
+    float rstd = 0.0f, nrstd = 0.0f;
+    const auto load = [&](int row, uint4 (&ra)[VPT], uint4 (&rn)[VPT], uint4 (&rd)[VPT], float &rs) {
         const size_t r0 = static_cast<size_t>(row) * vecs;
-        const uint4 *dy = static_cast<const uint4 *>(p.dy) + r0, *h = static_cast<const uint4 *>(p.h) + r0;
-        const float rstd = __ldg(p.rstd + row);
-        uint4 a[VPT], n[VPT], d[VPT];
+        rs = __ldg(p.rstd + row);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = t + k * T;
-            a[k] = n[k] = d[k] = make_uint4(0, 0, 0, 0);
             if (v < vecs) {
-                a[k] = ld_once(dy + v);
-                n[k] = ld_once(h + v);
-                if (p.dh) d[k] = ld_once(static_cast<const uint4 *>(p.dh) + r0 + v);
+                ra[k] = ld_once(static_cast<const uint4 *>(p.dy) + r0 + v);
+                rn[k] = ld_once(static_cast<const uint4 *>(p.h) + r0 + v);
+                if (p.dh) rd[k] = ld_once(static_cast<const uint4 *>(p.dh) + r0 + v);
             }
         }
-        float dot = 0.0f;
+    };
+    int flip = 0;
+    const int step = gridDim.x * R;
+    int row = blockIdx.x * R + g;
+    pdl_wait();
+    if (PRE && row < p.rows) load(row, na, nn, nd, nrstd);
+    for (; row < p.rows; row += step, flip ^= 1) {
+        const size_t r0 = static_cast<size_t>(row) * vecs;
+        if (PRE) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) a[k] = na[k], n[k] = nn[k], d[k] = nd[k];
+            rstd = nrstd;
+            if (row + step < p.rows) load(row + step, na, nn, nd, nrstd);
+        } else {
+            load(row, a, n, d, rstd);
+        }
+        f32x2 dot2 = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = t + k * T;
             if (v < vecs) {
-                float fa[8], fn[8], g[8];
+                f32x2 fa[4], fn[4], gm[4];
                 unpack8<BF16>(a[k], fa);
                 unpack8<BF16>(n[k], fn);
-                unpack8<BF16>(__ldg(gamma + v), g);
+                unpack8<BF16>(__ldg(gamma + v), gm);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = fa[i] * (fn[i] * rstd);
-                    dg[k][i] += u;
-                    dot += u * g[i];
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 u = mul2(fa[i], mul2(fn[i], both(rstd)));
+                    dg[k][i] = add2(dg[k][i], u);
+                    dot2 = fma2(u, gm[i], dot2);
                 }
             }
         }
-        dot = block_sum(dot, slots[flip]) / static_cast<float>(p.H);
+        float dot, odd;
+        split(dot2, dot, odd);
+        const float2 total = row_sum(dot + odd, slots[flip] + g * (T / 32), t, T, 1 + g);
+        // dx = dh + rstd (a - n m) = dh + dy gamma rstd - h (rstd^2 m)
+        const float m = (total.x + total.y) / static_cast<float>(p.H);
+        const f32x2 c1 = both(rstd), c2 = both(-rstd * rstd * m);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = t + k * T;
             if (v < vecs) {
-                float fa[8], fn[8], g[8], o[8];
+                f32x2 fa[4], fn[4], gm[4], o[4] = {0, 0, 0, 0};
                 unpack8<BF16>(a[k], fa);
                 unpack8<BF16>(n[k], fn);
-                unpack8<BF16>(__ldg(gamma + v), g);
-                unpack8<BF16>(d[k], o);
+                unpack8<BF16>(__ldg(gamma + v), gm);
+                if (p.dh) unpack8<BF16>(d[k], o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += rstd * (fa[i] * g[i] - fn[i] * rstd * dot);
+                for (int i = 0; i < 4; ++i) o[i] = add2(o[i], fma2(mul2(fa[i], gm[i]), c1, mul2(fn[i], c2)));
                 static_cast<uint4 *>(p.dx)[r0 + v] = pack8<BF16>(o);
             }
         }
     }
+    pdl_trigger();  // the sum over the blocks may be launched; it waits for this grid's end
     if (!p.dgamma) return;
+    float4 *out = reinterpret_cast<float4 *>(p.partial + static_cast<size_t>(blockIdx.x) * p.H);
+    for (int turn = 0; turn < R; ++turn) {
+        if (turn == g) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int v = t + k * T;
-        if (v < vecs) {
-            float4 *out = reinterpret_cast<float4 *>(p.partial + static_cast<size_t>(blockIdx.x) * p.H) + 2 * v;
-            out[0] = make_float4(dg[k][0], dg[k][1], dg[k][2], dg[k][3]);
-            out[1] = make_float4(dg[k][4], dg[k][5], dg[k][6], dg[k][7]);
+            for (int k = 0; k < VPT; ++k) {
+                const int v = t + k * T;
+                if (v < vecs) {
+                    float4 lo, hi;
+                    split(dg[k][0], lo.x, lo.y);
+                    split(dg[k][1], lo.z, lo.w);
+                    split(dg[k][2], hi.x, hi.y);
+                    split(dg[k][3], hi.z, hi.w);
+                    if (turn > 0) {
+                        const float4 l = share[2 * v], h = share[2 * v + 1];
+                        lo = make_float4(l.x + lo.x, l.y + lo.y, l.z + lo.z, l.w + lo.w);
+                        hi = make_float4(h.x + hi.x, h.y + hi.y, h.z + hi.z, h.w + hi.w);
+                    }
+                    float4 *to = turn == R - 1 ? out : share;
+                    to[2 * v] = lo;
+                    to[2 * v + 1] = hi;
+                }
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -205,6 +323,8 @@ constexpr int kSlices = 16;
 __global__ void __launch_bounds__(32 * kSlices) dgamma_sum_kernel(const float *__restrict__ partial, int blocks, int H,
                                                                   float *__restrict__ dgamma) {
     __shared__ float s[kSlices][33];
+    pdl_trigger();
+    pdl_wait();  // the partial sums are visible
     const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
     const int c = blockIdx.x * 32 + lane;
     float sum = 0.0f;
@@ -218,52 +338,76 @@ __global__ void __launch_bounds__(32 * kSlices) dgamma_sum_kernel(const float *_
     }
 }
 
-constexpr int kGradBlocks = 608;
+// One block of 512 threads an SM, with the next row's three vectors requested
+// while a row is reduced: 16,384 x 2048 bf16 rows take 47 us (5.7 TB/s), two
+// blocks without the early request 52, two of 256 threads with it 51 (and
+// twice the partial sums).
+constexpr int kGradBlocks = 152;
+constexpr int kGradThreads = 512;
+
+// Resident threads an SM that the norm's grid is made for: its 64 registers a
+// thread allow 1024.  Two vectors a thread: 12,288 x 7168 bf16 rows to E4M3FN
+// codes take 98 us (6.3 TB/s, 93 % of the copy rate); without the next row's
+// early request 118, four vectors 104, one 127.
+constexpr int kNormThreadsPerSm = 1024;
+
+struct GradShape {
+    int vpt, threads, rows;  // vectors a thread, threads a row, rows a block
+};
+GradShape grad_shape(int64_t H) {
+    const int vecs = static_cast<int>(H / 8);
+    int vpt = 2;
+    while (vpt < 8 && threads_for(vecs, vpt) > (vpt == 2 ? 512 : 1024)) vpt *= 2;
+    const int threads = threads_for(vecs, vpt);
+    // (the shares of dgamma of a block with several rows meet in at most 32 KB)
+    return {vpt, threads, std::max(1, std::min(kGradThreads / threads, 8))};
+}
+
+template <bool BF16>
+cudaError_t launch_norm_type(const RmsNormLaunch &p, int kind, int sms, cudaStream_t stream) {
+    const int vecs = p.H / 8;
+    const auto go = [&](auto launch, int vpt) {
+        const int threads = threads_for(vecs, vpt);
+        return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, kNormThreadsPerSm / threads)), stream);
+    };
+    if (p.rows <= sms && vecs <= 1024) return go(launch_norm_vpt<BF16, 1, 1024>, 1);
+    if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2, 1024>, 2);
+    if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4, 1024>, 4);
+    return go(launch_norm_vpt<BF16, 8, 1024>, 8);
+}
 
 }  // namespace
 
-cudaError_t launch_rms_norm(const RmsNormLaunch &p, bool bf16, int qmode, int sms, cudaStream_t stream) {
-    const int vecs = p.H / 8;
-    int vpt = 1;
-    while (vpt < 8 && (threads_for(vecs, vpt) > 1024 || (p.rows > sms && vpt < 4))) vpt *= 2;
-    const int threads = threads_for(vecs, vpt);
-    const int grid = std::min(p.rows, sms * 16);
-    switch (vpt) {
-#define A2AV_NORM(V)                                                                       \
-    return bf16 ? launch_norm_vpt<true, V>(p, qmode, threads, grid, stream)                \
-                : launch_norm_vpt<false, V>(p, qmode, threads, grid, stream)
-        case 1: A2AV_NORM(1);
-        case 2: A2AV_NORM(2);
-        case 4: A2AV_NORM(4);
-        default: A2AV_NORM(8);
-#undef A2AV_NORM
-    }
+cudaError_t launch_rms_norm(const RmsNormLaunch &p, bool bf16, int kind, int sms, cudaStream_t stream) {
+    return bf16 ? launch_norm_type<true>(p, kind, sms, stream) : launch_norm_type<false>(p, kind, sms, stream);
 }
 
-int rms_norm_grad_blocks(int64_t rows, int64_t) { return static_cast<int>(std::min<int64_t>(rows, kGradBlocks)); }
+int rms_norm_grad_blocks(int64_t rows, int64_t H) {
+    const int64_t r = grad_shape(H).rows;
+    return static_cast<int>(std::min<int64_t>((rows + r - 1) / r, kGradBlocks));
+}
 
 cudaError_t launch_rms_norm_grad(const RmsNormGradLaunch &p, bool bf16, cudaStream_t stream) {
-    const int vecs = p.H / 8;
-    int vpt = 2;
-    while (vpt < 8 && threads_for(vecs, vpt) > 1024) vpt *= 2;
-    const int threads = threads_for(vecs, vpt);
+    const GradShape shape = grad_shape(p.H);
     if (p.blocks > 0) {
-        switch (vpt) {
-#define A2AV_GRAD(V)                                                                                   \
-    if (bf16) rms_norm_grad_kernel<true, V><<<p.blocks, threads, 0, stream>>>(p);                      \
-    else rms_norm_grad_kernel<false, V><<<p.blocks, threads, 0, stream>>>(p);                          \
+        const dim3 block(shape.threads, shape.rows);
+        const size_t smem = shape.rows > 1 ? static_cast<size_t>(p.H) * 4 : 0;
+        cudaError_t err;
+        switch (shape.vpt) {
+#define A2AV_GRAD(V, MAXT)                                                                             \
+    err = bf16 ? launch_pdl(rms_norm_grad_kernel<true, V, MAXT>, p.blocks, block, smem, 0, stream, p)  \
+               : launch_pdl(rms_norm_grad_kernel<false, V, MAXT>, p.blocks, block, smem, 0, stream, p); \
     break
-            case 2: A2AV_GRAD(2);
-            case 4: A2AV_GRAD(4);
-            default: A2AV_GRAD(8);
+            case 2: A2AV_GRAD(2, 512);
+            case 4: A2AV_GRAD(4, 1024);
+            default: A2AV_GRAD(8, 1024);
 #undef A2AV_GRAD
         }
-        const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
-    if (p.dgamma)
-        dgamma_sum_kernel<<<(p.H + 31) / 32, 32 * kSlices, 0, stream>>>(p.partial, p.blocks, p.H, p.dgamma);
-    return cudaGetLastError();
+    if (!p.dgamma) return cudaSuccess;
+    return launch_pdl(dgamma_sum_kernel, (p.H + 31) / 32, 32 * kSlices, 0, 0, stream,
+                      static_cast<const float *>(p.partial), p.blocks, p.H, p.dgamma);
 }
 
 }  // namespace a2av
