@@ -35,10 +35,10 @@
 // operands by a warp of each CTA before the MMA may read them: multiplying by
 // zero on one side alone would let another expert's infinities through.
 //
-// The rows of A may still be in the making when this kernel starts: the kernel
-// before it in the stream (stage.cu) writes them in the order the tiles go and
+// A gated block's D_p may still be in the making when this kernel starts: the
+// kernel before it (glu_grad.cu) writes them in the order the tiles go and
 // counts the finished pieces of each 128 rows, and the producer waits for a
-// tile's counts.  That kernel is small enough to share the SMs with this one.
+// tile's counts.
 //
 // Per CTA: warp 0 loads, warp 1 clears ragged rows (weights' gradient), warp 4
 // allocates TMEM and (even CTA) issues, warps 5-8 are the epilogue.  Two
@@ -72,7 +72,6 @@ struct GroupInfo {
     int32_t row0;   // first expert-major row
     int32_t rows;
     int32_t tile0;  // first tile over its rows
-    int32_t half0;  // first 128-row half
 };
 
 struct Control {
@@ -188,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
 
     // ---- prologue: groups and tiles (warp 0), barriers (warp 1), TMEM (MMA warp)
     if (warp == 0) {
-        // (With rows in the making, the kernel that makes them has waited for
-        // all before it, and recvCounts was there for it too.)
-        if (!p.pieces) pdl_wait();
+        // (A kernel that this one overlaps has waited for all before it, and
+        // recvCounts was there for it too.)
+        const bool overlaps = p.pieces || p.after_permute;
+        if (!overlaps) pdl_wait();
         const bool good = build_segment_table(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int row0 = 0, rows = 0, tiles = 0;
         if (lane < p.e) {
@@ -198,17 +198,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             rows = C.seg.dst[(lane + 1) * p.W] - row0;
             tiles = good ? (rows + TILE_M - 1) / TILE_M * walk.tn : 0;
         }
-        const int halves = (rows + BM - 1) / BM;
-        int inc = tiles, hinc = halves;
+        int inc = tiles;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, off), h = __shfl_up_sync(0xffffffffu, hinc, off);
-            if (lane >= off) inc += v, hinc += h;
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
         }
-        if (lane < p.e) C.g[lane] = GroupInfo{row0, rows, inc - tiles, hinc - halves};
+        if (lane < p.e) C.g[lane] = GroupInfo{row0, rows, inc - tiles};
         const int total = __shfl_sync(0xffffffffu, inc, 31);
         if (lane == 0) {
-            C.g[p.e] = GroupInfo{0, 0, total, 0};
+            C.g[p.e] = GroupInfo{0, 0, total};
             C.row_tiles = total;
             C.total_tiles = total + (good ? p.e * walk.wm * walk.wn : 0);
             C.abort = 0;
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            bool all_there = !p.pieces;  // the kernel before this one has completed
+            bool all_there = !p.pieces && !p.after_permute;  // the kernel before this one has completed
             for (int t = unit; t < total && ok; t += nunits) {
                 const Tile w = tile_at(C, t, walk);
                 const int K = contraction(w);
@@ -274,16 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     ta = &p.tmDirect;
                     arow = source_row(C.seg, p.W, p.e, row);
                 } else if (!all_there) {
-                    if (w.weights) {  // all of the rows are contracted
+                    if (!GRAD || w.weights) {  // staged rows, or all rows contracted
                         pdl_wait();
                         all_there = true;
                     } else if (row < g_end) {
-                        // Staged halves are counted by half, the gradients' rows by blocks of 128 rows.
-                        const int c0 = GRAD ? row / BM : C.g[w.g].half0 + 2 * w.m + static_cast<int>(rank);
-                        const int c1 = GRAD ? (min(row + BM, g_end) - 1) / BM : c0;
-                        for (int c = c0; c <= c1 && ok; ++c)
-                            ok = wait_pieces(&C.abort, p.pieces + c, GRAD && c == p.A / BM ? p.last_pieces : p.row_pieces,
-                                             p.status, p.wait_limit_ns);
+                        for (int c = row / BM; c <= (min(row + BM, g_end) - 1) / BM && ok; ++c)
+                            ok = wait_pieces(&C.abort, p.pieces + c, c == p.A / BM ? p.last_pieces : p.row_pieces, p.status,
+                                             p.wait_limit_ns);
                         if (!ok) break;
                     }
                 }

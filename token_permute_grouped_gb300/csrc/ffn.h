@@ -50,31 +50,14 @@ struct GluLaunch {
 };
 cudaError_t launch_glu_quant(GluLaunch p, bool bf16, int act, int kind, cudaStream_t stream);
 
-// Rows in the making for a GEMM that may run beside their kernel (stage.cu).
-// `pieces`: counts of finished pieces by 128 rows, zero at the start; NULL: not
-// counted (the GEMM waits for the whole kernel).
-
-// Expert-major copy of rank-major rows, in the order of the GEMM's 128-row
-// halves (counted from each expert's first row).
-struct StageRowsLaunch {
-    const int32_t *recvCounts;
-    int32_t W, e, A, H1;
-    const void *src;
-    void *dst;
-    int32_t *status;         // stored (0 or kStatusBadCounts)
-    int32_t only_straddling; // copy only the halves that straddle a run boundary
-    int32_t *pieces;         // by half; only halves that straddle are counted
-};
-int stage_rows_pieces(int64_t H1);  // pieces of a half
-cudaError_t launch_stage_rows(const StageRowsLaunch &p, int sms, cudaStream_t stream);
-
 // dG = dh U act'(G), dU = dh act(G) for [rows, N] values.
 struct GluGradLaunch {
     int32_t rows, N;
     const void *dh;
     const float *gate, *up;
     void *dgate, *dup;
-    int32_t *pieces;  // by block of 128 rows
+    int32_t *pieces;  // counts of finished pieces by 128 rows, zero at the start, for a GEMM that runs beside
+                      // this kernel; NULL: not counted, and the kernel takes the SMs for itself
 };
 int glu_grad_pieces(int64_t rows, int64_t N);  // pieces of a block of this many (up to 128) rows
 cudaError_t launch_glu_grad(const GluGradLaunch &p, bool bf16, int act, int sms, cudaStream_t stream);
@@ -96,8 +79,9 @@ struct ExpertGemmLaunch {
     int32_t one_x;
     int32_t half_step;      // columns from a tile's first accumulator half to its second: 128 where both
                             // halves belong to one matrix, 0 where the second half is another matrix
-    const int32_t *pieces;  // rows of A in the making beside this kernel, by 128 (NULL: all there)
-    int32_t row_pieces, last_pieces;  // of 128 rows; of the last block of A (gradient)
+    const int32_t *pieces;  // gradient: the D_p are in the making beside this kernel (glu_grad.cu)
+    int32_t row_pieces, last_pieces;  // pieces of 128 rows; of the last block of A
+    int32_t after_permute;  // gated: launched to overlap the permute kernel before it
     int32_t *status;
     int32_t write_status;
     int32_t grid;           // CTAs, two a cluster

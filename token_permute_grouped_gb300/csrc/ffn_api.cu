@@ -8,6 +8,7 @@
 
 #include "a2av_ffn.h"
 #include "ffn.h"
+#include "kernels.h"
 #include "plan.cuh"
 #include "quantise.cuh"
 
@@ -18,6 +19,11 @@ using a2av::ExpertGemmLaunch;
 constexpr size_t kStatusBytes = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
 constexpr int kMaxDevices = 64;
+// Rows from which the slopes of a backward pass are computed beside its GEMM.
+// (65,308 rows of 2048 x 1408, forward and backward: 1550 us, 1715 one after
+// the other; 5013 rows of 1032 x 328: 99 against 97, the counts' reset and the
+// single block an SM cost more than they hide.)
+constexpr int64_t kSideRows = 8192;
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
@@ -199,23 +205,26 @@ a2av_status validate(const a2av_gated_desc *d) {
 
 // Whether the weight-streaming kernel (gated_rows.cu) takes a forward call: the
 // rows its fullest expert is expected to have fit one pass over the weights, or
-// two where the tile kernel would leave half of the SMs without a tile.
-// Measured (us, streaming / tiles), rows an expert: 4 experts of 4096 x 1024,
-// 16: 21 / 42, 32: 24 / 39, 64 (two passes): 31 / 38, 128: 42 / 39; one expert
-// of 7168 x 2048, 16: 17 / 43, 64: 20 / 43, 128: 28 / 43, 256: 45 / 43; 16
-// experts of 2048 x 1408, 32: 51 / 59, 64: 69 / 55.
+// two where the tile kernel would have tiles for half of the SMs at most and a
+// long way to go or a permute before it.
+// Measured (us, streaming / tiles), rows an expert: 4 experts of 4096 x 1024
+// from 8 sources, 16: 20 / 42, 32: 22 / 40, 96 (two passes): 30 / 39, 128
+// (three): 41 / 39; one expert of 7168 x 2048, 16: 17 / 42, 128: 26 / 42; of
+// 2048 x 704, 64: 12 / 16, 96: 18 / 16; 16 experts of 2048 x 1408, 32: 48 / 59,
+// 64: 64 / 55; 8 of 1032 x 328 from 2 sources, 64: 15 / 21.
 bool few_rows(const a2av_gated_desc &d) {
     if (d.A == 0 || d.want_permute_out) return false;
     const double most = a2av::gated_rows_most(d.A, d.e);
-    return most <= 64.0 || (most <= 128.0 && d.H1 >= 4096 && d.e * ((d.N + 127) / 128) < 40);
+    if (most <= 64.0) return true;
+    return most <= 128.0 && d.e * ((d.N + 127) / 128) < 40 && (d.H1 >= 4096 || d.W > 1);
 }
 
 size_t staged_bytes(const a2av_gated_desc *d) {
     return d->W > 1 && !d->want_permute_out ? round256(static_cast<size_t>(d->A) * d->H1 * 2) : 0;
 }
-// Counts of finished pieces, by 128 rows of each expert or of all.
+// Counts of finished pieces of the slopes, by 128 rows.
 size_t pieces_bytes(const a2av_gated_desc *d) {
-    return (d->W > 1 || d->save) && d->A > 0 ? round256((static_cast<size_t>(d->A) / 128 + d->e + 1) * 4) : 0;
+    return d->save && d->A > 0 ? round256((static_cast<size_t>(d->A) / 128 + 1) * 4) : 0;
 }
 size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
     return d->save ? round256(static_cast<size_t>(d->A) * d->N * 2) : 0;
@@ -368,20 +377,18 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     if (d.W > 1 && d.A > 0) {
         // Expert-major rows: all of them in permuteOut, or in the workspace
         // those 128-row halves of a tile that straddle a (source, expert) run
-        // boundary; the GEMM reads the other halves in place either way.
-        uint8_t *ws = static_cast<uint8_t *>(workspace) + kStatusBytes;
-        void *dst = d.want_permute_out ? permuteOut : ws + pieces_bytes(desc);
-        int32_t *pieces = reinterpret_cast<int32_t *>(ws);
-        if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
-        a2av::StageRowsLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status,
-                                 d.want_permute_out ? 0 : 1, pieces};
-        if (a2av::launch_stage_rows(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
-        g.pieces = pieces;
-        g.row_pieces = a2av::stage_rows_pieces(d.H1);
-        g.direct_halves = 1;
+        // boundary, the others being read in place.  (With all of them in
+        // permuteOut, just written, they are read there: 463 us against 498
+        // with the others in place, 65,308 rows of 2048 x 1408.)
+        void *dst = d.want_permute_out ? permuteOut
+                                       : static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
+        g.direct_halves = d.want_permute_out ? 0 : 1;
+        a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, g.direct_halves, 8};
+        if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        g.after_permute = 1;
         g.write_status = 0;
         rows = dst;
-        if (!operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
+        if (g.direct_halves && !operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
     }
     if (d.A > 0) {
         if (!operand_map(&g.tmA[0], rows, 1, d.A, d.H1, bf16, g.one_a) ||
@@ -425,8 +432,13 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
     uint8_t *slopes = static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
     void *const dG = slopes, *const dU = slopes + slope_bytes(desc);
     if (d.A > 0) {
-        int32_t *pieces = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
-        if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        // Side by side with the GEMM where the rows' gradient gives it something
+        // to do before all slopes are there, and there is enough to hide.
+        int32_t *pieces = nullptr;
+        if (dAtaOut && d.A >= kSideRows) {
+            pieces = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+            if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        }
         a2av::GluGradLaunch s{g.A, static_cast<int32_t>(d.N), dh, saved, saved + d.A * d.N, dG, dU, pieces};
         if (a2av::launch_glu_grad(s, g.bf16, d.act, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         g.pieces = pieces;

@@ -38,6 +38,7 @@ constexpr int kMmaWarp = 1;
 constexpr int kEpiWarp0 = 2;
 constexpr int kCopyWarp0 = 6;
 constexpr int kCopyWarps = 4;
+constexpr int kMaxSplit = 8;                 // CTAs of a cluster
 constexpr int kBK = 128;                     // contraction elements a stage
 constexpr int kCols = 64;                    // output columns of a job
 constexpr uint32_t kAtom = 128 * 128;        // 128 k-rows x 64 columns of weights
@@ -47,7 +48,7 @@ template <int R>
 struct RowShape {
     static constexpr uint32_t kXAtom = R * 128;              // R rows x 64 elements
     static constexpr uint32_t kStage = kWBytes + 2 * kXAtom;
-    static constexpr int kStages = R == 64 ? 3 : 5;
+    static constexpr int kStages = R <= 32 ? 5 : 3;
     static constexpr uint32_t kLag = kStages > 3 ? 2 : 1;    // stages whose rows of x are in flight beside the newest
     static constexpr uint32_t kPart = R * 128 * 4;           // fp32 [R][128]
     static constexpr uint32_t kTmemCols = 2 * R < 32 ? 32 : 2 * R;
@@ -56,7 +57,7 @@ struct RowShape {
 struct RowControl {
     uint64_t full[5], empty[5];
     uint64_t tfull[2], tempty[2];
-    uint64_t ready;   // every CTA of the cluster has stored its part
+    uint64_t ready;   // every CTA of the cluster has stored its rows' part
     uint64_t free;    // every CTA of the cluster has read this CTA's part
     uint32_t tmem_base;
     int32_t abort;
@@ -73,9 +74,12 @@ constexpr size_t row_smem() {
 }
 static_assert(row_smem<16>() <= 232448 && row_smem<32>() <= 232448 && row_smem<64>() <= 232448, "shared memory");
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -305,10 +309,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             const int live = min(R, rows - w.first);
             const int acc = jl & 1;
             if (!pair::wait_phase(&C.abort, smem_u32(&C.tfull[acc]), (jl >> 1) & 1, p.status, p.wait_limit_ns)) break;
-            if (!pair::wait_phase(&C.abort, freed, (jl & 1) ^ 1, p.status, p.wait_limit_ns)) break;
             __syncwarp();
             tc_fence_after_sync();
             const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * R;
+            if (!pair::wait_phase(&C.abort, freed, (jl & 1) ^ 1, p.status, p.wait_limit_ns)) break;
+            __syncwarp();
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
                 uint32_t r[16];
@@ -326,25 +331,34 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             }
             if (!pair::wait_phase(&C.abort, ready, jl & 1, p.status, p.wait_limit_ns)) break;
             __syncwarp();
-            for (int i = tid; i < live * own / 2; i += 4 * 32) {
-                const int r = i / (own / 2), c = rank * own + i % (own / 2) * 2;
-                if (w.col0 + c < p.N) {  // (N is even: both columns or neither)
-                    float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+            for (int i = tid; i < live * own / 4; i += 4 * 32) {
+                const int r = i / (own / 4), c = rank * own + i % (own / 4) * 4;
+                if (w.col0 + c < p.N) {  // (N is a multiple of 8: all four columns or none)
                     const uint32_t at = smem_u32(part + r * 128 + c);
-                    for (int k = 0; k < split; ++k) {
-                        const uint32_t a = pair::map_to_rank(at, k);
-                        g[0] += ld_cluster_f32(a);
-                        g[1] += ld_cluster_f32(a + 4);
-                        u[0] += ld_cluster_f32(a + 256);
-                        u[1] += ld_cluster_f32(a + 260);
+                    float4 g[kMaxSplit], u[kMaxSplit];
+#pragma unroll
+                    for (int k = 0; k < kMaxSplit; ++k) {
+                        if (k < split) {
+                            const uint32_t a = pair::map_to_rank(at, k);
+                            g[k] = ld_cluster_f32x4(a);
+                            u[k] = ld_cluster_f32x4(a + kCols * 4);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 1; k < kMaxSplit; ++k) {
+                        if (k < split) {
+                            g[0] = make_float4(g[0].x + g[k].x, g[0].y + g[k].y, g[0].z + g[k].z, g[0].w + g[k].w);
+                            u[0] = make_float4(u[0].x + u[k].x, u[0].y + u[k].y, u[0].z + u[k].z, u[0].w + u[k].w);
+                        }
                     }
                     const size_t o = static_cast<size_t>(row0 + w.first + r) * p.N + w.col0 + c;
                     if (p.saved[0]) {
-                        *reinterpret_cast<float2 *>(p.saved[0] + o) = make_float2(g[0], g[1]);
-                        *reinterpret_cast<float2 *>(p.saved[1] + o) = make_float2(u[0], u[1]);
+                        *reinterpret_cast<float4 *>(p.saved[0] + o) = g[0];
+                        *reinterpret_cast<float4 *>(p.saved[1] + o) = u[0];
                     }
-                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.h) + o) =
-                        pack2<BF16>(mul2(act_value<ACT>(pair_of(g[0], g[1])), pair_of(u[0], u[1])));
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.h) + o) = make_uint2(
+                        pack2<BF16>(mul2(act_value<ACT>(pair_of(g[0].x, g[0].y)), pair_of(u[0].x, u[0].y))),
+                        pack2<BF16>(mul2(act_value<ACT>(pair_of(g[0].z, g[0].w)), pair_of(u[0].z, u[0].w))));
                 }
             }
             __syncwarp();

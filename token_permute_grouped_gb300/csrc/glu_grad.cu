@@ -1,0 +1,110 @@
+// The gated block's element-wise gradient, dG = dh U act'(G), dU = dh act(G):
+// the operands of the GEMM behind it (expert_gemm.cu).
+//
+// HBM-bound while that GEMM is tensor-bound, so the two run side by side: one
+// block of 256 threads an SM, which fits beside a GEMM CTA, works through the
+// rows in the order the GEMM does and counts the finished pieces of each 128
+// rows, for which the GEMM's producer waits.  This kernel never waits for the
+// GEMM, and all its blocks are resident before the GEMM starts, so neither can
+// hold up the other.  65,308 x 1408 values: 325 us alone with one block an SM
+// (190 with eight, at the copy rate), but the block's whole backward pass,
+// with 897 us of GEMM, takes 1010 us, against 1095 one after the other.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "ffn.h"
+#include "pdl.cuh"
+
+namespace a2av {
+
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kRows = 128;         // rows of a counted block
+constexpr int kFlatVecs = 2048;    // vectors of a piece
+
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// The block's stores of this piece are done: one more finished piece of `count`.
+__device__ __forceinline__ void count_piece(int32_t *count) {
+    __syncthreads();
+    if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(count) : "memory");
+}
+
+// A block of 128 rows is contiguous in every tensor: its vectors are taken in
+// pieces of kFlatVecs.
+template <bool BF16, int ACT>
+__global__ void __launch_bounds__(kGradThreads) glu_grad_kernel(const GluGradLaunch p) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t per_block = static_cast<int64_t>(kRows) * (p.N / 8), total = static_cast<int64_t>(p.rows) * (p.N / 8);
+    const int pieces = static_cast<int>((per_block + kFlatVecs - 1) / kFlatVecs);
+    const int blocks = (p.rows + kRows - 1) / kRows;
+    for (int64_t i = blockIdx.x; i < static_cast<int64_t>(blocks) * pieces; i += gridDim.x) {
+        const int64_t block = i / pieces;
+        const int64_t v0 = block * per_block + (i - block * pieces) * kFlatVecs;
+        const int64_t end = min(min(v0 + kFlatVecs, (block + 1) * per_block), total);
+        if (v0 >= end) continue;  // (the last block may have fewer pieces)
+#pragma unroll 2
+        for (int64_t v = v0 + threadIdx.x; v < end; v += kGradThreads) {
+            const uint4 d = ld_stream(static_cast<const uint4 *>(p.dh) + v);
+            const uint4 g0 = ld_stream(reinterpret_cast<const uint4 *>(p.gate) + 2 * v);
+            const uint4 g1 = ld_stream(reinterpret_cast<const uint4 *>(p.gate) + 2 * v + 1);
+            const uint4 u0 = ld_stream(reinterpret_cast<const uint4 *>(p.up) + 2 * v);
+            const uint4 u1 = ld_stream(reinterpret_cast<const uint4 *>(p.up) + 2 * v + 1);
+            const auto f = [](uint32_t a, uint32_t b) { return pair_of(__uint_as_float(a), __uint_as_float(b)); };
+            const f32x2 g[4] = {f(g0.x, g0.y), f(g0.z, g0.w), f(g1.x, g1.y), f(g1.z, g1.w)};
+            const f32x2 u[4] = {f(u0.x, u0.y), f(u0.z, u0.w), f(u1.x, u1.y), f(u1.z, u1.w)};
+            f32x2 fd[4], dg[4], du[4];
+            unpack8<BF16>(d, fd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f32x2 slope;
+                const f32x2 a = act_value_slope<ACT>(g[k], slope);
+                dg[k] = mul2(mul2(fd[k], u[k]), slope);
+                du[k] = mul2(fd[k], a);
+            }
+            static_cast<uint4 *>(p.dgate)[v] = pack8<BF16>(dg);
+            static_cast<uint4 *>(p.dup)[v] = pack8<BF16>(du);
+        }
+        if (p.pieces) count_piece(p.pieces + block);
+    }
+}
+
+// An SM's split of L1 and shared memory holds while blocks run on it, and a GEMM
+// CTA needs the largest share, so a kernel that is to share its SMs asks for
+// that share too (otherwise the SM is set for L1, and the GEMM starts only as
+// these blocks end).
+template <typename Kernel>
+cudaError_t beside_gemm(Kernel kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
+}  // namespace
+
+int glu_grad_pieces(int64_t rows, int64_t N) {
+    return static_cast<int>((rows * (N / 8) + kFlatVecs - 1) / kFlatVecs);
+}
+
+cudaError_t launch_glu_grad(const GluGradLaunch &p, bool bf16, int act, int sms, cudaStream_t stream) {
+    const int64_t items = (static_cast<int64_t>(p.rows) + kRows - 1) / kRows * glu_grad_pieces(kRows, p.N);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, p.pieces ? sms : sms * 8));
+    const auto kern = bf16 ? (act == A2AV_ACT_SILU ? glu_grad_kernel<true, A2AV_ACT_SILU>
+                                                   : glu_grad_kernel<true, A2AV_ACT_GELU_TANH>)
+                           : (act == A2AV_ACT_SILU ? glu_grad_kernel<false, A2AV_ACT_SILU>
+                                                   : glu_grad_kernel<false, A2AV_ACT_GELU_TANH>);
+    if (p.pieces) {
+        const cudaError_t err = beside_gemm(kern);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(kern, grid, kGradThreads, 0, 0, stream, p);
+}
+
+}  // namespace a2av
