@@ -146,7 +146,9 @@ a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const vo
  *
  * Backward, for a gradient dh [A, N] of h:
  *     dG = dh * U * act'(G),  dU = dh * act(G)      rounded to T, the type the
- *                                                   tensor cores multiply
+ *                                                   tensor cores multiply (A <= 32:
+ *                                                   with the rest of the rounding as
+ *                                                   a second T)
  *     dPermuteOut = dG x gateWeight^T + dU x upWeight^T
  *     dGate = permuteOut^T x dG,  dUp = permuteOut^T x dU   per expert
  * dAtaOut [A, H1] holds dPermuteOut's rows back in rank-major order; dGate,

@@ -113,6 +113,7 @@ def test_gated_workspace(lib):
     # status, counts of finished pieces by 128 rows, then the larger of the staged rows and the two slopes
     pieces = (4 * (1000 // 128 + 1) + 255) // 256 * 256
     assert gated_size(lib)[1] == 256 + pieces + 2 * 1000 * 256 * 2
+    assert gated_size(lib, A=32)[1] == 256 + 256 + 4 * 32 * 256 * 2  # each slope with what its rounding left over
     assert gated_size(lib, save=0)[1] == 256
     assert gated_size(lib, save=0, want_permute_out=0)[1] == 256 + 1000 * 512 * 2
     assert gated_size(lib, W=1, save=0, want_permute_out=0)[1] == 256

@@ -28,6 +28,9 @@
 //   rows' gradient    D: rows x K    K-major     W: out columns x K    K-major
 //   weights' gradient X: K x M       MN-major    D: K x columns        MN-major
 //
+// A D_p may come as two summands (a rounding and what it left over); the second
+// ones are further products into the same accumulator.
+//
 // In the weights' gradient K runs over an expert's rows, whose last block is
 // ragged, and the rows behind it belong to the next expert.  That block goes
 // first in each tile, is multiplied only up to its last 16 rows, and the rows
@@ -251,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     const uint32_t ragged0 = smem_u32(&C.ragged[0]), cleared0 = smem_u32(&C.cleared[0]);
     const auto contraction = [&](const Tile &w) { return w.weights ? C.g[w.g].rows : p.K; };
     const auto is_ragged = [&](const Tile &w, const Block &b) { return w.weights && (b.len & 15) != 0; };
-    const auto steps_of = [&](const Tile &w, int kblocks) { return GRAD && !w.weights ? p.phases * kblocks : kblocks; };
+    // Contraction blocks of a tile: each product's, and those of the second summands.
+    const auto steps_of = [&](const Tile &w, int kblocks) {
+        return GRAD ? (w.weights ? p.parts : p.phases * p.parts) * kblocks : kblocks;
+    };
 
     if (warp == 0) {
         // =========================================================== producer
@@ -283,10 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         if (!ok) break;
                     }
                 }
-                for (int i = 0; i < steps; ++i, ++it) {
+                for (int i = 0, kb = 0, phase = 0; i < steps; ++i, ++it, ++kb) {
                     const int s = it % kStages;
-                    const int phase = GRAD && !w.weights && i >= kblocks ? 1 : 0;
-                    const Block b = block_of(w.weights, K, i - phase * kblocks);
+                    if (kb == kblocks) kb = 0, ++phase;
+                    const Block b = block_of(w.weights, K, kb);
                     if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.status,
                                           p.wait_limit_ns)) {
                         ok = false;
@@ -311,11 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         b_map = &p.tmB[rank], bx = w.n * 128, by = b.first;
                     } else if (!w.weights) {
                         a_map = &p.tmA[phase], ax = b.first, ay = row;
-                        b_map = &p.tmB[phase], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128;
+                        b_map = &p.tmB[phase % p.phases], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128;
                     } else {
                         ay = by = C.g[w.g].row0 + b.first;
                         a_map = &p.tmX, ax = w.m * TILE_M + static_cast<int>(rank) * BM;
-                        b_map = &p.tmA[p.half_step ? 0 : rank], bx = w.n * w_n + static_cast<int>(rank) * p.half_step;
+                        b_map = &p.tmA[phase * p.phases + (p.half_step ? 0 : rank)], bx = w.n * w_n + static_cast<int>(rank) * p.half_step;
                         bz = 0;
                         one_a = p.one_x, one_b = p.one_a;
                     }
@@ -344,14 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         // ============================================= ragged rows of the block
         uint32_t it = 0;
         uint32_t used = 0;  // parity, by stage, of the ragged blocks seen
-        for (int t = unit; t < total; t += nunits) {
+        bool ok = true;
+        for (int t = unit; t < total && ok; t += nunits) {
             const Tile w = tile_at(C, t, walk);
             const int K = contraction(w);
             const int kblocks = (K + BK - 1) / BK;
             const Block b = kblocks ? block_of(w.weights, K, 0) : Block{0, 0};
-            if (is_ragged(w, b)) {
-                const int s = it % kStages;
-                if (!pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns)) break;
+            for (int part = 0; part < (is_ragged(w, b) ? p.parts : 0) && ok; ++part) {
+                const int s = (it + part * kblocks) % kStages;
+                ok = pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns);
+                if (!ok) break;
                 used ^= 1u << s;
                 __syncwarp();
                 // Rows len .. the next multiple of 16, 128 bytes in each of
@@ -395,15 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     break;
                 tc_fence_after_sync();
                 const uint32_t d_tmem = C.tmem_base + acc * kAccCols;
-                for (int i = 0; i < steps; ++i, ++it) {
+                for (int i = 0, kb = 0; i < steps; ++i, ++it, ++kb) {
                     const int s = it % kStages;
+                    if (kb == kblocks) kb = 0;
                     const uint32_t par = (it / kStages) & 1;
                     if (!mbar_try_wait(full0 + 8 * s, par) &&
                         !pair::wait_phase(&C.abort, full0 + 8 * s, par, p.status, p.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
-                    const Block b = block_of(w.weights, K, i >= kblocks ? i - kblocks : i);
+                    const Block b = block_of(w.weights, K, kb);
                     if (is_ragged(w, b)) {
                         if (!pair::wait_phase(&C.abort, cleared0 + 8 * s, (used >> s) & 1, p.status,
                                               p.wait_limit_ns)) {

@@ -56,6 +56,7 @@ struct GluGradLaunch {
     const void *dh;
     const float *gate, *up;
     void *dgate, *dup;
+    int64_t low;      // 16-byte vectors from a slope to what its rounding left over, rounded in turn (0: not kept)
     int32_t *pieces;  // counts of finished pieces by 128 rows, zero at the start, for a GEMM that runs beside
                       // this kernel; NULL: not counted, and the kernel takes the SMs for itself
 };
@@ -72,6 +73,7 @@ struct ExpertGemmLaunch {
     // Tiles over the experts' rows: gated [A, N] = [A, K] x [K, N] twice;
     // gradient [A, N] = sum over phases of [A, K] x [N, K]^T.  N 0: none.
     int32_t K, N, phases;
+    int32_t parts;          // gradients: 2 where each D_p comes as two summands
     int32_t one_a, one_b;   // 1: a stage's operand is one TMA load (4-D map), 0: two (3-D map)
     int32_t direct_halves;  // gated: halves inside one segment are read in place from ataOut
     // Tiles of the weights' gradients, [wM, wN] an expert = X^T D.  wM 0: none.
@@ -88,7 +90,7 @@ struct ExpertGemmLaunch {
     uint64_t wait_limit_ns;
     void *out, *out_w[2];   // over the rows; weights' gradients by accumulator half
     float *saved[2];        // gated: unrounded G and U, or NULL
-    CUtensorMap tmA[2], tmB[2], tmX, tmY, tmW[2];
+    CUtensorMap tmA[4], tmB[2], tmX, tmY, tmW[2];  // tmA: by phase, then the second summands
     CUtensorMap tmDirect;
 };
 cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream);

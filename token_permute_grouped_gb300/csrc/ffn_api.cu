@@ -153,15 +153,17 @@ ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, con
 
 // Gradients of one or two products with the same rows, in one launch:
 // dX = sum_p D_p W_p^T, dW_p = X^T D_p.
-a2av_status run_gradients(ExpertGemmLaunch g, int phases, int64_t H1, int64_t N, const void *const D[2],
+// D: by product, then the second summands (parts 2).
+a2av_status run_gradients(ExpertGemmLaunch g, int phases, int parts, int64_t H1, int64_t N, const void *const D[4],
                           const void *X, const void *const Wt[2], void *dX, void *const dW[2], cudaStream_t stream) {
     const bool bf16 = g.bf16 != 0;
     g.grad = 1;
     g.phases = phases;
+    g.parts = parts;
     g.half_step = phases == 2 ? 0 : 128;
     g.one_a = g.one_b = N % 64 == 0;
     g.one_x = H1 % 64 == 0;
-    for (int p = 0; p < phases && g.A > 0; ++p)
+    for (int p = 0; p < phases * parts && g.A > 0; ++p)
         if (!operand_map(&g.tmA[p], D[p], 1, g.A, N, bf16, g.one_a)) return A2AV_ERR_CUDA;
     int64_t tiles = 0;
     if (dX && g.A > 0) {
@@ -226,6 +228,12 @@ size_t staged_bytes(const a2av_gated_desc *d) {
 size_t pieces_bytes(const a2av_gated_desc *d) {
     return d->save && d->A > 0 ? round256((static_cast<size_t>(d->A) / 128 + 1) * 4) : 0;
 }
+// Summands a slope is kept in.  One rounding to T adds about as much to a
+// gradient's error as the gradient's own rounding; over a few rows that is the
+// error of a few values, which nothing averages, so there each slope is kept
+// with what its rounding left over.  (The tensor cores then multiply twice as
+// much, which a few rows do not notice: the weights' bytes bound them.)
+int slope_parts(const a2av_gated_desc *d) { return d->A <= 32 ? 2 : 1; }
 size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
     return d->save ? round256(static_cast<size_t>(d->A) * d->N * 2) : 0;
 }
@@ -319,7 +327,7 @@ a2av_status a2av_gated_workspace_size(const a2av_gated_desc *desc, size_t *bytes
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + pieces_bytes(desc) + std::max(staged_bytes(desc), 2 * slope_bytes(desc));
+    *bytes = kStatusBytes + pieces_bytes(desc) + std::max(staged_bytes(desc), 2 * slope_parts(desc) * slope_bytes(desc));
     return A2AV_OK;
 }
 
@@ -430,6 +438,7 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
 
     ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
     uint8_t *slopes = static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
+    const int parts = slope_parts(desc);
     void *const dG = slopes, *const dU = slopes + slope_bytes(desc);
     if (d.A > 0) {
         // Side by side with the GEMM where the rows' gradient gives it something
@@ -439,15 +448,17 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
             pieces = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
             if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
         }
-        a2av::GluGradLaunch s{g.A, static_cast<int32_t>(d.N), dh, saved, saved + d.A * d.N, dG, dU, pieces};
+        a2av::GluGradLaunch s{g.A, static_cast<int32_t>(d.N), dh, saved, saved + d.A * d.N, dG, dU, 0, pieces};
+        if (parts == 2) s.low = 2 * slope_bytes(desc) / 16;
         if (a2av::launch_glu_grad(s, g.bf16, d.act, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         g.pieces = pieces;
         g.row_pieces = a2av::glu_grad_pieces(128, d.N);
         g.last_pieces = a2av::glu_grad_pieces(d.A % 128, d.N);
     }
-    const void *const D[2] = {dG, dU}, *const Wt[2] = {gateWeight, upWeight};
+    const void *const D[4] = {dG, dU, slopes + 2 * slope_bytes(desc), slopes + 3 * slope_bytes(desc)};
+    const void *const Wt[2] = {gateWeight, upWeight};
     void *const dW[2] = {dGate, dUp};
-    return run_gradients(g, 2, d.H1, d.N, D, permuteOut, Wt, dAtaOut, dW, stream);
+    return run_gradients(g, 2, parts, d.H1, d.N, D, permuteOut, Wt, dAtaOut, dW, stream);
 }
 
 a2av_status a2av_gmm_backward_workspace_size(const a2av_gmm_desc *desc, size_t *bytes) {
@@ -476,9 +487,9 @@ a2av_status a2av_gmm_backward(const a2av_gmm_desc *desc, const void *dY, const v
     if (!aligned(recvCounts, 4)) return A2AV_ERR_UNSUPPORTED;
     if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
     const ExpertGemmLaunch g = base_launch(d.W, d.e, d.A, d.dtype, recvCounts, static_cast<int32_t *>(workspace));
-    const void *const D[2] = {dY, nullptr}, *const Wt[2] = {gmmWeight, nullptr};
+    const void *const D[4] = {dY, nullptr, nullptr, nullptr}, *const Wt[2] = {gmmWeight, nullptr};
     void *const dW[2] = {dWeight, nullptr};
-    return run_gradients(g, 1, d.H1, d.N1, D, permuteOut, Wt, dAtaOut, dW,
+    return run_gradients(g, 1, 1, d.H1, d.N1, D, permuteOut, Wt, dAtaOut, dW,
                          reinterpret_cast<cudaStream_t>(stream_handle));
 }
 

@@ -38,6 +38,13 @@ __device__ __forceinline__ void count_piece(int32_t *count) {
     if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(count) : "memory");
 }
 
+// What a rounding left over; nothing where the value or its rounding is not finite.
+__device__ __forceinline__ f32x2 finite_part(f32x2 v) {
+    float a, b;
+    split(v, a, b);
+    return pair_of(fabsf(a) < __uint_as_float(0x7f800000u) ? a : 0.0f, fabsf(b) < __uint_as_float(0x7f800000u) ? b : 0.0f);
+}
+
 // A block of 128 rows is contiguous in every tensor: its vectors are taken in
 // pieces of kFlatVecs.
 template <bool BF16, int ACT>
@@ -71,8 +78,21 @@ __global__ void __launch_bounds__(kGradThreads) glu_grad_kernel(const GluGradLau
                 dg[k] = mul2(mul2(fd[k], u[k]), slope);
                 du[k] = mul2(fd[k], a);
             }
-            static_cast<uint4 *>(p.dgate)[v] = pack8<BF16>(dg);
-            static_cast<uint4 *>(p.dup)[v] = pack8<BF16>(du);
+            const uint4 hg = pack8<BF16>(dg), hu = pack8<BF16>(du);
+            static_cast<uint4 *>(p.dgate)[v] = hg;
+            static_cast<uint4 *>(p.dup)[v] = hu;
+            if (p.low) {
+                f32x2 rg[4], ru[4];
+                unpack8<BF16>(hg, rg);
+                unpack8<BF16>(hu, ru);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    dg[k] = finite_part(fma2(rg[k], both(-1.0f), dg[k]));
+                    du[k] = finite_part(fma2(ru[k], both(-1.0f), du[k]));
+                }
+                static_cast<uint4 *>(p.dgate)[p.low + v] = pack8<BF16>(dg);
+                static_cast<uint4 *>(p.dup)[p.low + v] = pack8<BF16>(du);
+            }
         }
         if (p.pieces) count_piece(p.pieces + block);
     }

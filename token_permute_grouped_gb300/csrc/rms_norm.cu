@@ -57,15 +57,19 @@ __device__ __forceinline__ float2 row_sum(float v, float2 *slots, int t, int thr
     return make_float2(v, fabsf(v) < __uint_as_float(0x7f800000u) ? lo : 0.0f);  // (an infinite sum's error is a NaN)
 }
 
-// 1 / sqrt(v): one Newton step on the hardware's reciprocal root, and in `lo`
-// what the next step would add.
-__device__ __forceinline__ float inv_sqrt(float v, float &lo) {
+// 1 / sqrt(sum / H + eps) for a sum of two parts: one Newton step on the
+// hardware's reciprocal root, and in `lo` what is missing from it, the roundings
+// of the mean among it.
+__device__ __forceinline__ float inv_rms(float2 sum, float H, float eps, float &lo) {
+    const float q = sum.x / H, q_lo = (fmaf(-q, H, sum.x) + sum.y) / H;
+    const float v = q + eps, z = v - q;
+    const float v_lo = (q - (v - z)) + (eps - z) + q_lo;
     float r = rsqrtf(v);
     lo = 0.0f;
     if (v > 0.0f && v < __uint_as_float(0x7f800000u)) {
         r = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
-        const float q = v * r, e = fmaf(v, r, -q);  // v r^2 = (q + e) r
-        lo = -0.5f * r * (fmaf(q, r, -1.0f) + e * r);
+        const float w = v * r, e = fmaf(v, r, -w);  // v r^2 = (w + e) r
+        lo = -0.5f * r * (fmaf(w, r, -1.0f) + (e + v_lo * r) * r);
     }
     return r;
 }
@@ -128,9 +132,8 @@ __global__ void __launch_bounds__(MAXT) rms_norm_kernel(const RmsNormLaunch p) {
         float sum, odd;
         split(sum2, sum, odd);
         const float2 total = row_sum(sum + odd, slots[flip], t, T, 0);
-        const float mean = (total.x + total.y) / static_cast<float>(p.H) + p.eps;
         float rstd_lo;
-        const float rstd = inv_sqrt(mean, rstd_lo);
+        const float rstd = inv_rms(total, static_cast<float>(p.H), p.eps, rstd_lo);
         if (p.rstd && t == 0) p.rstd[row] = rstd;
         if (!Q::kAny && !p.y) continue;
         f32x2 y[VPT][4];
