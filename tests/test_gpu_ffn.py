@@ -341,6 +341,16 @@ def test_gated_no_rows():
     b = plan.backward(dh, t.permuteOut, rc, w, w, t.saved, dGate=ones, dUp=ones.clone())
     assert _status(plan) == (0, 0)
     assert t.h.shape == (0, 64) and bool((b.dGate == 0).all()) and bool((b.dUp == 0).all())
+    # the (empty) rows' gradient alone: nothing to write, and a status to read
+    plan.workspace.fill_(0xff)
+    b = plan.backward(dh, t.permuteOut, rc, w, w, t.saved, want_weights=False)
+    assert b.dAtaOut.shape == (0, 128) and _status(plan) == (0, 0)
+    m = binding.GmmBackwardPlan(2, 3, 0, 128, 64)
+    m.workspace.fill_(0xff)
+    dx, dw = m.run(dh, x, rc, w, want_weights=False)
+    assert dx.shape == (0, 128) and dw is None and _status(m) == (0, 0)
+    _, dw = m.run(dh, x, rc, w, want_rows=False)
+    assert bool((dw == 0).all())
 
 
 @pytest.mark.parametrize("W", [1, 3])

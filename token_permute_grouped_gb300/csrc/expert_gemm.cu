@@ -119,7 +119,12 @@ __device__ __forceinline__ Tile tile_at(const Control &c, int t, const Walk &k) 
     return {g, local / k.tn, local % k.tn, false};
 }
 
-__device__ __forceinline__ void st_global_f32x8(float *ptr, const uint32_t *r) {
+__device__ __forceinline__ void st_global_v4(void *ptr, uint4 v) {
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 32 bytes, a whole sector, to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_b32x8(void *ptr, const uint32_t *r) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
@@ -235,11 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         }
     } else if (warp == 2) {
         if (lane == 0) {
-            if (walk.tn > 0) {
+            if (p.A > 0) {  // (the maps of tiles that there are none of were not made)
                 prefetch_tensormap(&p.tmA[0]);
-                prefetch_tensormap(&p.tmB[GRAD ? 0 : rank]);
-            } else {
-                prefetch_tensormap(&p.tmX);
+                if (walk.tn > 0) prefetch_tensormap(&p.tmB[GRAD ? 0 : rank]);
+                if (walk.wm > 0) prefetch_tensormap(&p.tmX);
             }
         }
     } else if (warp == kMmaWarp) {
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const uint32_t stage = epi0 + static_cast<uint32_t>(warp - kMmaWarp - 1) * kEpiWarpBytes;
         const uint32_t tempty0 = pair::map_to_rank(smem_u32(&C.tempty[0]), 0);
-        uint32_t tl = 0, nblk = 0;
+        uint32_t tl = 0;
         for (int t = unit; t < total; t += nunits, ++tl) {
             const Tile w = tile_at(C, t, walk);
             const int acc = tl & 1;
@@ -473,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             }
             const bool zero = w.weights && gi.rows == 0;  // nothing was accumulated
             const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kAccCols;
+            const bool wide = N % 16 == 0;
             constexpr int kChunks = GRAD ? 8 : 4;
             for (int c = 0; c < kChunks; ++c) {
                 const int half = c >> 2;
                 const int col = !GRAD ? w.n * 128 + c * 32
                                       : !w.weights ? w.n * 256 + c * 32 : w.n * w_n + half * p.half_step + (c & 3) * 32;
                 if (col >= N) continue;  // uniform
-                const uint32_t buf = stage + (nblk++ & 1u) * kEpiBufBytes;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_base + c * 32, r);
                 if constexpr (!GRAD) {
@@ -491,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             if (col + v * 8 < p.N) {
-                                st_global_f32x8(g_out + v * 8, r + v * 8);
-                                st_global_f32x8(u_out + v * 8, u + v * 8);
+                                st_global_b32x8(g_out + v * 8, r + v * 8);
+                                st_global_b32x8(u_out + v * 8, u + v * 8);
                             }
                         }
                     }
@@ -512,47 +516,28 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         for (int i = 0; i < 32; ++i) r[i] = 0;
                     }
                 }
-                // The store that read this buffer two blocks ago is done when at
-                // most one bulk group (every block commits one) is pending.
-                if (lane == 0) bulk_wait_read_1();
-                __syncwarp();
+                uint32_t w16[16];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint4 pk;
-                    pk.x = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 0]), __uint_as_float(r[v * 8 + 1])));
-                    pk.y = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 2]), __uint_as_float(r[v * 8 + 3])));
-                    pk.z = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 4]), __uint_as_float(r[v * 8 + 5])));
-                    pk.w = pack2<BF16>(pair_of(__uint_as_float(r[v * 8 + 6]), __uint_as_float(r[v * 8 + 7])));
-                    st_shared_v4(buf + lane * 64 + ((v ^ ((lane >> 1) & 3)) << 4), pk);
-                }
-                if (together) {  // one TMA store; columns past N are clipped
-                    const int y = static_cast<int>(__shfl_sync(0xffffffffu, orow, 0));
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(w.weights ? &p.tmW[half] : &p.tmY, buf, col, y);
-                        bulk_commit_group();
-                    }
-                } else {
-                    if (lane == 0) bulk_commit_group();  // an empty group keeps the count
-                    __syncwarp();
-                    const int v = lane & 3;
-                    uint16_t *out = static_cast<uint16_t *>(w.weights ? p.out_w[half] : p.out);
+                for (int v = 0; v < 16; ++v)
+                    w16[v] = pack2<BF16>(pair_of(__uint_as_float(r[2 * v]), __uint_as_float(r[2 * v + 1])));
+                if (valid) {
+                    uint16_t *out = static_cast<uint16_t *>(w.weights ? p.out_w[half] : p.out) + orow * N + col;
+                    if (wide) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int rr = 8 * k + (lane >> 2);
-                        const int64_t dst = __shfl_sync(0xffffffffu, orow, rr);
-                        const uint4 val = ld_shared_v4(buf + rr * 64 + ((v ^ ((rr >> 1) & 3)) << 4));
-                        if (row0w + rr < rows && col + v * 8 < N) st_stream_v4(out + dst * N + col + v * 8, val);
+                        for (int v = 0; v < 2; ++v)
+                            if (col + v * 16 < N) st_global_b32x8(out + v * 16, w16 + v * 8);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            if (col + v * 8 < N)
+                                st_global_v4(out + v * 8, make_uint4(w16[4 * v], w16[4 * v + 1], w16[4 * v + 2], w16[4 * v + 3]));
                     }
                 }
-                __syncwarp();
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) pair::arrive_cluster(tempty0 + 8 * acc);
         }
-        if (lane == 0) bulk_wait_all();
     }
 
     __syncwarp();  // the single-lane roles are done

@@ -185,8 +185,7 @@ a2av_status run_gradients(ExpertGemmLaunch g, int phases, int parts, int64_t H1,
         if (g.A > 0 && !operand_map(&g.tmX, X, 1, g.A, H1, bf16, g.one_x)) return A2AV_ERR_CUDA;
         tiles += g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? 128 : 256);
     }
-    if (tiles == 0) return A2AV_OK;
-    g.grid = gemm_grid(tiles);
+    g.grid = gemm_grid(tiles);  // (without a tile the launch still stores the status)
     return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 
@@ -424,7 +423,7 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
     if (!d.save) return A2AV_ERR_INVALID;
     if (!recvCounts || !gateWeight || !upWeight || !workspace) return A2AV_ERR_NULLPTR;
     if (d.A > 0 && (!dh || !permuteOut || !saved)) return A2AV_ERR_NULLPTR;
-    if ((dGate == nullptr) != (dUp == nullptr) || (!dAtaOut && !dGate)) return A2AV_ERR_NULLPTR;
+    if ((dGate == nullptr) != (dUp == nullptr) || (d.A > 0 && !dAtaOut && !dGate)) return A2AV_ERR_NULLPTR;
     for (const void *p : {dh, permuteOut, gateWeight, upWeight, static_cast<const void *>(dAtaOut),
                           static_cast<const void *>(dGate), static_cast<const void *>(dUp)})
         if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
@@ -478,8 +477,8 @@ a2av_status a2av_gmm_backward(const a2av_gmm_desc *desc, const void *dY, const v
     const a2av_status s = a2av_gmm_backward_workspace_size(desc, &need);
     if (s != A2AV_OK) return s;
     const a2av_gmm_desc &d = *desc;
-    if (!recvCounts || !workspace || (!dAtaOut && !dWeight)) return A2AV_ERR_NULLPTR;
-    if (d.A > 0 && (!dY || (dWeight && !permuteOut))) return A2AV_ERR_NULLPTR;
+    if (!recvCounts || !workspace) return A2AV_ERR_NULLPTR;
+    if (d.A > 0 && (!dY || (!dAtaOut && !dWeight) || (dWeight && !permuteOut))) return A2AV_ERR_NULLPTR;
     if (dAtaOut && !gmmWeight) return A2AV_ERR_NULLPTR;
     for (const void *p : {dY, permuteOut, gmmWeight, static_cast<const void *>(dAtaOut),
                           static_cast<const void *>(dWeight)})
