@@ -428,6 +428,52 @@ def test_outputs_are_not_overrun():
         assert bool((f[o.numel():] == 5.0).all())
 
 
+def test_outputs_on_16_byte_boundaries():
+    """Outputs and inputs that start 16 bytes into a 32-byte sector."""
+    W, H1, N, sizes = 2, 128, 64, [300, 41]
+    e, A, counts, x, wg, wu = _inputs(W, H1, N, sizes, torch.bfloat16, seed=130)
+    rc = torch.from_numpy(counts).cuda()
+
+    def off(t):
+        buf = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        return buf[8:].view(t.shape).copy_(t)
+
+    f = R.gated(x, counts, W, e, wg, wu, "silu")
+    dh = rnd(133, A, N)
+    plan = binding.GatedPlan(W, e, A, H1, N, save=True)
+    xd, gd, ud, dd = off(x), off(wg), off(wu), off(dh)
+    t = plan.run(xd, rc, gd, ud, h=off(torch.zeros(A, N).bfloat16()), permuteOut=off(torch.zeros(A, H1).bfloat16()))
+    R.assert_rounded(t.h, f["h"], f["eh"], "h")
+    z = lambda *s: off(torch.zeros(*s).bfloat16())
+    b = plan.backward(dd, t.permuteOut, rc, gd, ud, t.saved, dAtaOut=z(A, H1), dGate=z(e, H1, N), dUp=z(e, H1, N))
+    (dx, ex), ((dg, eg), (du, eu)) = R.gated_backward(f, dh, wg, wu, "silu", torch.bfloat16)
+    R.assert_rounded(b.dAtaOut, dx, ex, "dAtaOut")
+    R.assert_rounded(b.dGate, dg, eg, "dGate")
+    R.assert_rounded(b.dUp, du, eu, "dUp")
+    few = binding.GatedPlan(1, e, 9, H1, N)
+    rc9 = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    got = few.run(off(x[:9]), rc9, gd, ud, h=z(9, N)).h
+    f = R.gated(x[:9], [4, 5], 1, e, wg, wu, "silu")
+    R.assert_rounded(got, f["h"], f["eh"], "h (few rows)")
+
+
+def test_earlier_results_are_written_again_only_where_they_fit():
+    x, gamma = rnd(140, 6, 256).cuda(), rnd(141, 256).cuda()
+    r = binding.a2av_rms_norm(x, gamma, x, qtype="e4m3fn")
+    again = binding.a2av_rms_norm(x, gamma, x, qtype="e4m3fn", out=r)
+    assert again.codes.data_ptr() == r.codes.data_ptr()
+    with pytest.raises(ValueError, match="codes must be"):
+        binding.a2av_rms_norm(x[:4], gamma, qtype="e4m3fn", out=r)
+    with pytest.raises((TypeError, ValueError), match="scales must be"):
+        binding.a2av_rms_norm(x, gamma, qtype="e4m3fn", mode="group128", out=r)
+    y = binding.a2av_rms_norm(x, gamma, x, want_y=True, qtype="e4m3fn", out=r)
+    assert y.y is not None and torch.equal(y.codes, again.codes)
+    g = binding.a2av_glu_quant(x)
+    assert binding.a2av_glu_quant(x, out=g).codes.data_ptr() == g.codes.data_ptr()
+    with pytest.raises(ValueError, match="codes must be"):
+        binding.a2av_glu_quant(x[:3], out=g)
+
+
 def test_another_stream():
     W, H1, N, sizes = 2, 256, 128, [100, 60]
     e, A, counts, x, wg, wu = _inputs(W, H1, N, sizes, torch.bfloat16, seed=110)

@@ -507,12 +507,16 @@ def _code_outputs(out, rows, cols, mode, like):
                  (rows, cols // (32 if mx else 128)), like))
 
 
-class RmsNormOut(NamedTuple):
+class _RmsNormFields(NamedTuple):
     h: Optional[torch.Tensor]       # x + residual, element type (None without a residual)
     y: Optional[torch.Tensor]       # normed rows, element type
     codes: Optional[torch.Tensor]   # uint8 codes of the normed rows
     scales: Optional[torch.Tensor]  # uint8 E8M0 per 32 (mx) or float32 per 128 (group128)
     rstd: Optional[torch.Tensor]    # float32 [rows]
+
+
+class RmsNormOut(_RmsNormFields):
+    """Also holds, for a call that writes its tensors again, what they were made for and the descriptor."""
 
 
 def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want_y=None, want_rstd=False,
@@ -525,13 +529,19 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
     shape, dtype = x.shape, x.dtype
     rows, H = shape
     _is(gamma, "gamma", dtype, (H,))
-    q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
-    rs, h = 0, None
+    rs = None
     if residual is not None:
         _, rs = _rows_of(residual, "residual")
         if residual.shape != shape or residual.dtype != dtype:
             raise ValueError("residual must have the shape and type of x")
-        h = _out(out.h if out else None, "h", dtype, shape, x)
+    key = (shape, dtype, xs, rs, eps, qtype, mode, want_y, want_rstd, x.get_device())
+    if out is not None and getattr(out, "key", None) == key:  # its tensors and descriptor fit as they are
+        h, y, codes, scales, rstd = out
+        _call("a2av_rms_norm", out.desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y), _at(codes),
+              _at(scales), _at(rstd), _on(stream, x))
+        return out
+    q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
+    h = None if residual is None else _out(out.h if out else None, "h", dtype, shape, x)
     y = codes = scales = rstd = None
     if want_y or (want_y is None and qtype is None):
         y = _out(out.y if out else None, "y", dtype, shape, x)
@@ -539,10 +549,12 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
         rstd = _out(out.rstd if out else None, "rstd", torch.float32, (rows,), x)
     if qtype is not None:
         codes, scales = _code_outputs(out, rows, H, mode, x)
-    desc = RmsNormDesc(rows, H, xs, rs, code, q, m, eps)
-    _call("a2av_rms_norm", ctypes.byref(desc), x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
+    desc = ctypes.byref(RmsNormDesc(rows, H, xs, rs or 0, code, q, m, eps))
+    _call("a2av_rms_norm", desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
           _at(codes), _at(scales), _at(rstd), _on(stream, x))
-    return RmsNormOut(h, y, codes, scales, rstd)
+    result = RmsNormOut(h, y, codes, scales, rstd)
+    result.key, result.desc = key, desc
+    return result
 
 
 def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, workspace=None, stream=None):
@@ -567,10 +579,14 @@ def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, wo
     return dx, dgamma
 
 
-class GluQuantOut(NamedTuple):
+class _GluQuantFields(NamedTuple):
     codes: Optional[torch.Tensor]
     scales: Optional[torch.Tensor]
     h: Optional[torch.Tensor]
+
+
+class GluQuantOut(_GluQuantFields):
+    """Also holds what its tensors were made for and the descriptor, as RmsNormOut does."""
 
 
 def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, out: Optional[GluQuantOut] = None,
@@ -578,21 +594,30 @@ def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, 
     """act(gate) * up of gate_up [rows, 2N] (gate columns, then up columns) as codes and scales and / or in the
     element type (want_h; by default without a qtype)."""
     code, stride = _rows_of(gate_up, "gate_up")
-    rows, cols = gate_up.shape
+    shape = gate_up.shape
+    rows, cols = shape
     N = cols // 2
     if cols != 2 * N:
         raise ValueError("gate_up must have an even number of columns")
+    gate = gate_up.data_ptr()
+    key = (shape, gate_up.dtype, stride, act, qtype, mode, want_h, gate_up.get_device())
+    if out is not None and getattr(out, "key", None) == key:
+        codes, scales, h = out
+        _call("a2av_glu_quant", out.desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
+              _on(stream, gate_up))
+        return out
     q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
-    desc = GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode"))
+    desc = ctypes.byref(GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode")))
     codes = scales = h = None
     if qtype is not None:
         codes, scales = _code_outputs(out, rows, N, mode, gate_up)
     if want_h or (want_h is None and qtype is None):
         h = _out(out.h if out else None, "h", gate_up.dtype, (rows, N), gate_up)
-    gate = gate_up.data_ptr()
-    _call("a2av_glu_quant", ctypes.byref(desc), gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
+    _call("a2av_glu_quant", desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
           _on(stream, gate_up))
-    return GluQuantOut(codes, scales, h)
+    result = GluQuantOut(codes, scales, h)
+    result.key, result.desc = key, desc
+    return result
 
 
 class GatedOut(NamedTuple):

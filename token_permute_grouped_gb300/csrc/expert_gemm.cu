@@ -9,8 +9,9 @@
 // computes a tile of 256 rows x 256 accumulator columns with one cta_group::2
 // MMA: each CTA stages 128 of the rows of A and half of the columns of B.  The
 // even CTA issues the MMAs; each CTA holds its 128 rows of the accumulator.
+// Where that leaves too few tiles for the SMs, tiles are half as wide (BN 128).
 //
-// The gated tile is 128 output columns: the even CTA stages them from Wg, the
+// The gated tile is BN / 2 output columns: the even CTA stages them from Wg, the
 // odd one from Wu, so the accumulator's first half is G and its second U for
 // the same rows and columns, and the epilogue forms act(G) * U lane by lane
 // before anything is written.  The same split gives both weights' gradients
@@ -59,17 +60,24 @@ namespace {
 constexpr int BM = 128;        // rows a CTA stages
 constexpr int TILE_M = 256;    // rows of a pair's tile
 constexpr int BK = 128;        // contraction elements a stage
-constexpr int kStages = 3;
 constexpr uint32_t kAtomBytes = 128 * 128;     // 128 rows x 64 elements
-constexpr uint32_t kTileBytes = 2 * kAtomBytes;
-constexpr uint32_t kStageBytes = 2 * kTileBytes;  // A and B
+constexpr uint32_t kTileBytes = 2 * kAtomBytes;   // A
+constexpr int kMaxStages = 4;
 constexpr int kClearWarp = 1;
 constexpr int kMmaWarp = 4;
 constexpr int kThreads = 9 * 32;
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kAccCols = 256;
-constexpr uint32_t kEpiBufBytes = 32 * 64;  // 32 rows x 32 columns of 16 bits
-constexpr uint32_t kEpiWarpBytes = 2 * kEpiBufBytes;
+
+// BN: accumulator columns of a tile, half of them from each CTA's B.
+template <int BN>
+struct Shape {
+    static constexpr int kBRows = BN / 2;  // columns of B a CTA stages
+    static constexpr uint32_t kBBytes = kBRows * 256;
+    static constexpr uint32_t kStageBytes = kTileBytes + kBBytes;
+    static constexpr int kStages = BN == 256 ? 3 : 4;
+    static constexpr uint32_t kTmemCols = 2 * BN;
+    static constexpr uint32_t kMnAtoms = kBRows / 64;       // B MN-major: atoms of 64 columns
+    static constexpr uint32_t kKmAtomBytes = kBRows * 128;  // B K-major: an atom of 64 k
+};
 
 struct GroupInfo {
     int32_t row0;   // first expert-major row
@@ -78,10 +86,10 @@ struct GroupInfo {
 };
 
 struct Control {
-    uint64_t full[kStages];    // even CTA: a stage has landed in both CTAs
-    uint64_t empty[kStages];   // the MMAs that read a stage have completed
-    uint64_t ragged[kStages];  // this CTA's part of a ragged block has landed
-    uint64_t cleared[kStages]; // even CTA: both CTAs have cleared a ragged block's rows
+    uint64_t full[kMaxStages];    // even CTA: a stage has landed in both CTAs
+    uint64_t empty[kMaxStages];   // the MMAs that read a stage have completed
+    uint64_t ragged[kMaxStages];  // this CTA's part of a ragged block has landed
+    uint64_t cleared[kMaxStages]; // even CTA: both CTAs have cleared a ragged block's rows
     uint64_t tfull[2];         // accumulator ready for the epilogue
     uint64_t tempty[2];        // even CTA: both epilogues have drained it
     uint32_t tmem_base;
@@ -92,8 +100,11 @@ struct Control {
 };
 
 constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
-constexpr size_t kSmemBytes = 1024 + kStages * kStageBytes + kControlBytes + 4 * kEpiWarpBytes;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+template <int BN>
+constexpr size_t smem_bytes() {
+    return 1024 + Shape<BN>::kStages * Shape<BN>::kStageBytes + kControlBytes;
+}
+static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory per CTA");
 
 struct Tile {
     int g, m, n;
@@ -119,8 +130,9 @@ __device__ __forceinline__ Tile tile_at(const Control &c, int t, const Walk &k) 
     return {g, local / k.tn, local % k.tn, false};
 }
 
-__device__ __forceinline__ void st_global_v4(void *ptr, uint4 v) {
-    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void st_global_b32x4(void *ptr, const uint32_t *r) {
+    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // 32 bytes, a whole sector, to a 32-byte aligned address.
@@ -131,11 +143,11 @@ __device__ __forceinline__ void st_global_b32x8(void *ptr, const uint32_t *r) {
 }
 
 // Instruction descriptor for kind::f16 with an fp32 accumulator and the
-// operands' majors, M = N = 256.
-template <bool BF16>
+// operands' majors, M = 256.
+template <bool BF16, int BN>
 __device__ __forceinline__ constexpr uint32_t instr_desc(bool a_mn, bool b_mn) {
     return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
-           ((b_mn ? 1u : 0u) << 16) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+           ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(BN >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 // Contraction block kb of a tile: its first element and how many of its 128
@@ -177,20 +189,22 @@ __device__ __noinline__ bool wait_pieces(int32_t *abort_flag, const int32_t *cou
 }
 
 // GRAD: the gradients' tiles (both kinds); otherwise the gated block's.
-template <bool BF16, bool GRAD, int ACT>
+template <bool BF16, bool GRAD, int ACT, int BN>
 __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_constant__ ExpertGemmLaunch p) {
+    using S = Shape<BN>;
+    constexpr int kStages = S::kStages;
+    constexpr uint32_t kStageBytes = S::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
     Control &C = *reinterpret_cast<Control *>(base_ptr + kStages * kStageBytes);
-    const uint32_t epi0 = base + kStages * kStageBytes + kControlBytes;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = pair::cluster_rank();
     const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
     // Columns of the output one tile covers; the tiles of a launch.
-    const int row_n = GRAD ? 256 : 128, w_n = p.half_step ? 256 : 128;
+    const int row_n = GRAD ? BN : BN / 2, w_n = p.half_step ? BN : BN / 2;
     const Walk walk{(p.N + row_n - 1) / row_n, (p.wM + TILE_M - 1) / TILE_M, (p.wN + w_n - 1) / w_n};
 
     // ---- prologue: groups and tiles (warp 0), barriers (warp 1), TMEM (MMA warp)
@@ -247,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             }
         }
     } else if (warp == kMmaWarp) {
-        pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
+        pair::tmem_alloc_pair(smem_u32(&C.tmem_base), S::kTmemCols);
     }
     tc_fence_before_sync();
     pair::sync_all();
@@ -318,14 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     bool one_a = p.one_a, one_b = p.one_b;
                     if constexpr (!GRAD) {
                         a_map = ta, ax = b.first, ay = arow;
-                        b_map = &p.tmB[rank], bx = w.n * 128, by = b.first;
+                        b_map = &p.tmB[rank], bx = w.n * (BN / 2), by = b.first;
                     } else if (!w.weights) {
                         a_map = &p.tmA[phase], ax = b.first, ay = row;
-                        b_map = &p.tmB[phase % p.phases], bx = b.first, by = w.n * 256 + static_cast<int>(rank) * 128;
+                        b_map = &p.tmB[phase % p.phases], bx = b.first, by = w.n * BN + static_cast<int>(rank) * S::kBRows;
                     } else {
                         ay = by = C.g[w.g].row0 + b.first;
                         a_map = &p.tmX, ax = w.m * TILE_M + static_cast<int>(rank) * BM;
-                        b_map = &p.tmA[phase * p.phases + (p.half_step ? 0 : rank)], bx = w.n * w_n + static_cast<int>(rank) * p.half_step;
+                        b_map = &p.tmD[phase * p.phases + (p.half_step ? 0 : rank)], bx = w.n * w_n + static_cast<int>(rank) * p.half_step;
                         bz = 0;
                         one_a = p.one_x, one_b = p.one_a;
                     }
@@ -337,9 +351,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     }
                     if (one_b) {
                         pair::load_4d(b_st, b_map, bar, 0, by, bx / 64, bz);
-                    } else {
+                    } else {  // the second atom: 64 more columns, or 64 more of K
+                        const bool km = GRAD && !w.weights;
                         pair::load_3d(b_st, b_map, bar, bx, by, bz);
-                        pair::load_3d(b_st + kAtomBytes, b_map, bar, bx + 64, by, bz);
+                        if (km || S::kMnAtoms == 2)
+                            pair::load_3d(b_st + (km ? S::kKmAtomBytes : kAtomBytes), b_map, bar, bx + 64, by, bz);
                     }
                 }
             }
@@ -367,10 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 used ^= 1u << s;
                 __syncwarp();
                 // Rows len .. the next multiple of 16, 128 bytes in each of
-                // the four atoms (the swizzle stays within a row).
+                // each atom of A and B (the swizzle stays within a row).
                 const int rows = 16 - (b.len & 15);
                 const uint32_t st = base + s * kStageBytes + b.len * 128;
-                for (int i = lane; i < rows * 32; i += 32)  // atom i / (8 rows), 16-byte piece of its rows
+                for (int i = lane; i < rows * 8 * static_cast<int>(2 + S::kMnAtoms); i += 32)  // atom i / (8 rows), 16-byte piece of its rows
                     st_shared_v4(st + (i / (rows * 8)) * kAtomBytes + (i % (rows * 8)) * 16, make_uint4(0, 0, 0, 0));
                 fence_proxy_async_shared();
                 __syncwarp();
@@ -388,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             //    32 B along the row, the second atom 16 KB on.
             // MN-major: atoms of 64 columns 16 KB apart (leading offset), 8-row
             //    K groups 1024 B apart; a K step of 16 rows is 2 KB.
-            const uint64_t a_km = smem_desc(base, 16, 1024, kSwizzle128B);
-            const uint64_t a_mn = smem_desc(base, kAtomBytes, 1024, kSwizzle128B);
+            const uint64_t desc_km = smem_desc(base, 16, 1024, kSwizzle128B);
+            const uint64_t desc_mn = smem_desc(base, kAtomBytes, 1024, kSwizzle128B);
             const uint64_t to_b = kTileBytes >> 4;
             uint32_t it = 0, tl = 0, used = 0;
             bool ok = true;
@@ -400,13 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 const int acc = tl & 1;
                 // A: MN-major for the weights' gradient only; B: K-major for the rows' gradient only.
                 const bool a_is_mn = GRAD && w.weights, b_is_mn = !GRAD || w.weights;
-                const uint32_t idesc = instr_desc<BF16>(a_is_mn, b_is_mn);
-                const uint64_t a_desc0 = a_is_mn ? a_mn : a_km, b_desc0 = (b_is_mn ? a_mn : a_km) + to_b;
+                const uint32_t idesc = instr_desc<BF16, BN>(a_is_mn, b_is_mn);
+                const uint64_t a_desc0 = a_is_mn ? desc_mn : desc_km;
+                const uint64_t b_desc0 = (b_is_mn ? desc_mn : desc_km) + to_b;
                 if (!pair::wait_phase(&C.abort, smem_u32(&C.tempty[acc]), ((tl >> 1) & 1) ^ 1, p.status,
                                       p.wait_limit_ns))
                     break;
                 tc_fence_after_sync();
-                const uint32_t d_tmem = C.tmem_base + acc * kAccCols;
+                const uint32_t d_tmem = C.tmem_base + acc * BN;
                 for (int i = 0, kb = 0; i < steps; ++i, ++it, ++kb) {
                     const int s = it % kStages;
                     if (kb == kblocks) kb = 0;
@@ -432,8 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk) {
                         if (kk < ksteps) {
-                            const uint32_t km = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4, mn = 128 * kk;
-                            pair::mma(d_tmem, ad0 + (a_is_mn ? mn : km), bd0 + (b_is_mn ? mn : km), idesc,
+                            const uint32_t mn = 128 * kk;
+                            const uint32_t a_km = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4;
+                            const uint32_t b_km = ((kk >> 2) * S::kKmAtomBytes + (kk & 3) * 32) >> 4;
+                            pair::mma(d_tmem, ad0 + (a_is_mn ? mn : a_km), bd0 + (b_is_mn ? mn : b_km), idesc,
                                       (i | kk) != 0);
                         }
                     }
@@ -445,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     } else if (warp > kMmaWarp) {
         // =========================================================== epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may read
-        const uint32_t stage = epi0 + static_cast<uint32_t>(warp - kMmaWarp - 1) * kEpiWarpBytes;
         const uint32_t tempty0 = pair::map_to_rank(smem_u32(&C.tempty[0]), 0);
         uint32_t tl = 0;
         for (int t = unit; t < total; t += nunits, ++tl) {
@@ -458,37 +476,30 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             const int row0w = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;  // this warp's first row
             const int rows = w.weights ? p.wM : gi.rows, N = w.weights ? p.wN : p.N;
             const bool valid = row0w + lane < rows;
-            const bool all_rows = row0w + 32 <= rows;
-            // Output row of this lane's row, and whether the warp's 32 rows are
-            // consecutive there.
+            // Output row of this lane's row.
             int64_t orow = 0;
-            bool together = all_rows;
             if (w.weights) {
                 orow = static_cast<int64_t>(w.g) * p.wM + row0w + lane;
             } else if constexpr (!GRAD) {
                 orow = gi.row0 + row0w + lane;
-            } else {  // the gradient's rows go back to their order of arrival
-                int seg = 0;
-                if (valid) {
-                    seg = segment_of(C.seg, p.W, p.e, gi.row0 + row0w + lane);
-                    orow = source_row_in(C.seg, p.W, p.e, seg, gi.row0 + row0w + lane);
-                }
-                together = all_rows && __shfl_sync(0xffffffffu, seg, 0) == __shfl_sync(0xffffffffu, seg, 31);
+            } else if (valid) {  // the gradient's rows go back to their order of arrival
+                orow = source_row(C.seg, p.W, p.e, gi.row0 + row0w + lane);
             }
             const bool zero = w.weights && gi.rows == 0;  // nothing was accumulated
-            const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kAccCols;
+            const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
             const bool wide = N % 16 == 0;
-            constexpr int kChunks = GRAD ? 8 : 4;
+            constexpr int kChunks = GRAD ? BN / 32 : BN / 64;
             for (int c = 0; c < kChunks; ++c) {
-                const int half = c >> 2;
-                const int col = !GRAD ? w.n * 128 + c * 32
-                                      : !w.weights ? w.n * 256 + c * 32 : w.n * w_n + half * p.half_step + (c & 3) * 32;
+                const int half = c / (BN / 64);
+                const int col = !GRAD ? w.n * (BN / 2) + c * 32
+                                      : !w.weights ? w.n * BN + c * 32
+                                                   : w.n * w_n + half * p.half_step + c % (BN / 64) * 32;
                 if (col >= N) continue;  // uniform
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_base + c * 32, r);
                 if constexpr (!GRAD) {
                     uint32_t u[32];
-                    tmem_ld_32x32b_x32(t_base + 128 + c * 32, u);
+                    tmem_ld_32x32b_x32(t_base + BN / 2 + c * 32, u);
                     tmem_ld_wait();
                     if (p.saved[0] && valid) {
                         float *g_out = p.saved[0] + orow * p.N + col, *u_out = p.saved[1] + orow * p.N + col;
@@ -521,16 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 for (int v = 0; v < 16; ++v)
                     w16[v] = pack2<BF16>(pair_of(__uint_as_float(r[2 * v]), __uint_as_float(r[2 * v + 1])));
                 if (valid) {
-                    uint16_t *out = static_cast<uint16_t *>(w.weights ? p.out_w[half] : p.out) + orow * N + col;
-                    if (wide) {
+                    uint16_t *const out = static_cast<uint16_t *>(w.weights ? p.out_w[half] : p.out) + orow * N + col;
+                    if (wide && (reinterpret_cast<uintptr_t>(out) & 31) == 0) {
 #pragma unroll
                         for (int v = 0; v < 2; ++v)
                             if (col + v * 16 < N) st_global_b32x8(out + v * 16, w16 + v * 8);
                     } else {
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
-                            if (col + v * 8 < N)
-                                st_global_v4(out + v * 8, make_uint4(w16[4 * v], w16[4 * v + 1], w16[4 * v + 2], w16[4 * v + 3]));
+                            if (col + v * 8 < N) st_global_b32x4(out + v * 8, w16 + v * 4);
                     }
                 }
             }
@@ -545,17 +555,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     pair::sync_all();
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
-        pair::tmem_free_pair(C.tmem_base, kTmemCols);
+        pair::tmem_free_pair(C.tmem_base, S::kTmemCols);
     }
+}
+
+template <bool BF16, bool GRAD, int ACT, int BN>
+cudaError_t launch_shape(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    auto kern = expert_gemm_kernel<BF16, GRAD, ACT, BN>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<BN>()));
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kern, p.grid, kThreads, smem_bytes<BN>(), 2, stream, p);
 }
 
 template <bool BF16, bool GRAD, int ACT>
 cudaError_t launch_kind(const ExpertGemmLaunch &p, cudaStream_t stream) {
-    auto kern = expert_gemm_kernel<BF16, GRAD, ACT>;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
-    if (err != cudaSuccess) return err;
-    return launch_pdl(kern, p.grid, kThreads, kSmemBytes, 2, stream, p);
+    return p.bn == 256 ? launch_shape<BF16, GRAD, ACT, 256>(p, stream) : launch_shape<BF16, GRAD, ACT, 128>(p, stream);
 }
 
 template <bool BF16>
@@ -571,9 +586,9 @@ cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream) {
     return p.bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
 }
 
-// Every kind has the same shared memory and at most one CTA an SM.
+// Every kind needs nearly all of an SM's shared memory: one CTA an SM.
 int expert_gemm_max_clusters() {
-    return max_clusters(expert_gemm_kernel<true, false, A2AV_ACT_SILU>, kThreads, kSmemBytes, 2);
+    return max_clusters(expert_gemm_kernel<true, false, A2AV_ACT_SILU, 256>, kThreads, smem_bytes<256>(), 2);
 }
 
 }  // namespace a2av

@@ -79,8 +79,9 @@ struct ExpertGemmLaunch {
     // Tiles of the weights' gradients, [wM, wN] an expert = X^T D.  wM 0: none.
     int32_t wM, wN;
     int32_t one_x;
-    int32_t half_step;      // columns from a tile's first accumulator half to its second: 128 where both
+    int32_t half_step;      // columns from a tile's first accumulator half to its second: bn / 2 where both
                             // halves belong to one matrix, 0 where the second half is another matrix
+    int32_t bn;             // accumulator columns of a tile: 256 or 128
     const int32_t *pieces;  // gradient: the D_p are in the making beside this kernel (glu_grad.cu)
     int32_t row_pieces, last_pieces;  // pieces of 128 rows; of the last block of A
     int32_t after_permute;  // gated: launched to overlap the permute kernel before it
@@ -90,7 +91,8 @@ struct ExpertGemmLaunch {
     uint64_t wait_limit_ns;
     void *out, *out_w[2];   // over the rows; weights' gradients by accumulator half
     float *saved[2];        // gated: unrounded G and U, or NULL
-    CUtensorMap tmA[4], tmB[2], tmX, tmY, tmW[2];  // tmA: by phase, then the second summands
+    // tmA: the D_p by phase, then their second summands, as A; tmD: the same as B of the weights' gradient.
+    CUtensorMap tmA[4], tmB[2], tmX, tmD[4];
     CUtensorMap tmDirect;
 };
 cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream);

@@ -85,11 +85,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Operand tiles of [groups][rows][cols] row-major: 128 rows x 128 elements as
-// two 64-element atoms, 128-byte swizzled.  `one`: the 4-D view
-// [groups][cols / 64][rows][64], both atoms in one box (cols a multiple of
-// 64); otherwise the 3-D view, one atom a box.
-bool operand_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t cols, bool bf16, bool one) {
+// Operand tiles of [groups][rows][cols] row-major: 128 rows x 128 elements (or
+// another box) as 64-element atoms, 128-byte swizzled.  `one`: the 4-D view
+// [groups][cols / 64][rows][64], all atoms in one box (cols a multiple of 64);
+// otherwise the 3-D view, one atom a box.
+bool operand_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t cols, bool bf16, bool one,
+                 uint32_t box_rows = 128, uint32_t atoms = 2) {
     auto fn = encode_fn();
     if (!fn) return false;
     const auto type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -101,31 +102,18 @@ bool operand_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, 
         const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
                                     static_cast<cuuint64_t>(groups)};
         const cuuint64_t strides[3] = {pitch, 128, plane};
-        const cuuint32_t box[4] = {64, 128, 2, 1};
+        const cuuint32_t box[4] = {64, box_rows, atoms, 1};
         r = fn(m, type, 4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     } else {
         const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                     static_cast<cuuint64_t>(groups)};
         const cuuint64_t strides[2] = {pitch, plane};
-        const cuuint32_t box[3] = {64, 128, 1};
+        const cuuint32_t box[3] = {64, box_rows, 1};
         r = fn(m, type, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     }
     return r == CUDA_SUCCESS;
-}
-
-// [rows][cols] row-major output, stored in boxes of 32 x 32, 64-byte swizzled.
-bool output_map(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, bool bf16) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-    const cuuint32_t box[2] = {32, 32};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Persistent grid: the clusters resident at once, never more than there can be tiles.
@@ -136,6 +124,15 @@ int gemm_grid(int64_t max_tiles) {
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Accumulator columns of a tile: 128 where even tiles of that width are no more
+// than the clusters, else 256.  A 256-wide tile keeps the tensor cores and an
+// SM's 64 bytes a clock from L2 equally busy; a narrower one is bound by the
+// latter (1.6 times the time of a large product), but spreads a small product
+// over more SMs.  Measured (us, 256 / 128 wide): gated, 4 experts x 128 rows of
+// 4096 x 1024 28 / 24, one x 256 of 2048 x 704 15.4 / 14.0, 16 x 128 of
+// 2048 x 1408 (176 tiles of 256) 45 / 50.
+int pick_bn(int64_t tiles128) { return tiles128 <= std::max(1, gemm_clusters()) ? 128 : 256; }
 
 ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, const int32_t *recvCounts, int32_t *status) {
     ExpertGemmLaunch g;
@@ -160,32 +157,35 @@ a2av_status run_gradients(ExpertGemmLaunch g, int phases, int parts, int64_t H1,
     g.grad = 1;
     g.phases = phases;
     g.parts = parts;
-    g.half_step = phases == 2 ? 0 : 128;
     g.one_a = g.one_b = N % 64 == 0;
     g.one_x = H1 % 64 == 0;
+    const auto count = [&](int64_t bn) {
+        int64_t n = 0;
+        if (dX && g.A > 0) n += (ceil_div(g.A, 256) + g.e / 2) * ceil_div(H1, bn);
+        if (dW[0]) n += g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? bn / 2 : bn);
+        return n;
+    };
+    g.bn = pick_bn(count(128));
+    g.half_step = phases == 2 ? 0 : g.bn / 2;
+    const uint32_t b_cols = g.bn / 2;  // columns of B a CTA stages
     for (int p = 0; p < phases * parts && g.A > 0; ++p)
-        if (!operand_map(&g.tmA[p], D[p], 1, g.A, N, bf16, g.one_a)) return A2AV_ERR_CUDA;
-    int64_t tiles = 0;
+        if (!operand_map(&g.tmA[p], D[p], 1, g.A, N, bf16, g.one_a) ||
+            !operand_map(&g.tmD[p], D[p], 1, g.A, N, bf16, g.one_a, 128, b_cols / 64))
+            return A2AV_ERR_CUDA;
     if (dX && g.A > 0) {
         g.K = static_cast<int32_t>(N);
         g.N = static_cast<int32_t>(H1);
         g.out = dX;
         for (int p = 0; p < phases; ++p)
-            if (!operand_map(&g.tmB[p], Wt[p], g.e, H1, N, bf16, g.one_b)) return A2AV_ERR_CUDA;
-        if (!output_map(&g.tmY, dX, g.A, H1, bf16)) return A2AV_ERR_CUDA;
-        tiles += (ceil_div(g.A, 256) + g.e) * ceil_div(H1, 256);
+            if (!operand_map(&g.tmB[p], Wt[p], g.e, H1, N, bf16, g.one_b, b_cols)) return A2AV_ERR_CUDA;
     }
     if (dW[0]) {
         g.wM = static_cast<int32_t>(H1);
         g.wN = static_cast<int32_t>(N);
-        for (int i = 0; i < 2; ++i) {  // by accumulator half
-            g.out_w[i] = dW[phases == 2 ? i : 0];
-            if (!output_map(&g.tmW[i], g.out_w[i], g.e * H1, N, bf16)) return A2AV_ERR_CUDA;
-        }
+        for (int i = 0; i < 2; ++i) g.out_w[i] = dW[phases == 2 ? i : 0];  // by accumulator half
         if (g.A > 0 && !operand_map(&g.tmX, X, 1, g.A, H1, bf16, g.one_x)) return A2AV_ERR_CUDA;
-        tiles += g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? 128 : 256);
     }
-    g.grid = gemm_grid(tiles);  // (without a tile the launch still stores the status)
+    g.grid = gemm_grid(count(g.bn) + g.e * ceil_div(H1, g.bn));  // (without a tile the launch still stores the status)
     return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 
@@ -380,6 +380,8 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     g.N = static_cast<int32_t>(d.N);
     g.one_a = d.H1 % 64 == 0;
     g.one_b = d.N % 64 == 0;
+    const auto count = [&](int64_t bn) { return (ceil_div(d.A, 256) + d.e / 2) * ceil_div(d.N, bn / 2); };
+    g.bn = pick_bn(count(128));
     const void *rows = ataOut;
     if (d.W > 1 && d.A > 0) {
         // Expert-major rows: all of them in permuteOut, or in the workspace
@@ -398,10 +400,10 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
         if (g.direct_halves && !operand_map(&g.tmDirect, ataOut, 1, d.A, d.H1, bf16, g.one_a)) return A2AV_ERR_CUDA;
     }
     if (d.A > 0) {
+        const uint32_t atoms = g.bn / 128;
         if (!operand_map(&g.tmA[0], rows, 1, d.A, d.H1, bf16, g.one_a) ||
-            !operand_map(&g.tmB[0], gateWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
-            !operand_map(&g.tmB[1], upWeight, d.e, d.H1, d.N, bf16, g.one_b) ||
-            !output_map(&g.tmY, h, d.A, d.N, bf16))
+            !operand_map(&g.tmB[0], gateWeight, d.e, d.H1, d.N, bf16, g.one_b, 128, atoms) ||
+            !operand_map(&g.tmB[1], upWeight, d.e, d.H1, d.N, bf16, g.one_b, 128, atoms))
             return A2AV_ERR_CUDA;
         g.out = h;
         if (d.save) {
@@ -409,7 +411,7 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
             g.saved[1] = saved + static_cast<size_t>(d.A) * d.N;
         }
     }
-    g.grid = gemm_grid((ceil_div(d.A, 256) + d.e) * ceil_div(d.N, 128));
+    g.grid = gemm_grid((ceil_div(d.A, 256) + d.e) * ceil_div(d.N, g.bn / 2));
     return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 
