@@ -206,18 +206,19 @@ a2av_status validate(const a2av_gated_desc *d) {
 
 // Whether the weight-streaming kernel (gated_rows.cu) takes a forward call: the
 // rows its fullest expert is expected to have fit one pass over the weights, or
-// two where the tile kernel would have tiles for half of the SMs at most and a
-// long way to go or a permute before it.
+// somewhat more where the tile kernel would have tiles for half of the SMs at
+// most and a long way to go or a permute before it.
 // Measured (us, streaming / tiles), rows an expert: 4 experts of 4096 x 1024
-// from 8 sources, 16: 20 / 42, 32: 22 / 40, 96 (two passes): 30 / 39, 128
-// (three): 41 / 39; one expert of 7168 x 2048, 16: 17 / 42, 128: 26 / 42; of
-// 2048 x 704, 64: 12 / 16, 96: 18 / 16; 16 experts of 2048 x 1408, 32: 48 / 59,
-// 64: 64 / 55; 8 of 1032 x 328 from 2 sources, 64: 15 / 21.
+// from 8 sources, 16: 20 / 42, 32: 23 / 40, 96: 31 / 39, 128: 42 / 39; one
+// expert of 7168 x 2048, 16: 17 / 42, 128: 21 / 42, 256: 35 / 42; of 2048 x
+// 704, 64: 12 / 14, 128: 14 / 14; 16 experts of 2048 x 1408, 32: 49 / 59, 64: 67
+// / 55; 8 of 1032 x 328 from 2 sources, 64: 15 / 19.
 bool few_rows(const a2av_gated_desc &d) {
-    if (d.A == 0 || d.want_permute_out) return false;
+    if (d.A == 0) return false;
     const double most = a2av::gated_rows_most(d.A, d.e);
     if (most <= 64.0) return true;
-    return most <= 128.0 && d.e * ((d.N + 127) / 128) < 40 && (d.H1 >= 4096 || d.W > 1);
+    if (d.e * ((d.N + 127) / 128) >= 40) return false;
+    return d.e == 1 ? d.A <= 256 && d.H1 >= 4096 : most <= 128.0 && (d.H1 >= 4096 || d.W > 1);
 }
 
 size_t staged_bytes(const a2av_gated_desc *d) {
@@ -351,6 +352,11 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     if (sms <= 0) return A2AV_ERR_CUDA;
 
     if (few_rows(d)) {
+        if (d.want_permute_out) {  // for the backward pass; this kernel gathers the rows itself
+            a2av::PermuteLaunch pl{recvCounts, d.W, d.e, static_cast<int32_t>(d.A), static_cast<int32_t>(d.H1), ataOut,
+                                   permuteOut, static_cast<int32_t *>(workspace), 1, 0, 8};
+            if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        }
         const bool bf16 = d.dtype == A2AV_BF16;
         a2av::GatedRowsLaunch r;
         std::memset(&r, 0, sizeof r);

@@ -3,7 +3,7 @@
 //
 // Bound by the bytes of the active experts' weights, so the weights stream:
 // they are the 128-row operand of tcgen05.mma (M, MN-major as they lie in
-// memory) and the rows of x the narrow one (N: 16, 32 or 64, K-major, copied
+// memory) and the rows of x the narrow one (N: 16 to 128, K-major, copied
 // from where they arrived by four warps; a TMA row gather brings four rows an
 // instruction, and 16 a stage were slower than the weights).  A job is 64
 // columns of one expert: a stage's weight tile is 128 of K x 64 columns of Wg
@@ -51,6 +51,9 @@ struct RowShape {
     static constexpr int kStages = R <= 32 ? 5 : 3;
     static constexpr uint32_t kLag = kStages > 3 ? 2 : 1;    // stages whose rows of x are in flight beside the newest
     static constexpr uint32_t kPart = R * 128 * 4;           // fp32 [R][128]
+    // With 128 rows the parts take the place of the stages, which then wait
+    // for them between jobs (there is no room for both).
+    static constexpr bool kShared = R == 128;
     static constexpr uint32_t kTmemCols = 2 * R < 32 ? 32 : 2 * R;
 };
 
@@ -70,9 +73,12 @@ constexpr size_t kRowControlBytes = (sizeof(RowControl) + 1023) / 1024 * 1024;
 
 template <int R>
 constexpr size_t row_smem() {
-    return 1024 + RowShape<R>::kStages * RowShape<R>::kStage + RowShape<R>::kPart + kRowControlBytes;
+    return 1024 + RowShape<R>::kStages * RowShape<R>::kStage + (RowShape<R>::kShared ? 0 : RowShape<R>::kPart) +
+           kRowControlBytes;
 }
-static_assert(row_smem<16>() <= 232448 && row_smem<32>() <= 232448 && row_smem<64>() <= 232448, "shared memory");
+static_assert(row_smem<16>() <= 232448 && row_smem<32>() <= 232448 && row_smem<64>() <= 232448 &&
+                  row_smem<128>() <= 232448,
+              "shared memory per CTA");
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
@@ -118,8 +124,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
-    float *part = reinterpret_cast<float *>(base_ptr + S::kStages * S::kStage);
-    RowControl &C = *reinterpret_cast<RowControl *>(base_ptr + S::kStages * S::kStage + S::kPart);
+    float *part = reinterpret_cast<float *>(base_ptr + (S::kShared ? 0 : S::kStages * S::kStage));
+    RowControl &C =
+        *reinterpret_cast<RowControl *>(base_ptr + S::kStages * S::kStage + (S::kShared ? 0 : S::kPart));
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int split = p.split;  // CTAs of a cluster
@@ -179,14 +186,22 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const int kblocks = (p.K + kBK - 1) / kBK;
     const int kb0 = kblocks * rank / split, kb1 = kblocks * (rank + 1) / split;  // this CTA's part
     const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
+    const uint32_t ready = smem_u32(&C.ready), freed = smem_u32(&C.free);
+    // Before the stages of a CTA's job number jl are filled: the parts of the
+    // job before it have been read, where they share the memory.
+    const auto stages_free = [&](uint32_t jl) {
+        return !S::kShared || jl == 0 || pair::wait_phase(&C.abort, freed, (jl - 1) & 1, p.status, p.wait_limit_ns);
+    };
 
     if (warp == 0) {
         // ================================================== producer (weights)
         if (lane == 0) {
-            uint32_t it = 0;
+            uint32_t it = 0, jl = 0;
             bool ok = true;
-            for (int job = cluster; job < total && ok; job += clusters) {
+            for (int job = cluster; job < total && ok; job += clusters, ++jl) {
                 const Job w = job_at(C, job, p.W, R);
+                ok = stages_free(jl);
+                if (!ok) break;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % S::kStages;
                     if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / S::kStages) & 1) ^ 1, p.status,
@@ -209,19 +224,27 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
         // ================================================== producer (rows of x)
         // A thread copies the same 16-byte piece of a stage's 256 bytes of every
         // eighth row.  The copies are generic-proxy writes, so a stage is handed
-        // to the MMA by this thread's fence once they have landed, S::kLag
-        // stages later.
+        // to the MMA by this thread's fence once they have landed: S::kLag stages
+        // later, or as soon as there is no stage to fill.
         const int ct = threadIdx.x - kCopyWarp0 * 32, piece = ct % 16, r0 = ct / 16;
         const uint32_t to = (piece / 8) * S::kXAtom + r0 * 128 + (((piece % 8) ^ (r0 & 7)) << 4);
-        uint32_t it = 0;
+        uint32_t it = 0, given = 0, jl = 0;  // stages issued, stages handed over, jobs
         bool ok = true;
-        const auto hand_over = [&](uint32_t stage_no) {
+        const auto hand_over = [&](uint32_t until) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(full0 + 8 * (stage_no % S::kStages));
+            for (; given < until; ++given)
+                if (lane == 0) mbar_arrive(full0 + 8 * (given % S::kStages));
         };
-        for (int job = cluster; job < total && ok; job += clusters) {
+        for (int job = cluster; job < total && ok; job += clusters, ++jl) {
             const Job w = job_at(C, job, p.W, R);
+            if (S::kShared) {  // (nothing of this job can be read before the parts are gone)
+                cp_async_wait<0>();
+                hand_over(it);
+            }
+            ok = stages_free(jl);
+            if (!ok) break;
+            __syncwarp();
             const int row0 = C.seg.dst[w.expert * p.W], rows = C.seg.dst[(w.expert + 1) * p.W] - row0;
             const uint16_t *src[R / 8];
 #pragma unroll
@@ -234,8 +257,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % S::kStages;
-                if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / S::kStages) & 1) ^ 1, p.status,
-                                      p.wait_limit_ns)) {
+                const uint32_t par = ((it / S::kStages) & 1) ^ 1;
+                // No stage to fill yet: hand over what has been copied rather than wait for more.
+                if (given < it && !__all_sync(0xffffffffu, pair::try_wait_cluster(empty0 + 8 * s, par))) {
+                    cp_async_wait<0>();
+                    hand_over(it);
+                }
+                if (!pair::wait_phase(&C.abort, empty0 + 8 * s, par, p.status, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
@@ -249,15 +277,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                                         live ? 16 : 0);
                 }
                 cp_async_commit();
-                if (it >= S::kLag) {
+                if (it - given >= S::kLag) {
                     cp_async_wait<S::kLag>();
-                    hand_over(it - S::kLag);
+                    hand_over(it + 1 - S::kLag);
                 }
             }
         }
         cp_async_wait<0>();
-        if (ok)
-            for (uint32_t i = it >= S::kLag ? it - S::kLag : 0; i < it; ++i) hand_over(i);
+        if (ok) hand_over(it);
     } else if (warp == kMmaWarp) {
         // =========================================================== MMA issuer
         if (lane == 0) {
@@ -300,7 +327,6 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
         // =========================================================== epilogue
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int tid = threadIdx.x - kEpiWarp0 * 32;
-        const uint32_t ready = smem_u32(&C.ready), freed = smem_u32(&C.free);
         const int own = kCols / split;  // columns this CTA finishes
         uint32_t jl = 0;
         for (int job = cluster; job < total; job += clusters, ++jl) {
@@ -429,6 +455,10 @@ cudaError_t launch_rows_tile(GatedRowsLaunch &p, cudaStream_t stream) {
     const double most = gated_rows_most(p.A, p.e);  // so that one pass over the weights is usual
     if (most <= 16) return launch_rows<BF16, ACT, 16>(p, stream);
     if (most <= 32) return launch_rows<BF16, ACT, 32>(p, stream);
+    // 128 rows where one pass is then likely (fuller experts than expected come
+    // with skewed routing, and a second pass costs this shape more than 64
+    // rows a third: 4 experts x 96 rows of 4096 x 1024, 42 against 31 us).
+    if (most > 64 && (p.e == 1 || most <= 100)) return launch_rows<BF16, ACT, 128>(p, stream);
     return launch_rows<BF16, ACT, 64>(p, stream);
 }
 
