@@ -8,8 +8,9 @@
  * layouts, the caller owns every buffer, nothing is allocated, kept or
  * synchronised, work is only enqueued on `stream`, every call returns a
  * status code, and the same inputs give bitwise the same outputs (sums run in
- * a fixed order, without atomics).  Element type T: bf16 or fp16 (a2av_dtype),
- * the same for every T tensor of a call.  Sums, statistics and activations
+ * a fixed order).  Outputs do not overlap inputs or each other, but where a
+ * call says that they may.  Element type T: bf16 or fp16 (a2av_dtype), the
+ * same for every T tensor of a call.  Sums, statistics and activations
  * are computed in fp32; each T output is rounded once (nearest even).
  *
  * Errors, for every call: A2AV_ERR_NULLPTR for a missing required pointer,
@@ -148,7 +149,8 @@ a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const vo
  *     dG = dh * U * act'(G),  dU = dh * act(G)      rounded to T, the type the
  *                                                   tensor cores multiply (A <= 32:
  *                                                   with the rest of the rounding as
- *                                                   a second T)
+ *                                                   a second T; an infinity of x or
+ *                                                   a weight may then end as a NaN)
  *     dPermuteOut = dG x gateWeight^T + dU x upWeight^T
  *     dGate = permuteOut^T x dG,  dUp = permuteOut^T x dU   per expert
  * dAtaOut [A, H1] holds dPermuteOut's rows back in rank-major order; dGate,

@@ -474,6 +474,39 @@ def test_earlier_results_are_written_again_only_where_they_fit():
         binding.a2av_glu_quant(x[:3], out=g)
 
 
+@pytest.mark.parametrize("rows", [5, 400, 9000])  # few rows; one after the other; slopes beside the gradients' GEMM
+def test_captured_in_a_graph(rows):
+    """A layer's step captured once and replayed on new data gives what the calls give."""
+    W, e, H1, N = 2, 2, 256, 128
+    sizes = [rows - rows // 3, rows // 3]
+    _, A, counts, x, wg, wu = _inputs(W, H1, N, sizes, torch.bfloat16, seed=150)
+    rc = torch.from_numpy(counts).cuda()
+    xd, gd, ud, gamma, dh = dev(x, wg, wu, rnd(153, H1), rnd(154, A, N))
+    plan = binding.GatedPlan(W, e, A, H1, N, save=True)
+
+    def step():
+        n = binding.a2av_rms_norm(xd, gamma, want_y=True, want_rstd=True)
+        t = plan.run(n.y, rc, gd, ud)
+        b = plan.backward(dh, t.permuteOut, rc, gd, ud, t.saved)
+        dx, dgamma = binding.a2av_rms_norm_backward(b.dAtaOut, xd, gamma, n.rstd)
+        q = binding.a2av_glu_quant(t.h.view(A, N), qtype="e4m3fn")
+        return [t.h, b.dGate, b.dUp, dx, dgamma, q.codes, q.scales]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in (155, 156):
+        xd.copy_(rnd(seed, A, H1))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert _status(plan) == (0, 0)
+
+
 def test_another_stream():
     W, H1, N, sizes = 2, 256, 128, [100, 60]
     e, A, counts, x, wg, wu = _inputs(W, H1, N, sizes, torch.bfloat16, seed=110)
