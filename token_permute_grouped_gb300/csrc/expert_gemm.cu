@@ -131,13 +131,13 @@ __device__ __forceinline__ Tile tile_at(const Control &c, int t, const Walk &k) 
 }
 
 __device__ __forceinline__ void st_global_b32x4(void *ptr, const uint32_t *r) {
-    asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+    asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
 // 32 bytes, a whole sector, to a 32-byte aligned address.
 __device__ __forceinline__ void st_global_b32x8(void *ptr, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
@@ -382,12 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 if (!ok) break;
                 used ^= 1u << s;
                 __syncwarp();
-                // Rows len .. the next multiple of 16, 128 bytes in each of
-                // each atom of A and B (the swizzle stays within a row).
-                const int rows = 16 - (b.len & 15);
-                const uint32_t st = base + s * kStageBytes + b.len * 128;
-                for (int i = lane; i < rows * 8 * static_cast<int>(2 + S::kMnAtoms); i += 32)  // atom i / (8 rows), 16-byte piece of its rows
-                    st_shared_v4(st + (i / (rows * 8)) * kAtomBytes + (i % (rows * 8)) * 16, make_uint4(0, 0, 0, 0));
+                // Rows len .. the next multiple of 16, 128 bytes in each atom of
+                // A and B (the swizzle stays within a row): eight lanes an atom.
+                const uint32_t st = base + s * kStageBytes + b.len * 128 + (lane / 8) * kAtomBytes + (lane % 8) * 16;
+                if (lane / 8 < 2 + S::kMnAtoms)
+                    for (int r = b.len & 15; r < 16; ++r) st_shared_v4(st + (r - (b.len & 15)) * 128, make_uint4(0, 0, 0, 0));
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) pair::arrive_cluster(tempty0 + 8 * acc);
+            if (lane == 0) pair::arrive_reads_done(tempty0 + 8 * acc);
         }
     }
 

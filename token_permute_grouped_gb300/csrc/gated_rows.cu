@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             }
             __syncwarp();
             if (lane == 0)
-                for (int c = 0; c < split; ++c) pair::arrive_cluster(pair::map_to_rank(freed, c));
+                for (int c = 0; c < split; ++c) pair::arrive_reads_done(pair::map_to_rank(freed, c));
         }
     }
 

@@ -32,6 +32,14 @@ __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same after reads only (of TMEM, or of another CTA's shared memory, their
+// values used or waited for): it does not hold the arrival back until this
+// thread's stores to global memory have been seen by the cluster, which costs an
+// epilogue more than the stores.
+__device__ __forceinline__ void arrive_reads_done(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
