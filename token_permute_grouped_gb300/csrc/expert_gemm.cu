@@ -52,6 +52,7 @@
 #include "ffn.h"
 #include "pair.cuh"
 #include "pdl.cuh"
+#include "segments.cuh"
 
 namespace a2av {
 
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         // recvCounts was there for it too.)
         const bool overlaps = p.pieces || p.after_permute;
         if (!overlaps) pdl_wait();
-        const bool good = build_segment_table(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
+        const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int row0 = 0, rows = 0, tiles = 0;
         if (lane < p.e) {
             row0 = C.seg.dst[lane * p.W];

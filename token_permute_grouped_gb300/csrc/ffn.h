@@ -107,6 +107,7 @@ struct GatedRowsLaunch {
     int32_t *status;
     uint64_t wait_limit_ns;
     int32_t split, grid;  // set by the launch: CTAs of a cluster, CTAs
+    int32_t guess;        // likewise: experts taken to have rows before they are counted (all, or 0)
     const void *x;            // ataOut
     CUtensorMap tmGate, tmUp; // [e][K][N], box 64 columns x 128 k
 };

@@ -24,6 +24,12 @@ constexpr int kMaxDevices = 64;
 // the other; 5013 rows of 1032 x 328: 99 against 97, the counts' reset and the
 // single block an SM cost more than they hide.)
 constexpr int64_t kSideRows = 8192;
+// Mean rows of a (source, expert) run from which whole halves are read in place
+// (us, in place / all rows staged; mean run): 5013 rows of 1032 x 328 (20) 36.7
+// / 32.6, 20,000 of 2048 x 1408 (78) 177 / 169, 34,502 of 7168 x 2048 (135) 1285
+// / 1307, 65,308 of 2048 x 1408 (255) 474 / 484, 16,407 of 4096 x 1024 (513)
+// 168 / 193.
+constexpr int64_t kLongRun = 96;
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
@@ -390,14 +396,14 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     g.bn = pick_bn(count(128));
     const void *rows = ataOut;
     if (d.W > 1 && d.A > 0) {
-        // Expert-major rows: all of them in permuteOut, or in the workspace
+        // Expert-major rows: all of them, in permuteOut or the workspace, or only
         // those 128-row halves of a tile that straddle a (source, expert) run
-        // boundary, the others being read in place.  (With all of them in
-        // permuteOut, just written, they are read there: 463 us against 498
-        // with the others in place, 65,308 rows of 2048 x 1408.)
+        // boundary, the others being read in place.  (What has been staged is
+        // read there: 463 us against 498 with whole runs read in place beside a
+        // full permuteOut, 65,308 rows of 2048 x 1408.)
         void *dst = d.want_permute_out ? permuteOut
                                        : static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
-        g.direct_halves = d.want_permute_out ? 0 : 1;
+        g.direct_halves = !d.want_permute_out && d.A >= kLongRun * d.W * d.e;
         a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, g.direct_halves, 8};
         if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         g.after_permute = 1;

@@ -28,6 +28,7 @@
 #include "ffn.h"
 #include "pair.cuh"
 #include "pdl.cuh"
+#include "segments.cuh"
 
 namespace a2av {
 
@@ -38,6 +39,7 @@ constexpr int kMmaWarp = 1;
 constexpr int kEpiWarp0 = 2;
 constexpr int kCopyWarp0 = 6;
 constexpr int kCopyWarps = 4;
+constexpr int kAhead = 8;                    // K blocks of a job's weights fetched before the rows are counted
 constexpr int kMaxSplit = 8;                 // CTAs of a cluster
 constexpr int kBK = 128;                     // contraction elements a stage
 constexpr int kCols = 64;                    // output columns of a job
@@ -94,6 +96,14 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// A TMA box into L2 only.
+__device__ __forceinline__ void prefetch_3d(const void *tmap, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -134,7 +144,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const int strips = (p.N + kCols - 1) / kCols;
     if (warp == 0) {
         pdl_wait();
-        const bool good = build_segment_table(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
+        const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int rows = 0;
         if (lane < p.e && good) rows = C.seg.dst[(lane + 1) * p.W] - C.seg.dst[lane * p.W];
         const int jobs = (rows + R - 1) / R * strips;
@@ -176,6 +186,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     } else if (warp == kEpiWarp0 + 1 && lane == 0) {
         prefetch_tensormap(&p.tmGate);
         prefetch_tensormap(&p.tmUp);
+        // With rows for nearly every expert, this CTA's first job is known
+        // before they are counted, and while the kernel before this one ends:
+        // its weights may be on their way to L2.
+        const int job = blockIdx.x / split, kblocks = (p.K + kBK - 1) / kBK;
+        const int kb0 = kblocks * rank / split, kb1 = kblocks * (rank + 1) / split;
+        if (job < p.guess * strips)
+            for (int kb = kb0; kb < min(kb1, kb0 + kAhead); ++kb) {
+                prefetch_3d(&p.tmGate, job % strips * kCols, kb * kBK, job / strips);
+                prefetch_3d(&p.tmUp, job % strips * kCols, kb * kBK, job / strips);
+            }
     }
     tc_fence_before_sync();
     pair::sync_all();
@@ -433,6 +453,7 @@ cudaError_t launch_rows(GatedRowsLaunch &p, cudaStream_t stream) {
     const double reached = p.e * (1.0 - std::pow(1.0 - 1.0 / p.e, static_cast<double>(p.A)));
     const int strips = (p.N + kCols - 1) / kCols;
     const double jobs = std::ceil(reached - 0.5) * strips;
+    p.guess = reached > 0.85 * p.e ? p.e : 0;
     const int kblocks = (p.K + kBK - 1) / kBK;
     double best = 0.0;
     for (int i = 0; i < 4; ++i) {
