@@ -101,7 +101,8 @@ a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const v
  * the gradient passes as through y (straight-through).
  *   dy, dh, h, dx [rows, H] T, contiguous; gamma [H] T; rstd [rows] float32;
  *   dgamma [H] float32.  dx may be dh or dy itself.  dgamma NULL: not computed.
- * Phase 1 gives the workspace (per-block partial sums of dgamma).
+ * Phase 1 gives the workspace (per-block partial sums of dgamma; 0 bytes for a
+ * few rows, workspace may then be NULL).
  * Limits as above (H a multiple of 8).
  */
 a2av_status a2av_rms_norm_backward_workspace_size(int64_t rows, int64_t H, int32_t dtype, size_t *bytes);

@@ -54,7 +54,7 @@ def test_norm_null_descriptor(lib):
     assert NAMES[lib.a2av_rms_norm(None, *[ptr(i) for i in range(8)], None)] == NULLPTR
 
 
-def norm_back(lib, rows=4, H=256, dtype=0, wsbytes=1 << 20, **kw):
+def norm_back(lib, rows=400, H=256, dtype=0, wsbytes=1 << 20, **kw):
     names = ["dy", "dh", "h", "gamma", "rstd", "dx", "dgamma", "workspace"]
     args = [kw.get(n, ptr(i)) for i, n in enumerate(names)]
     return NAMES[lib.a2av_rms_norm_backward(rows, H, dtype, *args, wsbytes, None)]

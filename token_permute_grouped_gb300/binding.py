@@ -10,6 +10,7 @@ every entry point raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -488,6 +489,8 @@ def _rows_of(t, name):
 def _out(t, name, dtype, shape, like):
     """The caller's output tensor, checked, or a new one on `like`'s device."""
     if t is None:
+        if like.shape == shape and like.dtype == dtype and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=like.device)
     _is(t, name, dtype, shape)
     return t
@@ -557,6 +560,11 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
     return result
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_backward_size(rows, H, code):
+    return _size("a2av_rms_norm_backward_workspace_size", rows, H, code)
+
+
 def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, workspace=None, stream=None):
     """(dx [rows, H], dgamma float32 [H]) from the gradient dy of the normed rows and, optionally, the gradient dh
     that reaches h directly.  dx is the gradient of x and of the residual."""
@@ -571,11 +579,11 @@ def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, wo
     _is(rstd, "rstd", torch.float32, (rows,))
     dx = _out(dx, "dx", dtype, shape, dy)
     dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy)
-    if workspace is None:
-        workspace = torch.empty(_size("a2av_rms_norm_backward_workspace_size", rows, H, code), dtype=torch.uint8,
-                                device=dy.device)
+    need = _norm_backward_size(rows, H, code)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
     _call("a2av_rms_norm_backward", rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd), _at(dx),
-          _at(dgamma), _at(workspace), workspace.numel(), _on(stream, dy))
+          _at(dgamma), _at(workspace), 0 if workspace is None else workspace.numel(), _on(stream, dy))
     return dx, dgamma
 
 
@@ -663,7 +671,7 @@ class GatedPlan:
         self._check_shared(recvCounts, gateWeight, upWeight)
         h = _out(h, "h", dtype, (A, N), ws)
         saved = _out(saved, "saved", torch.float32, (2, A, N), ws) if d.save else None
-        permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ws) if d.want_permute_out else None
+        permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ataOut) if d.want_permute_out else None
         _call("a2av_gated_run", ctypes.byref(d), ataOut.data_ptr(), recvCounts.data_ptr(), gateWeight.data_ptr(),
               upWeight.data_ptr(), _at(permuted), h.data_ptr(), _at(saved), ws.data_ptr(), ws.numel(),
               _on(stream, ws))
@@ -677,9 +685,9 @@ class GatedPlan:
         _is(permuteOut, "permuteOut", dtype, (A, H1))
         self._check_shared(recvCounts, gateWeight, upWeight)
         _is(saved, "saved", torch.float32, (2, A, N))
-        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), ws) if want_rows else None
-        gate = _out(dGate, "dGate", dtype, (d.e, H1, N), ws) if want_weights else None
-        up = _out(dUp, "dUp", dtype, (d.e, H1, N), ws) if want_weights else None
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut) if want_rows else None
+        gate = _out(dGate, "dGate", dtype, (d.e, H1, N), gateWeight) if want_weights else None
+        up = _out(dUp, "dUp", dtype, (d.e, H1, N), upWeight) if want_weights else None
         _call("a2av_gated_backward", ctypes.byref(d), dh.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
               gateWeight.data_ptr(), upWeight.data_ptr(), saved.data_ptr(), _at(rows), _at(gate), _at(up),
               ws.data_ptr(), ws.numel(), _on(stream, ws))
@@ -705,8 +713,8 @@ class GmmBackwardPlan:
         _is(permuteOut, "permuteOut", dtype, (A, H1))
         _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
         _is(gmmWeight, "gmmWeight", dtype, (d.e, H1, N1))
-        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), ws) if want_rows else None
-        weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), ws) if want_weights else None
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut) if want_rows else None
+        weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), gmmWeight) if want_weights else None
         _call("a2av_gmm_backward", ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
               gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel(), _on(stream, ws))
         return rows, weights

@@ -280,7 +280,8 @@ a2av_status a2av_rms_norm_backward_workspace_size(int64_t rows, int64_t H, int32
     if (!bytes) return A2AV_ERR_NULLPTR;
     if (rows < 0 || rows > INT32_MAX || H <= 0 || H >= 65536 || !type16(dtype)) return A2AV_ERR_INVALID;
     if (!mult8(H)) return A2AV_ERR_UNSUPPORTED;
-    *bytes = round256(std::max<size_t>(1, static_cast<size_t>(a2av::rms_norm_grad_blocks(rows, H)) * H * 4));
+    const int blocks = a2av::rms_norm_grad_blocks(rows, H);
+    *bytes = blocks > 1 ? round256(static_cast<size_t>(blocks) * H * 4) : 0;
     return A2AV_OK;
 }
 
@@ -294,7 +295,7 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
     for (const void *p : {dy, dh, h, gamma, static_cast<const void *>(dx), static_cast<const void *>(dgamma)})
         if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
     if (!aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
-    if (dgamma && rows > 0) {
+    if (dgamma && need > 0) {
         if (!workspace) return A2AV_ERR_NULLPTR;
         if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
     }

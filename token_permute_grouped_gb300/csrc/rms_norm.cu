@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLa
     }
     pdl_trigger();  // the sum over the blocks may be launched; it waits for this grid's end
     if (!p.dgamma) return;
-    float4 *out = reinterpret_cast<float4 *>(p.partial + static_cast<size_t>(blockIdx.x) * p.H);
+    float4 *out = reinterpret_cast<float4 *>(p.blocks == 1 ? p.dgamma : p.partial + static_cast<size_t>(blockIdx.x) * p.H);
     for (int turn = 0; turn < R; ++turn) {
         if (turn == g) {
 #pragma unroll
@@ -386,8 +386,10 @@ cudaError_t launch_rms_norm(const RmsNormLaunch &p, bool bf16, int kind, int sms
 }
 
 int rms_norm_grad_blocks(int64_t rows, int64_t H) {
+    // Up to two turns of its rows by one block, whose sum is then all of it.
     const int64_t r = grad_shape(H).rows;
-    return static_cast<int>(std::min<int64_t>((rows + r - 1) / r, kGradBlocks));
+    return rows <= 2 * r ? static_cast<int>(std::min<int64_t>(rows, 1))
+                         : static_cast<int>(std::min<int64_t>((rows + r - 1) / r, kGradBlocks));
 }
 
 cudaError_t launch_rms_norm_grad(const RmsNormGradLaunch &p, bool bf16, cudaStream_t stream) {
@@ -408,7 +410,7 @@ cudaError_t launch_rms_norm_grad(const RmsNormGradLaunch &p, bool bf16, cudaStre
         }
         if (err != cudaSuccess) return err;
     }
-    if (!p.dgamma) return cudaSuccess;
+    if (!p.dgamma || p.blocks == 1) return cudaSuccess;
     return launch_pdl(dgamma_sum_kernel, (p.H + 31) / 32, 32 * kSlices, 0, 0, stream,
                       static_cast<const float *>(p.partial), p.blocks, p.H, p.dgamma);
 }
