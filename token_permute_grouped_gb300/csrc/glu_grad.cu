@@ -6,9 +6,9 @@
 // rows in the order the GEMM does and counts the finished pieces of each 128
 // rows, for which the GEMM's producer waits.  This kernel never waits for the
 // GEMM, and all its blocks are resident before the GEMM starts, so neither can
-// hold up the other.  65,308 x 1408 values: 325 us alone with one block an SM
-// (190 with eight, at the copy rate), but the block's whole backward pass,
-// with 897 us of GEMM, takes 1010 us, against 1095 one after the other.
+// hold up the other.  65,308 x 1408 values: 315 us alone with one block an SM
+// (190 with eight, at the copy rate) and 905 us of GEMM; forward and backward of
+// the gated block together take 1550 us side by side, 1715 one after the other.
 #include <algorithm>
 
 #include "activation.cuh"

@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLa
     }
 }
 
-// dgamma[c] = sum over blocks of partial[block][c]: 32 columns a block of 32
-// row slices, each slice in block order, the slices joined in order.
+// dgamma[c] = sum over blocks of partial[block][c]: 32 columns a block of
+// kSlices slices of the partial sums, each in block order, the slices joined in
+// order: the same sum every time.  About 3 us behind the kernel above.
 constexpr int kSlices = 16;
 __global__ void __launch_bounds__(32 * kSlices) dgamma_sum_kernel(const float *__restrict__ partial, int blocks, int H,
                                                                   float *__restrict__ dgamma) {
@@ -342,15 +343,16 @@ __global__ void __launch_bounds__(32 * kSlices) dgamma_sum_kernel(const float *_
 }
 
 // One block of 512 threads an SM, with the next row's three vectors requested
-// while a row is reduced: 16,384 x 2048 bf16 rows take 47 us (5.7 TB/s), two
-// blocks without the early request 52, two of 256 threads with it 51 (and
-// twice the partial sums).
+// while a row is reduced: 16,384 x 2048 bf16 rows take 46 us with the sum over
+// the blocks (5.8 TB/s, 86 % of the copy rate; 40.5 without it, 6.6 TB/s), two
+// blocks without the early request 52, two of 256 threads with it 51 (and twice
+// the partial sums).
 constexpr int kGradBlocks = 152;
 constexpr int kGradThreads = 512;
 
 // Resident threads an SM that the norm's grid is made for: its 64 registers a
 // thread allow 1024.  Two vectors a thread: 12,288 x 7168 bf16 rows to E4M3FN
-// codes take 98 us (6.3 TB/s, 93 % of the copy rate); without the next row's
+// codes take 96 us (6.4 TB/s, 95 % of the copy rate); without the next row's
 // early request 118, four vectors 104, one 127.
 constexpr int kNormThreadsPerSm = 1024;
 
