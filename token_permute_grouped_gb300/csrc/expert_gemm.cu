@@ -39,6 +39,10 @@
 // operands by a warp of each CTA before the MMA may read them: multiplying by
 // zero on one side alone would let another expert's infinities through.
 //
+// Where the gradients' tiles are few, or some far longer than the rest, their
+// contraction is cut into slices, each a tile of its own whose fp32 sums go to
+// the workspace; a second kernel adds them in order.
+//
 // A gated block's D_p may still be in the making when this kernel starts: the
 // kernel before it (glu_grad.cu) writes them in the order the tiles go and
 // counts the finished pieces of each 128 rows, and the producer waits for a
@@ -120,25 +124,28 @@ static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "share
 struct Tile {
     int g, m, n;
     bool weights;  // of the weights' gradient
+    int slice;     // of its contraction
 };
 
 // What a launch's tiles cover.
 struct Walk {
     int tn;       // column tiles of a tile over rows
     int wm, wn;   // row and column tiles of an expert's weights' gradient
+    int slices, w_slices;
 };
 
 // The tiles over the experts' rows, then those of the weights' gradients; of
-// each expert the row tiles in order, column tiles innermost.
+// each expert the row tiles in order, slices in them, column tiles innermost.
 __device__ __forceinline__ Tile tile_at(const Control &c, int t, const Walk &k) {
     if (t >= c.row_tiles) {
-        const int u = t - c.row_tiles, per = k.wm * k.wn, local = u % per;
-        return {u / per, local / k.wn, local % k.wn, true};
+        const int u = t - c.row_tiles, per = k.wm * k.w_slices * k.wn, local = u % per;
+        const int m = local / k.wn;
+        return {u / per, m / k.w_slices, local % k.wn, true, m % k.w_slices};
     }
     int g = 0;
     while (t >= c.g[g + 1].tile0) ++g;
-    const int local = t - c.g[g].tile0;
-    return {g, local / k.tn, local % k.tn, false};
+    const int local = t - c.g[g].tile0, m = local / k.tn;
+    return {g, m / k.slices, local % k.tn, false, m % k.slices};
 }
 
 __device__ __forceinline__ void st_global_b32x4(void *ptr, const uint32_t *r) {
@@ -172,6 +179,17 @@ __device__ __forceinline__ Block block_of(bool weights, int K, int kb) {
         return {(kb - 1) * BK, BK};
     }
     return {kb * BK, min(BK, K - kb * BK)};
+}
+
+// Contraction blocks of one slice of a tile: those from `first` on, of K's.
+struct Span {
+    int first, count;
+};
+__device__ __forceinline__ Span span_of(int K, int slice, int slices) {
+    const int blocks = (K + BK - 1) / BK;
+    if (slices == 1) return {0, blocks};
+    const int first = static_cast<int>(static_cast<int64_t>(blocks) * slice / slices);
+    return {first, static_cast<int>(static_cast<int64_t>(blocks) * (slice + 1) / slices) - first};
 }
 
 // Until the count of finished pieces reaches `want`, by one thread; then the
@@ -216,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
     // Columns of the output one tile covers; the tiles of a launch.
     const int row_n = GRAD ? BN : BN / 2, w_n = p.half_step ? BN : BN / 2;
-    const Walk walk{(p.N + row_n - 1) / row_n, (p.wM + TILE_M - 1) / TILE_M, (p.wN + w_n - 1) / w_n};
+    const Walk walk{(p.N + row_n - 1) / row_n, (p.wM + TILE_M - 1) / TILE_M, (p.wN + w_n - 1) / w_n,
+                    GRAD ? p.slices : 1, GRAD ? p.w_slices : 1};
 
     // ---- prologue: groups and tiles (warp 0), barriers (warp 1), TMEM (MMA warp)
     if (warp == 0) {
@@ -229,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         if (lane < p.e) {
             row0 = C.seg.dst[lane * p.W];
             rows = C.seg.dst[(lane + 1) * p.W] - row0;
-            tiles = good ? (rows + TILE_M - 1) / TILE_M * walk.tn : 0;
+            tiles = good ? (rows + TILE_M - 1) / TILE_M * walk.slices * walk.tn : 0;
         }
         int inc = tiles;
 #pragma unroll
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         if (lane == 0) {
             C.g[p.e] = GroupInfo{0, 0, total};
             C.row_tiles = total;
-            C.total_tiles = total + (good ? p.e * walk.wm * walk.wn : 0);
+            C.total_tiles = total + (good ? p.e * walk.wm * walk.w_slices * walk.wn : 0);
             C.abort = 0;
             if (blockIdx.x == 0) {
                 if (p.write_status) *p.status = good ? 0 : kStatusBadCounts;
@@ -283,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     const uint32_t ragged0 = smem_u32(&C.ragged[0]), cleared0 = smem_u32(&C.cleared[0]);
     const auto contraction = [&](const Tile &w) { return w.weights ? C.g[w.g].rows : p.K; };
     const auto is_ragged = [&](const Tile &w, const Block &b) { return w.weights && (b.len & 15) != 0; };
+    const auto span = [&](const Tile &w, int K) { return span_of(K, w.slice, w.weights ? walk.w_slices : walk.slices); };
     // Contraction blocks of a tile: each product's, and those of the second summands.
     const auto steps_of = [&](const Tile &w, int kblocks) {
         return GRAD ? (w.weights ? p.parts : p.phases * p.parts) * kblocks : kblocks;
@@ -297,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             for (int t = unit; t < total && ok; t += nunits) {
                 const Tile w = tile_at(C, t, walk);
                 const int K = contraction(w);
-                const int kblocks = (K + BK - 1) / BK, steps = steps_of(w, kblocks);
+                const Span ks = span(w, K);
+                const int kblocks = ks.count, steps = steps_of(w, kblocks);
                 const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
                 const int row = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM;  // this CTA's first row
                 const CUtensorMap *ta = &p.tmA[0];
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 for (int i = 0, kb = 0, phase = 0; i < steps; ++i, ++it, ++kb) {
                     const int s = it % kStages;
                     if (kb == kblocks) kb = 0, ++phase;
-                    const Block b = block_of(w.weights, K, kb);
+                    const Block b = block_of(w.weights, K, ks.first + kb);
                     if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.status,
                                           p.wait_limit_ns)) {
                         ok = false;
@@ -385,8 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         for (int t = unit; t < total && ok; t += nunits) {
             const Tile w = tile_at(C, t, walk);
             const int K = contraction(w);
-            const int kblocks = (K + BK - 1) / BK;
-            const Block b = kblocks ? block_of(w.weights, K, 0) : Block{0, 0};
+            const Span ks = span(w, K);
+            const int kblocks = ks.count;
+            const Block b = kblocks ? block_of(w.weights, K, ks.first) : Block{0, 0};
             for (int part = 0; part < (is_ragged(w, b) ? p.parts : 0) && ok; ++part) {
                 const int s = (it + part * kblocks) % kStages;
                 ok = pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns);
@@ -422,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             for (int t = unit; t < total && ok; t += nunits, ++tl) {
                 const Tile w = tile_at(C, t, walk);
                 const int K = contraction(w);
-                const int kblocks = (K + BK - 1) / BK, steps = steps_of(w, kblocks);
+                const Span ks = span(w, K);
+                const int kblocks = ks.count, steps = steps_of(w, kblocks);
                 const int acc = tl & 1;
                 // A: MN-major for the weights' gradient only; B: K-major for the rows' gradient only.
                 const bool a_is_mn = GRAD && w.weights, b_is_mn = !GRAD || w.weights;
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                         ok = false;
                         break;
                     }
-                    const Block b = block_of(w.weights, K, kb);
+                    const Block b = block_of(w.weights, K, ks.first + kb);
                     if (is_ragged(w, b)) {
                         if (!pair::wait_phase(&C.abort, cleared0 + 8 * s, (used >> s) & 1, p.status,
                                               p.wait_limit_ns)) {
@@ -495,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             } else if (valid) {  // the gradient's rows go back to their order of arrival
                 orow = source_row(C.seg, p.W, p.e, gi.row0 + row0w + lane);
             }
-            const bool zero = w.weights && gi.rows == 0;  // nothing was accumulated
+            const bool zero = GRAD && span(w, contraction(w)).count == 0;  // nothing was accumulated
+            const int slices = w.weights ? walk.w_slices : walk.slices;
             const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * BN;
             const bool wide = N % 16 == 0;
             constexpr int kChunks = GRAD ? BN / 32 : BN / 64;
@@ -536,6 +560,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = 0;
                     }
+                    if (slices > 1) {
+                        if (valid) {
+                            const int64_t m = w.weights ? (p.half_step ? 0 : half) * slices + w.slice : w.slice;
+                            float *const to = (w.weights ? p.part_w : p.part) +
+                                              (m * (w.weights ? static_cast<int64_t>(p.e) * p.wM : p.A) + orow) * N + col;
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                if (col + v * 8 < N) st_global_b32x8(to + v * 8, r + v * 8);
+                        }
+                        continue;
+                    }
                 }
                 uint32_t w16[16];
 #pragma unroll
@@ -569,6 +604,60 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
     }
 }
 
+// The gradients' slices joined: out = the sum over slices of part, in order, for
+// up to three matrices, eight values a thread.  Bound by the sums' bytes, which
+// are in L2 where there are few: 4 slices of 448 x 896, 3 us behind the GEMM.
+struct Join {
+    const float *part[3];
+    void *out[3];
+    int64_t vecs[3];  // of a slice
+    int32_t slices[3];
+    const int32_t *status;
+};
+constexpr int kJoinThreads = 128;
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Join p) {
+    pdl_trigger();
+    pdl_wait();
+    if (*p.status != 0) return;  // the slices were not all written
+    int64_t v = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+    int i = 0;
+    while (i < 3 && v >= p.vecs[i]) v -= p.vecs[i++];
+    if (i == 3) return;
+    const float4 *from = reinterpret_cast<const float4 *>(p.part[i]) + 2 * v;
+    float4 lo = __ldcs(from), hi = __ldcs(from + 1);
+#pragma unroll 4
+    for (int s = 1; s < p.slices[i]; ++s) {
+        from += 2 * p.vecs[i];
+        const float4 a = __ldcs(from), b = __ldcs(from + 1);
+        lo = make_float4(lo.x + a.x, lo.y + a.y, lo.z + a.z, lo.w + a.w);
+        hi = make_float4(hi.x + b.x, hi.y + b.y, hi.z + b.z, hi.w + b.w);
+    }
+    const f32x2 o[4] = {pair_of(lo.x, lo.y), pair_of(lo.z, lo.w), pair_of(hi.x, hi.y), pair_of(hi.z, hi.w)};
+    static_cast<uint4 *>(p.out[i])[v] = pack8<BF16>(o);
+}
+
+cudaError_t launch_join(const ExpertGemmLaunch &p, cudaStream_t stream) {
+    Join j = {};
+    int64_t total = 0;
+    const auto add = [&](int i, const float *part, void *out, int64_t values, int slices) {
+        j.part[i] = part;
+        j.out[i] = out;
+        j.vecs[i] = values / 8;
+        j.slices[i] = slices;
+        total += j.vecs[i];
+    };
+    if (p.N > 0 && p.slices > 1) add(0, p.part, p.out, static_cast<int64_t>(p.A) * p.N, p.slices);
+    const int64_t matrix = static_cast<int64_t>(p.e) * p.wM * p.wN;
+    for (int i = 0; p.wM > 0 && p.w_slices > 1 && i < (p.half_step ? 1 : 2); ++i)
+        add(1 + i, p.part_w + i * p.w_slices * matrix, p.out_w[i], matrix, p.w_slices);
+    if (total == 0) return cudaSuccess;
+    j.status = p.status;
+    const unsigned blocks = static_cast<unsigned>((total + kJoinThreads - 1) / kJoinThreads);
+    return p.bf16 ? launch_pdl(join_kernel<true>, blocks, kJoinThreads, 0, 0, stream, j)
+                  : launch_pdl(join_kernel<false>, blocks, kJoinThreads, 0, 0, stream, j);
+}
+
 template <bool BF16, bool GRAD, int ACT, int BN>
 cudaError_t launch_shape(const ExpertGemmLaunch &p, cudaStream_t stream) {
     auto kern = expert_gemm_kernel<BF16, GRAD, ACT, BN>;
@@ -593,7 +682,8 @@ cudaError_t launch_type(const ExpertGemmLaunch &p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_expert_gemm(const ExpertGemmLaunch &p, cudaStream_t stream) {
-    return p.bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
+    const cudaError_t err = p.bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
+    return err == cudaSuccess && p.grad ? launch_join(p, stream) : err;
 }
 
 // Every kind needs nearly all of an SM's shared memory: one CTA an SM.

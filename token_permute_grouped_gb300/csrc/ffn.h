@@ -90,6 +90,11 @@ struct ExpertGemmLaunch {
     int32_t grid;           // CTAs, two a cluster
     uint64_t wait_limit_ns;
     void *out, *out_w[2];   // over the rows; weights' gradients by accumulator half
+    // Gradients: equal slices that the contraction of a tile over rows, and of a weights' gradient, is cut into.
+    // Above 1, a slice's sums go to part [slices][A][N] or part_w [matrix][w_slices][e][wM][wN] and a second kernel
+    // adds them in order.
+    int32_t slices, w_slices;
+    float *part, *part_w;
     float *saved[2];        // gated: unrounded G and U, or NULL
     // tmA: the D_p by phase, then their second summands, as A; tmD: the same as B of the weights' gradient.
     CUtensorMap tmA[4], tmB[2], tmX, tmD[4];

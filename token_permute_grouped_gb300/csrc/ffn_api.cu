@@ -30,6 +30,7 @@ constexpr int64_t kSideRows = 8192;
 // / 1307, 65,308 of 2048 x 1408 (255) 474 / 484, 16,407 of 4096 x 1024 (513)
 // 168 / 193.
 constexpr int64_t kLongRun = 96;
+constexpr int64_t kPairs = 76;  // pairs of SMs, each of which has a tile at a time
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
@@ -154,24 +155,76 @@ ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, con
     return g;
 }
 
+// Tiles of the gradients, of bn accumulator columns: the rows expected, and the weights'.
+int64_t row_tiles(int32_t e, int64_t A, int64_t H1, int64_t bn) {
+    return A > 0 ? (ceil_div(A, 256) + e / 2) * ceil_div(H1, bn) : 0;
+}
+int64_t weight_tiles(int32_t e, int64_t H1, int64_t N, int phases, int64_t bn) {
+    return e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? bn / 2 : bn);
+}
+
+// Slices of the gradients' contractions (see ExpertGemmLaunch): tiles that are
+// few or far longer than the rest leave SMs idle, so their contraction is cut,
+// and the slices' sums are joined by a second kernel.  Chosen by the blocks of
+// the contraction that the fullest pair of SMs would go through, its tiles being
+// dealt out in turn, plus the joining.  Measured (us, one slice / chosen): one
+// expert, 8386 rows of 448 x 896 47.6 / 26, 16,384 of 1024 x 1024 103.6 / 58.6,
+// 2 rows over 16 experts of 256 x 3456 27.3 / 19.0.  It depends on the shapes
+// alone, since the workspace holds the sums.
+constexpr double kTileCost = 3.0;       // of a tile beside its blocks, in blocks
+constexpr double kJoinCost = 5.0;       // of the second kernel, in blocks
+constexpr double kJoinBytes = 1.4e6;    // of sums written and read again in a block's time
+struct Slices {
+    int32_t rows, weights;
+    size_t row_bytes, weight_bytes;  // of their sums
+    size_t bytes() const { return row_bytes + weight_bytes; }
+};
+Slices slices_of(int32_t e, int64_t A, int64_t H1, int64_t N, int phases, int parts) {
+    Slices best{1, 1, 0, 0};
+    if (A == 0) return best;
+    const int64_t bn = row_tiles(e, A, H1, 128) + weight_tiles(e, H1, N, phases, 128) <= kPairs ? 128 : 256;
+    const int64_t tx = row_tiles(e, A, H1, bn), tw = weight_tiles(e, H1, N, phases, bn);
+    const int64_t kx = ceil_div(N, 128), kw = ceil_div(A, static_cast<int64_t>(e) * 128);
+    const double block = bn == 256 ? 1.0 : 0.75;
+    double least = 0.0;
+    for (int32_t sx = 1; sx <= std::min<int64_t>(kx, 16); sx *= 2)
+        for (int32_t sw = 1; sw <= std::min<int64_t>(kw, 16); sw *= 2) {
+            const Slices s{sx, sw, sx > 1 ? round256(static_cast<size_t>(sx) * A * H1 * 4) : 0,
+                           sw > 1 ? round256(static_cast<size_t>(sw) * phases * e * H1 * N * 4) : 0};
+            const double x = block * phases * parts * kx / sx + kTileCost, w = block * parts * kw / sw + kTileCost;
+            const int64_t nx = tx * sx, n = nx + tw * sw;
+            double cost = 0.0;
+            for (const int64_t u : {int64_t{0}, nx % kPairs, (n + kPairs - 1) % kPairs}) {  // the fullest is one of these
+                const int64_t mine = (n - u + kPairs - 1) / kPairs, mine_x = (std::max(nx - u, int64_t{0}) + kPairs - 1) / kPairs;
+                cost = std::max(cost, mine_x * x + (mine - mine_x) * w);
+            }
+            if (s.bytes() > 0) cost += kJoinCost + s.bytes() / kJoinBytes;
+            if (least == 0.0 || cost < least) least = cost, best = s;
+        }
+    return best;
+}
+
 // Gradients of one or two products with the same rows, in one launch:
 // dX = sum_p D_p W_p^T, dW_p = X^T D_p.
-// D: by product, then the second summands (parts 2).
+// D: by product, then the second summands (parts 2).  sums: of the slices.
 a2av_status run_gradients(ExpertGemmLaunch g, int phases, int parts, int64_t H1, int64_t N, const void *const D[4],
-                          const void *X, const void *const Wt[2], void *dX, void *const dW[2], cudaStream_t stream) {
+                          const void *X, const void *const Wt[2], void *dX, void *const dW[2], uint8_t *sums,
+                          cudaStream_t stream) {
     const bool bf16 = g.bf16 != 0;
     g.grad = 1;
     g.phases = phases;
     g.parts = parts;
     g.one_a = g.one_b = N % 64 == 0;
     g.one_x = H1 % 64 == 0;
-    const auto count = [&](int64_t bn) {
-        int64_t n = 0;
-        if (dX && g.A > 0) n += (ceil_div(g.A, 256) + g.e / 2) * ceil_div(H1, bn);
-        if (dW[0]) n += g.e * ceil_div(H1, 256) * ceil_div(N, phases == 2 ? bn / 2 : bn);
-        return n;
+    const auto count = [&](int64_t bn, int64_t slices, int64_t w_slices) {
+        return (dX ? slices * row_tiles(g.e, g.A, H1, bn) : 0) + (dW[0] ? w_slices * weight_tiles(g.e, H1, N, phases, bn) : 0);
     };
-    g.bn = pick_bn(count(128));
+    const Slices s = slices_of(g.e, g.A, H1, N, phases, parts);
+    g.slices = s.rows;
+    g.w_slices = s.weights;
+    g.part = reinterpret_cast<float *>(sums);
+    g.part_w = reinterpret_cast<float *>(sums + s.row_bytes);
+    g.bn = pick_bn(count(128, 1, 1));
     g.half_step = phases == 2 ? 0 : g.bn / 2;
     const uint32_t b_cols = g.bn / 2;  // columns of B a CTA stages
     for (int p = 0; p < phases * parts && g.A > 0; ++p)
@@ -191,7 +244,7 @@ a2av_status run_gradients(ExpertGemmLaunch g, int phases, int parts, int64_t H1,
         for (int i = 0; i < 2; ++i) g.out_w[i] = dW[phases == 2 ? i : 0];  // by accumulator half
         if (g.A > 0 && !operand_map(&g.tmX, X, 1, g.A, H1, bf16, g.one_x)) return A2AV_ERR_CUDA;
     }
-    g.grid = gemm_grid(count(g.bn) + g.e * ceil_div(H1, g.bn));  // (without a tile the launch still stores the status)
+    g.grid = gemm_grid(count(g.bn, s.rows, s.weights) + g.e * ceil_div(H1, g.bn) * s.rows);  // (without a tile the launch still stores the status)
     return a2av::launch_expert_gemm(g, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 
@@ -334,7 +387,9 @@ a2av_status a2av_gated_workspace_size(const a2av_gated_desc *desc, size_t *bytes
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + pieces_bytes(desc) + std::max(staged_bytes(desc), 2 * slope_parts(desc) * slope_bytes(desc));
+    size_t back = 2 * slope_parts(desc) * slope_bytes(desc);
+    if (desc->save) back += slices_of(desc->e, desc->A, desc->H1, desc->N, 2, slope_parts(desc)).bytes();
+    *bytes = kStatusBytes + pieces_bytes(desc) + std::max(staged_bytes(desc), back);
     return A2AV_OK;
 }
 
@@ -472,7 +527,8 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
     const void *const D[4] = {dG, dU, slopes + 2 * slope_bytes(desc), slopes + 3 * slope_bytes(desc)};
     const void *const Wt[2] = {gateWeight, upWeight};
     void *const dW[2] = {dGate, dUp};
-    return run_gradients(g, 2, parts, d.H1, d.N, D, permuteOut, Wt, dAtaOut, dW, stream);
+    return run_gradients(g, 2, parts, d.H1, d.N, D, permuteOut, Wt, dAtaOut, dW, slopes + 2 * parts * slope_bytes(desc),
+                         stream);
 }
 
 a2av_status a2av_gmm_backward_workspace_size(const a2av_gmm_desc *desc, size_t *bytes) {
@@ -481,7 +537,7 @@ a2av_status a2av_gmm_backward_workspace_size(const a2av_gmm_desc *desc, size_t *
     const a2av_status s = a2av_gmm_workspace_size(desc, &unused);  // the shapes' limits
     if (s != A2AV_OK) return s;
     if (desc->BS != 0) return A2AV_ERR_INVALID;
-    *bytes = kStatusBytes;
+    *bytes = kStatusBytes + slices_of(desc->e, desc->A, desc->H1, desc->N1, 1, 1).bytes();
     return A2AV_OK;
 }
 
@@ -504,7 +560,7 @@ a2av_status a2av_gmm_backward(const a2av_gmm_desc *desc, const void *dY, const v
     const void *const D[4] = {dY, nullptr, nullptr, nullptr}, *const Wt[2] = {gmmWeight, nullptr};
     void *const dW[2] = {dWeight, nullptr};
     return run_gradients(g, 1, 1, d.H1, d.N1, D, permuteOut, Wt, dAtaOut, dW,
-                         reinterpret_cast<cudaStream_t>(stream_handle));
+                         static_cast<uint8_t *>(workspace) + kStatusBytes, reinterpret_cast<cudaStream_t>(stream_handle));
 }
 
 }  // extern "C"
