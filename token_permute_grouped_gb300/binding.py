@@ -486,9 +486,12 @@ def _rows_of(t, name):
     return code, step if rows > 1 else cols
 
 
-def _out(t, name, dtype, shape, like):
-    """The caller's output tensor, checked, or a new one on `like`'s device."""
+def _out(t, name, dtype, shape, like, stream):
+    """The caller's output tensor, checked, or a new one on `like`'s device, of the stream that writes it."""
     if t is None:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return torch.empty(shape, dtype=dtype, device=like.device)
         if like.shape == shape and like.dtype == dtype and like.is_contiguous():
             return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -502,12 +505,12 @@ def _named(table, key, what):
     return table[key]
 
 
-def _code_outputs(out, rows, cols, mode, like):
+def _code_outputs(out, rows, cols, mode, like, stream):
     """(codes, scales) to write: those of an earlier result, or new ones."""
     mx = mode == "mx"
-    return (_out(out.codes if out else None, "codes", torch.uint8, (rows, cols), like),
+    return (_out(out.codes if out else None, "codes", torch.uint8, (rows, cols), like, stream),
             _out(out.scales if out else None, "scales", torch.uint8 if mx else torch.float32,
-                 (rows, cols // (32 if mx else 128)), like))
+                 (rows, cols // (32 if mx else 128)), like, stream))
 
 
 class _RmsNormFields(NamedTuple):
@@ -544,14 +547,14 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
               _at(scales), _at(rstd), _on(stream, x))
         return out
     q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
-    h = None if residual is None else _out(out.h if out else None, "h", dtype, shape, x)
+    h = None if residual is None else _out(out.h if out else None, "h", dtype, shape, x, stream)
     y = codes = scales = rstd = None
     if want_y or (want_y is None and qtype is None):
-        y = _out(out.y if out else None, "y", dtype, shape, x)
+        y = _out(out.y if out else None, "y", dtype, shape, x, stream)
     if want_rstd:
-        rstd = _out(out.rstd if out else None, "rstd", torch.float32, (rows,), x)
+        rstd = _out(out.rstd if out else None, "rstd", torch.float32, (rows,), x, stream)
     if qtype is not None:
-        codes, scales = _code_outputs(out, rows, H, mode, x)
+        codes, scales = _code_outputs(out, rows, H, mode, x, stream)
     desc = ctypes.byref(RmsNormDesc(rows, H, xs, rs or 0, code, q, m, eps))
     _call("a2av_rms_norm", desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
           _at(codes), _at(scales), _at(rstd), _on(stream, x))
@@ -577,11 +580,11 @@ def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, wo
         _is(dh, "dh", dtype, shape)
     _is(gamma, "gamma", dtype, (H,))
     _is(rstd, "rstd", torch.float32, (rows,))
-    dx = _out(dx, "dx", dtype, shape, dy)
-    dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy)
+    dx = _out(dx, "dx", dtype, shape, dy, stream)
+    dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy, stream)
     need = _norm_backward_size(rows, H, code)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        workspace = _out(None, "workspace", torch.uint8, (need,), dy, stream)
     _call("a2av_rms_norm_backward", rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd), _at(dx),
           _at(dgamma), _at(workspace), 0 if workspace is None else workspace.numel(), _on(stream, dy))
     return dx, dgamma
@@ -618,9 +621,9 @@ def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, 
     desc = ctypes.byref(GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode")))
     codes = scales = h = None
     if qtype is not None:
-        codes, scales = _code_outputs(out, rows, N, mode, gate_up)
+        codes, scales = _code_outputs(out, rows, N, mode, gate_up, stream)
     if want_h or (want_h is None and qtype is None):
-        h = _out(out.h if out else None, "h", gate_up.dtype, (rows, N), gate_up)
+        h = _out(out.h if out else None, "h", gate_up.dtype, (rows, N), gate_up, stream)
     _call("a2av_glu_quant", desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
           _on(stream, gate_up))
     result = GluQuantOut(codes, scales, h)
@@ -642,7 +645,8 @@ class GatedGrads(NamedTuple):
 
 class GatedPlan:
     """Descriptor + workspace of the gated block h = act(X Wg) * (X Wu) over ragged experts, and its backward pass,
-    for one shape.  save: keep what the backward pass needs (with several sources that includes permuteOut)."""
+    for one shape.  save: keep what the backward pass needs (with several sources that includes permuteOut).  The
+    workspace serves one call at a time: calls of one plan on different streams have to be ordered by the caller."""
 
     def __init__(self, W, e, A, H1, N, dtype=torch.bfloat16, act="silu", save=False, want_permute_out=None,
                  device=None):
@@ -669,9 +673,9 @@ class GatedPlan:
         A, H1, N = d.A, d.H1, d.N
         _is(ataOut, "ataOut", dtype, (A, H1))
         self._check_shared(recvCounts, gateWeight, upWeight)
-        h = _out(h, "h", dtype, (A, N), ws)
-        saved = _out(saved, "saved", torch.float32, (2, A, N), ws) if d.save else None
-        permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ataOut) if d.want_permute_out else None
+        h = _out(h, "h", dtype, (A, N), ws, stream)
+        saved = _out(saved, "saved", torch.float32, (2, A, N), ws, stream) if d.save else None
+        permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ataOut, stream) if d.want_permute_out else None
         _call("a2av_gated_run", ctypes.byref(d), ataOut.data_ptr(), recvCounts.data_ptr(), gateWeight.data_ptr(),
               upWeight.data_ptr(), _at(permuted), h.data_ptr(), _at(saved), ws.data_ptr(), ws.numel(),
               _on(stream, ws))
@@ -685,9 +689,9 @@ class GatedPlan:
         _is(permuteOut, "permuteOut", dtype, (A, H1))
         self._check_shared(recvCounts, gateWeight, upWeight)
         _is(saved, "saved", torch.float32, (2, A, N))
-        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut) if want_rows else None
-        gate = _out(dGate, "dGate", dtype, (d.e, H1, N), gateWeight) if want_weights else None
-        up = _out(dUp, "dUp", dtype, (d.e, H1, N), upWeight) if want_weights else None
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut, stream) if want_rows else None
+        gate = _out(dGate, "dGate", dtype, (d.e, H1, N), gateWeight, stream) if want_weights else None
+        up = _out(dUp, "dUp", dtype, (d.e, H1, N), upWeight, stream) if want_weights else None
         _call("a2av_gated_backward", ctypes.byref(d), dh.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
               gateWeight.data_ptr(), upWeight.data_ptr(), saved.data_ptr(), _at(rows), _at(gate), _at(up),
               ws.data_ptr(), ws.numel(), _on(stream, ws))
@@ -713,8 +717,8 @@ class GmmBackwardPlan:
         _is(permuteOut, "permuteOut", dtype, (A, H1))
         _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
         _is(gmmWeight, "gmmWeight", dtype, (d.e, H1, N1))
-        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut) if want_rows else None
-        weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), gmmWeight) if want_weights else None
+        rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut, stream) if want_rows else None
+        weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), gmmWeight, stream) if want_weights else None
         _call("a2av_gmm_backward", ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
               gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel(), _on(stream, ws))
         return rows, weights
