@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             for (int i = 0; i < kStages && ok; ++i, ++it)
                 ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % kStages), ((it / kStages) & 1) ^ 1, p.status,
                                       p.wait_limit_ns);
+            if (!ok) pair::let_settle();
         }
     } else if (warp == kClearWarp && GRAD) {
         // ============================================= ragged rows of the block

@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             for (int i = 0; i < S::kStages && ok; ++i, ++it)
                 ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % S::kStages), ((it / S::kStages) & 1) ^ 1, p.status,
                                       p.wait_limit_ns);
+            if (!ok) pair::let_settle();
         }
     } else if (warp >= kCopyWarp0) {
         // ================================================== producer (rows of x)
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                         pack2<BF16>(mul2(act_value<ACT>(pair_of(g[0].z, g[0].w)), pair_of(u[0].z, u[0].w))));
                 }
             }
+            if (S::kShared) fence_proxy_async_smem();  // TMA writes over the part next
             __syncwarp();
             if (lane == 0)
                 for (int c = 0; c < split; ++c) pair::arrive_reads_done(pair::map_to_rank(freed, c));

@@ -71,6 +71,13 @@ static __device__ __noinline__ bool wait_phase(int32_t *abort_flag, uint32_t bar
     }
 }
 
+// After a wait was given up: a millisecond for the copies and products still in
+// flight, which take microseconds, before shared memory and TMEM are given back.
+static __device__ __noinline__ void let_settle() {
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < 100000 && global_timer_ns() - t0 < 1000000; ++i) __nanosleep(1000);
+}
+
 // TMA loads whose barrier may live in the peer CTA.
 __device__ __forceinline__ void load_3d(uint32_t dst, const void *tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
     asm volatile(
