@@ -45,19 +45,22 @@ __device__ __forceinline__ f32x2 finite_part(f32x2 v) {
     return pair_of(fabsf(a) < __uint_as_float(0x7f800000u) ? a : 0.0f, fabsf(b) < __uint_as_float(0x7f800000u) ? b : 0.0f);
 }
 
-// A block of 128 rows is contiguous in every tensor: its vectors are taken in
-// pieces of kFlatVecs.
+// Counted, a block of 128 rows, which is contiguous in every tensor, is taken in
+// pieces of kFlatVecs; otherwise all rows are one block and a piece is a vector
+// a thread, so that few rows spread over the SMs (5013 x 328 values 9.5 us with
+// pieces of kFlatVecs, 6 so).
 template <bool BF16, int ACT>
 __global__ void __launch_bounds__(kGradThreads) glu_grad_kernel(const GluGradLaunch p) {
     pdl_wait();
     pdl_trigger();
-    const int64_t per_block = static_cast<int64_t>(kRows) * (p.N / 8), total = static_cast<int64_t>(p.rows) * (p.N / 8);
-    const int pieces = static_cast<int>((per_block + kFlatVecs - 1) / kFlatVecs);
-    const int blocks = (p.rows + kRows - 1) / kRows;
-    for (int64_t i = blockIdx.x; i < static_cast<int64_t>(blocks) * pieces; i += gridDim.x) {
-        const int64_t block = i / pieces;
-        const int64_t v0 = block * per_block + (i - block * pieces) * kFlatVecs;
-        const int64_t end = min(min(v0 + kFlatVecs, (block + 1) * per_block), total);
+    const int64_t total = static_cast<int64_t>(p.rows) * (p.N / 8);
+    const int64_t per_block = p.pieces ? static_cast<int64_t>(kRows) * (p.N / 8) : total;
+    const int size = p.pieces ? kFlatVecs : kGradThreads;
+    const int64_t pieces = (per_block + size - 1) / size, blocks = (total + per_block - 1) / per_block;
+    for (int64_t i = blockIdx.x; i < blocks * pieces; i += gridDim.x) {
+        const int64_t block = p.pieces ? i / pieces : 0;
+        const int64_t v0 = block * per_block + (i - block * pieces) * size;
+        const int64_t end = min(min(v0 + size, (block + 1) * per_block), total);
         if (v0 >= end) continue;  // (the last block may have fewer pieces)
 #pragma unroll 2
         for (int64_t v = v0 + threadIdx.x; v < end; v += kGradThreads) {
@@ -114,7 +117,9 @@ int glu_grad_pieces(int64_t rows, int64_t N) {
 }
 
 cudaError_t launch_glu_grad(const GluGradLaunch &p, bool bf16, int act, int sms, cudaStream_t stream) {
-    const int64_t items = (static_cast<int64_t>(p.rows) + kRows - 1) / kRows * glu_grad_pieces(kRows, p.N);
+    const int64_t values = static_cast<int64_t>(p.rows) * p.N, per = 8 * kGradThreads;
+    const int64_t items = p.pieces ? (static_cast<int64_t>(p.rows) + kRows - 1) / kRows * glu_grad_pieces(kRows, p.N)
+                                   : (values + per - 1) / per;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, p.pieces ? sms : sms * 8));
     const auto kern = bf16 ? (act == A2AV_ACT_SILU ? glu_grad_kernel<true, A2AV_ACT_SILU>
                                                    : glu_grad_kernel<true, A2AV_ACT_GELU_TANH>)
