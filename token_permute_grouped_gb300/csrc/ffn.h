@@ -111,6 +111,7 @@ struct GatedRowsLaunch {
     float *saved[2];
     int32_t *status;
     uint64_t wait_limit_ns;
+    int32_t after_permute;  // runs beside the permute kernel before it, which has cleared the status word
     int32_t split, grid;  // set by the launch: CTAs of a cluster, CTAs
     int32_t guess;        // likewise: experts taken to have rows before they are counted (all, or 0)
     const void *x;            // ataOut

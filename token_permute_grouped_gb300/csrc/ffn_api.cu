@@ -414,7 +414,7 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
     if (sms <= 0) return A2AV_ERR_CUDA;
 
     if (few_rows(d)) {
-        if (d.want_permute_out) {  // for the backward pass; this kernel gathers the rows itself
+        if (d.want_permute_out) {  // for the backward pass; this kernel gathers the rows itself, beside the permute
             a2av::PermuteLaunch pl{recvCounts, d.W, d.e, static_cast<int32_t>(d.A), static_cast<int32_t>(d.H1), ataOut,
                                    permuteOut, static_cast<int32_t *>(workspace), 1, 0, 8};
             if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
@@ -434,6 +434,7 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
             r.saved[1] = saved + d.A * d.N;
         }
         r.status = static_cast<int32_t *>(workspace);
+        r.after_permute = d.want_permute_out;
         r.wait_limit_ns = kWaitLimitNs;
         r.x = ataOut;
         if (!operand_map(&r.tmGate, gateWeight, d.e, d.H1, d.N, bf16, false) ||

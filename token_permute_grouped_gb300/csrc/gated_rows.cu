@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const int rank = static_cast<int>(pair::cluster_rank());
     const int strips = (p.N + kCols - 1) / kCols;
     if (warp == 0) {
-        pdl_wait();
+        // (The permute kernel was launched after all before it had completed, and
+        // nothing that it writes is read here.)
+        if (!p.after_permute) pdl_wait();
         const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int rows = 0;
         if (lane < p.e && good) rows = C.seg.dst[(lane + 1) * p.W] - C.seg.dst[lane * p.W];
@@ -169,7 +171,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
         if (lane == 0) {
             C.n_active = __popc(mask);
             C.abort = 0;
-            if (blockIdx.x == 0) *p.status = good ? 0 : kStatusBadCounts;
+            if (blockIdx.x == 0) {
+                if (!p.after_permute) *p.status = good ? 0 : kStatusBadCounts;
+                else if (!good) atomicOr(p.status, kStatusBadCounts);
+            }
         }
     } else if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(&C.tmem_base), S::kTmemCols);
@@ -241,6 +246,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                 }
             }
             pdl_trigger();
+            if (p.after_permute) pdl_wait();
             for (int i = 0; i < S::kStages && ok; ++i, ++it)
                 ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % S::kStages), ((it / S::kStages) & 1) ^ 1, p.status,
                                       p.wait_limit_ns);
