@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "liba2av_gmm.so")
 CHECKS_LIB = os.path.join(PKG, "liba2av_gmm_checks.so")
 CHECKS_SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu"]
 SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu", "grouped_gemm_mx.cu", "amp.cu", "quant_reduce.cu", "ffn_api.cu",
-           "rms_norm.cu", "glu.cu", "expert_gemm.cu", "gated_rows.cu", "glu_grad.cu"]
+           "rms_norm.cu", "glu.cu", "expert_gemm.cu", "gated_rows.cu", "glu_grad.cu", "stage_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

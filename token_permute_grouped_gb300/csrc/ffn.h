@@ -50,6 +50,16 @@ struct GluLaunch {
 };
 cudaError_t launch_glu_quant(GluLaunch p, bool bf16, int act, int kind, cudaStream_t stream);
 
+// All rows in expert-major order; clears the status word (stage_rows.cu).
+struct StageRowsLaunch {
+    const int32_t *recvCounts;
+    int32_t W, e, A, H1;
+    const void *src;
+    void *dst;
+    int32_t *status;
+};
+cudaError_t launch_stage_rows(const StageRowsLaunch &p, int sms, cudaStream_t stream);
+
 // dG = dh U act'(G), dU = dh act(G) for [rows, N] values.
 struct GluGradLaunch {
     int32_t rows, N;
@@ -84,7 +94,7 @@ struct ExpertGemmLaunch {
     int32_t bn;             // accumulator columns of a tile: 256 or 128
     const int32_t *pieces;  // gradient: the D_p are in the making beside this kernel (glu_grad.cu)
     int32_t row_pieces, last_pieces;  // pieces of 128 rows; of the last block of A
-    int32_t after_permute;  // gated: launched to overlap the permute kernel before it
+    int32_t after_permute;  // gated: launched to overlap the kernel before it, which stages the rows
     int32_t *status;
     int32_t write_status;
     int32_t grid;           // CTAs, two a cluster
@@ -111,7 +121,7 @@ struct GatedRowsLaunch {
     float *saved[2];
     int32_t *status;
     uint64_t wait_limit_ns;
-    int32_t after_permute;  // runs beside the permute kernel before it, which has cleared the status word
+    int32_t after_permute;  // runs beside the kernel before it, which stages the rows and has cleared the status word
     int32_t split, grid;  // set by the launch: CTAs of a cluster, CTAs
     int32_t guess;        // likewise: experts taken to have rows before they are counted (all, or 0)
     const void *x;            // ataOut

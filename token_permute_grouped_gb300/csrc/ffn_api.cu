@@ -415,9 +415,10 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
 
     if (few_rows(d)) {
         if (d.want_permute_out) {  // for the backward pass; this kernel gathers the rows itself, beside the permute
-            a2av::PermuteLaunch pl{recvCounts, d.W, d.e, static_cast<int32_t>(d.A), static_cast<int32_t>(d.H1), ataOut,
-                                   permuteOut, static_cast<int32_t *>(workspace), 1, 0, 8};
-            if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+            const a2av::StageRowsLaunch sl{recvCounts, d.W,        d.e,
+                                           static_cast<int32_t>(d.A), static_cast<int32_t>(d.H1),
+                                           ataOut,     permuteOut, static_cast<int32_t *>(workspace)};
+            if (a2av::launch_stage_rows(sl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         }
         const bool bf16 = d.dtype == A2AV_BF16;
         a2av::GatedRowsLaunch r;
@@ -461,8 +462,11 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
         void *dst = d.want_permute_out ? permuteOut
                                        : static_cast<uint8_t *>(workspace) + kStatusBytes + pieces_bytes(desc);
         g.direct_halves = !d.want_permute_out && d.A >= kLongRun * d.W * d.e;
-        a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, g.direct_halves, 8};
-        if (a2av::launch_permute(pl, sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        const a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status, 1, 1, 8};
+        const a2av::StageRowsLaunch sl{recvCounts, d.W, d.e, g.A, g.K, ataOut, dst, g.status};
+        if ((g.direct_halves ? a2av::launch_permute(pl, sms, stream) : a2av::launch_stage_rows(sl, sms, stream)) !=
+            cudaSuccess)
+            return A2AV_ERR_CUDA;
         g.after_permute = 1;
         g.write_status = 0;
         rows = dst;

@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const int rank = static_cast<int>(pair::cluster_rank());
     const int strips = (p.N + kCols - 1) / kCols;
     if (warp == 0) {
-        // (The permute kernel was launched after all before it had completed, and
-        // nothing that it writes is read here.)
+        // (The kernel that stages the rows let this one start after all before it had
+        // completed, and nothing that it writes is read here.)
         if (!p.after_permute) pdl_wait();
         const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
         int rows = 0;
