@@ -192,7 +192,9 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
  * call of their own with W = e = 1); want_permute_out, path and tiles are not
  * looked at.  dY [A, N1] expert-major, permuteOut [A, H1]; dAtaOut [A, H1]:
  * dPermuteOut's rows back in rank-major order; dWeight [e, H1, N1].  Either
- * output may be NULL.  The workspace holds the device status word.
+ * output may be NULL.  The workspace holds the device status word and, where a
+ * gradient has few tiles over a long contraction, the float32 sums of the
+ * contraction's slices, which are added in order.
  */
 a2av_status a2av_gmm_backward_workspace_size(const a2av_gmm_desc *desc, size_t *bytes);
 a2av_status a2av_gmm_backward(const a2av_gmm_desc *desc, const void *dY, const void *permuteOut,
