@@ -92,3 +92,22 @@ def test_gated_block():
     ref = xe.t() @ dG
     lim = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + (sizes[1] + 8) * 2.0 ** -23) * (xe.abs().t() @ dG.abs())
     assert bool(((b.dGate[1, :, cols].double() - ref).abs() <= lim).all())
+
+
+def test_staged_rows():
+    W, e, H1, N = 3, 2, 16384, 64
+    A = 140_000  # 2.3e9 values
+    counts = torch.tensor([30_000, 20_001, 1, 49_998, 25_000, 15_000], dtype=torch.int32)
+    assert int(counts.sum()) == A
+    x, wg, wu = filled(A, H1, seed=9), filled(e, H1, N, seed=10, std=H1 ** -0.5), filled(e, H1, N, seed=11, std=H1 ** -0.5)
+    plan = binding.GatedPlan(W, e, A, H1, N, save=True)
+    t = plan.run(x, counts.to(DEV), wg, wu)
+    assert binding.a2av_gmm_read_device_status(plan.workspace) == (0, 0)
+    idx, sizes = R.arrival_index(counts.tolist(), W, e)
+    for i in range(0, A, 10_000):
+        part = x[idx[i:i + 10_000].to(DEV)]
+        assert torch.equal(t.permuteOut[i:i + 10_000].view(torch.int16), part.view(torch.int16))
+    for k in (0, sizes[0] - 1, sizes[0], A - 1):
+        j = int(k >= sizes[0])
+        f = R.gated(x[idx[k]:idx[k] + 1].cpu(), [1], 1, 1, wg[j:j + 1].cpu(), wu[j:j + 1].cpu(), "silu")
+        R.assert_rounded(t.h[k:k + 1], f["h"], f["eh"], "h")
