@@ -59,8 +59,9 @@ def test_glu_quant():
     R.assert_codes(r.codes[at], r.scales[at], v, R.CHAIN, "e5m2", "group128", "codes")
 
 
-def test_gated_block():
-    W, e, H1, N = 3, 2, 64, 2048
+@pytest.mark.parametrize("H1", [64, 1024])  # slopes before the gradients' GEMM; beside it
+def test_gated_block(H1):
+    W, e, N = 3, 2, 2048
     A = 540_000  # saved: 2.2e9 values
     counts = torch.tensor([150_000, 70_001, 1, 199_998, 100_000, 20_000], dtype=torch.int32)
     assert int(counts.sum()) == A

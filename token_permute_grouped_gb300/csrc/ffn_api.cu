@@ -19,11 +19,16 @@ using a2av::ExpertGemmLaunch;
 constexpr size_t kStatusBytes = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
 constexpr int kMaxDevices = 64;
-// Rows from which the slopes of a backward pass are computed beside its GEMM.
-// (65,308 rows of 2048 x 1408, forward and backward: 1550 us, 1715 one after
-// the other; 5013 rows of 1032 x 328: 99 against 97, the counts' reset and the
-// single block an SM cost more than they hide.)
-constexpr int64_t kSideRows = 8192;
+// Whether the slopes of a backward pass are computed beside its GEMM, which hides
+// them but leaves them one block an SM: where that GEMM is long, in each of its
+// contractions too.  Measured (us, one after the other / beside; rows x H1 x N of
+// a whole training step): 20,000 x 2048 x 1408 565 / 531, 20,000 x 768 x 1408 288
+// / 270, 8917 x 2048 x 1408 294 / 289, 2500 x 4096 x 4096 451 / 445; 10,000 x
+// 1024 x 1024 128 / 131, 60,000 x 512 x 1024 493 / 501, 30,000 x 4096 x 256 312 /
+// 320, 60,000 x 256 x 512 213 / 241.
+bool slopes_beside(int64_t A, int64_t H1, int64_t N) {
+    return static_cast<double>(A) * H1 * N >= 2e10 && H1 >= 768 && N >= 512;
+}
 // Mean rows of a (source, expert) run from which whole halves are read in place
 // (us, in place / all rows staged; mean run): 5013 rows of 1032 x 328 (20) 36.7
 // / 32.6, 20,000 of 2048 x 1408 (78) 177 / 169, 34,502 of 7168 x 2048 (135) 1285
@@ -515,10 +520,10 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
     const int parts = slope_parts(desc);
     void *const dG = slopes, *const dU = slopes + slope_bytes(desc);
     if (d.A > 0) {
-        // Side by side with the GEMM where the rows' gradient gives it something
-        // to do before all slopes are there, and there is enough to hide.
+        // (Without the rows' gradient the GEMM has nothing to do before all slopes
+        // are there.)
         int32_t *pieces = nullptr;
-        if (dAtaOut && d.A >= kSideRows) {
+        if (dAtaOut && slopes_beside(d.A, d.H1, d.N)) {
             pieces = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
             if (cudaMemsetAsync(pieces, 0, pieces_bytes(desc), stream) != cudaSuccess) return A2AV_ERR_CUDA;
         }
