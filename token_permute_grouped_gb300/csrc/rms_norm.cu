@@ -100,10 +100,12 @@ __global__ void __launch_bounds__(MAXT) rms_norm_kernel(const RmsNormLaunch p) {
         }
     };
     int flip = 0;
+    const int step = gridDim.x;
+    const int last = p.rows - step;  // rows below it have a next one (row + step may not fit an int)
     pdl_trigger();
     pdl_wait();
     if (PRE) load(blockIdx.x);
-    for (int row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    for (int row = blockIdx.x; row < p.rows; row = row < last ? row + step : p.rows, flip ^= 1) {
         const size_t out0 = static_cast<size_t>(row) * vecs;
         if (!PRE) load(row);
         f32x2 s[VPT][4];
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_kernel(const RmsNormLaunch p) {
                 }
             }
         }
-        if (PRE && row + static_cast<int>(gridDim.x) < p.rows) load(row + gridDim.x);
+        if (PRE && row < last) load(row + step);
         f32x2 sum2 = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -239,17 +241,17 @@ __global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLa
         }
     };
     int flip = 0;
-    const int step = gridDim.x * R;
+    const int step = gridDim.x * R, last = p.rows - step;  // as above
     int row = blockIdx.x * R + g;
     pdl_wait();
     if (PRE && row < p.rows) load(row, na, nn, nd, nrstd);
-    for (; row < p.rows; row += step, flip ^= 1) {
+    for (; row < p.rows; row = row < last ? row + step : p.rows, flip ^= 1) {
         const size_t r0 = static_cast<size_t>(row) * vecs;
         if (PRE) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) a[k] = na[k], n[k] = nn[k], d[k] = nd[k];
             rstd = nrstd;
-            if (row + step < p.rows) load(row + step, na, nn, nd, nrstd);
+            if (row < last) load(row + step, na, nn, nd, nrstd);
         } else {
             load(row, a, n, d, rstd);
         }
