@@ -186,7 +186,7 @@ struct Span {
     int first, count;
 };
 __device__ __forceinline__ Span span_of(int K, int slice, int slices) {
-    const int blocks = (K + BK - 1) / BK;
+    const int blocks = blocks_of(K, BK);
     if (slices == 1) return {0, blocks};
     const int first = static_cast<int>(static_cast<int64_t>(blocks) * slice / slices);
     return {first, static_cast<int>(static_cast<int64_t>(blocks) * (slice + 1) / slices) - first};
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         if (lane < p.e) {
             row0 = C.seg.dst[lane * p.W];
             rows = C.seg.dst[(lane + 1) * p.W] - row0;
-            tiles = good ? (rows + TILE_M - 1) / TILE_M * walk.slices * walk.tn : 0;
+            tiles = good ? blocks_of(rows, TILE_M) * walk.slices * walk.tn : 0;
         }
         int inc = tiles;
 #pragma unroll
@@ -320,10 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                 const Span ks = span(w, K);
                 const int kblocks = ks.count, steps = steps_of(w, kblocks);
                 const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
-                const int row = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM;  // this CTA's first row
+                // This CTA's first row; without a row of its own, any one (nothing of it is stored).
+                const int from = w.m * TILE_M + static_cast<int>(rank) * BM;
+                const bool live = from < C.g[w.g].rows;
+                const int row = C.g[w.g].row0 + (live ? from : 0);
                 const CUtensorMap *ta = &p.tmA[0];
                 int arow = row;
-                if (!GRAD && p.direct_halves && row < g_end && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
+                if (!GRAD && p.direct_halves && live && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
                     // A half whose rows of this group lie in one (source, expert)
                     // run is read where it arrived.
                     ta = &p.tmDirect;
@@ -332,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
                     if (!GRAD || w.weights) {  // staged rows, or all rows contracted
                         pdl_wait();
                         all_there = true;
-                    } else if (row < g_end) {
-                        for (int c = row / BM; c <= (min(row + BM, g_end) - 1) / BM && ok; ++c)
+                    } else if (live) {
+                        for (int c = row / BM; c <= (run_end(row, BM, g_end) - 1) / BM && ok; ++c)
                             ok = wait_pieces(&C.abort, p.pieces + c, c == p.A / BM ? p.last_pieces : p.row_pieces, p.status,
                                              p.wait_limit_ns);
                         if (!ok) break;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             if (w.weights) {
                 orow = static_cast<int64_t>(w.g) * p.wM + row0w + lane;
             } else if constexpr (!GRAD) {
-                orow = gi.row0 + row0w + lane;
+                orow = static_cast<int64_t>(gi.row0) + row0w + lane;
             } else if (valid) {  // the gradient's rows go back to their order of arrival
                 orow = source_row(C.seg, p.W, p.e, gi.row0 + row0w + lane);
             }

@@ -90,8 +90,8 @@ __global__ void __launch_bounds__(kPermuteThreads)
             const int hi = i / per_half, rem = i - hi * per_half;
             const int r = rem / ppr;
             const int2 span = halves.span[hi];
-            const int d = span.x + r;
-            if (d < span.y) copy_piece(d, segment_of(table, W, e, d), rem - r * ppr);
+            if (r < span.y - span.x)
+                copy_piece(span.x + r, segment_of(table, W, e, span.x + r), rem - r * ppr);
         }
     } else {
         const int64_t items = static_cast<int64_t>(A) * ppr;
@@ -128,7 +128,7 @@ int permute_blocks_per_sm() {
 }  // namespace
 
 cudaError_t launch_permute(const PermuteLaunch &p, int num_sms, cudaStream_t stream) {
-    int blocks = (p.A + kPermuteWarps - 1) / kPermuteWarps;
+    int blocks = p.A / kPermuteWarps + (p.A % kPermuteWarps != 0 ? 1 : 0);
     // At most the blocks that are resident at once, so that none waits for a
     // second wave.
     const int resident = permute_blocks_per_sm();

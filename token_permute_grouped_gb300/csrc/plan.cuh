@@ -33,6 +33,14 @@ __device__ __forceinline__ bool in_bounds(bool ok, int32_t *status) {
 __device__ __forceinline__ constexpr bool in_bounds(bool, int32_t *) { return true; }
 #endif
 
+// Blocks of n rows that hold `rows` rows; the end of the n rows from `first` on,
+// at most `end` (first <= end).  Rows count up to 2^31 - 1, so a sum past them
+// does not fit an int.
+__device__ __forceinline__ int32_t blocks_of(int32_t rows, int32_t n) { return rows / n + (rows % n != 0 ? 1 : 0); }
+__device__ __forceinline__ int32_t run_end(int32_t first, int32_t n, int32_t end) {
+    return end - first > n ? first + n : end;
+}
+
 struct SegmentTable {
     int32_t src[kMaxSegments];      // rank-major index -> first ataOut row
     int32_t dst[kMaxSegments + 1];  // expert-major index -> first permuteOut row; dst[E] = A
@@ -121,7 +129,7 @@ constexpr int kHalfRows = 128;
 
 __device__ __forceinline__ bool half_in_one_segment(const SegmentTable &t, int W, int e, int32_t first,
                                                     int32_t group_end) {
-    const int32_t last = min(first + kHalfRows, group_end) - 1;
+    const int32_t last = run_end(first, kHalfRows, group_end) - 1;
     return segment_of(t, W, e, first) == segment_of(t, W, e, last);
 }
 
@@ -145,7 +153,7 @@ __device__ __forceinline__ void list_staged_halves(const SegmentTable &t, int W,
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, nwarps = blockDim.x / 32;
     if (warp == 0) {
         int nh = 0;
-        if (lane < e) nh = (t.dst[(lane + 1) * W] - t.dst[lane * W] + kHalfRows - 1) / kHalfRows;
+        if (lane < e) nh = blocks_of(t.dst[(lane + 1) * W] - t.dst[lane * W], kHalfRows);
         int inc = nh;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -168,7 +176,7 @@ __device__ __forceinline__ void list_staged_halves(const SegmentTable &t, int W,
             while (h >= s.half0[j + 1]) ++j;  // the group holding half h
             const int g1 = t.dst[(j + 1) * W];
             first = t.dst[j * W] + (h - s.half0[j]) * kHalfRows;
-            end = min(first + kHalfRows, g1);
+            end = run_end(first, kHalfRows, g1);
             staged = !half_in_one_segment(t, W, e, first, g1);
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, staged);
