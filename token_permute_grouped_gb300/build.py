@@ -14,10 +14,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liba2av_gmm.so")
 # Debug variant: device-side bounds checks that record a status bit instead
-# of trapping (-DA2AV_CHECKS).  Only the sources the checks touch are built
+# of trapping (-DA2AV_CHECKS), and a switch that makes a wait run out.  Only the sources the checks touch are built
 # again; the others are linked from the ordinary build.
 CHECKS_LIB = os.path.join(PKG, "liba2av_gmm_checks.so")
-CHECKS_SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu"]
+CHECKS_SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu", "ffn_api.cu"]
 SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu", "grouped_gemm_mx.cu", "amp.cu", "quant_reduce.cu", "ffn_api.cu",
            "rms_norm.cu", "glu.cu", "expert_gemm.cu", "gated_rows.cu", "glu_grad.cu", "stage_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -415,10 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
             const Block b = kblocks ? block_of(w.weights, K, ks.first) : Block{0, 0};
             for (int part = 0; part < (is_ragged(w, b) ? p.parts : 0) && ok; ++part) {
                 const int s = (it + part * kblocks) % kStages;
-                ok = pair::wait_phase(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns);
+                ok = pair::wait_phase_warp(&C.abort, ragged0 + 8 * s, (used >> s) & 1, p.status, p.wait_limit_ns);
                 if (!ok) break;
                 used ^= 1u << s;
-                __syncwarp();
                 // Rows len .. the next multiple of 16, 128 bytes in each atom of
                 // A and B (the swizzle stays within a row): eight lanes an atom.
                 const uint32_t st = base + s * kStageBytes + b.len * 128 + (lane / 8) * kAtomBytes + (lane % 8) * 16;
@@ -506,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_kernel(const __grid_c
         for (int t = unit; t < total; t += nunits, ++tl) {
             const Tile w = tile_at(C, t, walk);
             const int acc = tl & 1;
-            if (!pair::wait_phase(&C.abort, smem_u32(&C.tfull[acc]), (tl >> 1) & 1, p.status, p.wait_limit_ns)) break;
-            __syncwarp();
+            if (!pair::wait_phase_warp(&C.abort, smem_u32(&C.tfull[acc]), (tl >> 1) & 1, p.status, p.wait_limit_ns)) break;
             tc_fence_after_sync();
             const GroupInfo gi = C.g[w.g];
             const int row0w = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;  // this warp's first row

@@ -18,6 +18,14 @@ using a2av::ExpertGemmLaunch;
 
 constexpr size_t kStatusBytes = 256;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
+#ifdef A2AV_CHECKS
+// Debug builds can make a wait run out: slopes_short holds back one piece of every
+// 128 rows' slopes from the GEMM that waits for them.
+bool slopes_short = false;
+uint64_t wait_limit_ns = kWaitLimitNs;
+#else
+constexpr uint64_t wait_limit_ns = kWaitLimitNs;
+#endif
 constexpr int kMaxDevices = 64;
 // Whether the slopes of a backward pass are computed beside its GEMM, which hides
 // them but leaves them one block an SM: where that GEMM is long, in each of its
@@ -156,7 +164,7 @@ ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, con
     g.bf16 = dtype == A2AV_BF16;
     g.status = status;
     g.write_status = 1;
-    g.wait_limit_ns = kWaitLimitNs;
+    g.wait_limit_ns = wait_limit_ns;
     return g;
 }
 
@@ -306,6 +314,13 @@ size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
 
 extern "C" {
 
+#ifdef A2AV_CHECKS
+void a2av_checks_slopes_short(int32_t on, uint64_t limit_ns) {
+    slopes_short = on != 0;
+    wait_limit_ns = on ? limit_ns : kWaitLimitNs;
+}
+#endif
+
 a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const void *residual, const void *gamma,
                           void *h, void *y, void *codes, void *scales, float *rstd, a2av_stream_t stream) {
     if (!desc) return A2AV_ERR_NULLPTR;
@@ -441,7 +456,7 @@ a2av_status a2av_gated_run(const a2av_gated_desc *desc, const void *ataOut, cons
         }
         r.status = static_cast<int32_t *>(workspace);
         r.after_permute = d.want_permute_out;
-        r.wait_limit_ns = kWaitLimitNs;
+        r.wait_limit_ns = wait_limit_ns;
         r.x = ataOut;
         if (!operand_map(&r.tmGate, gateWeight, d.e, d.H1, d.N, bf16, false) ||
             !operand_map(&r.tmUp, upWeight, d.e, d.H1, d.N, bf16, false))
@@ -533,6 +548,9 @@ a2av_status a2av_gated_backward(const a2av_gated_desc *desc, const void *dh, con
         g.pieces = pieces;
         g.row_pieces = a2av::glu_grad_pieces(128, d.N);
         g.last_pieces = a2av::glu_grad_pieces(d.A % 128, d.N);
+#ifdef A2AV_CHECKS
+        if (slopes_short) ++g.row_pieces, ++g.last_pieces;
+#endif
     }
     const void *const D[4] = {dG, dU, slopes + 2 * slope_bytes(desc), slopes + 3 * slope_bytes(desc)};
     const void *const Wt[2] = {gateWeight, upWeight};

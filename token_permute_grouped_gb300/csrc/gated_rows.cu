@@ -217,10 +217,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
     const int kb0 = kblocks * rank / split, kb1 = kblocks * (rank + 1) / split;  // this CTA's part
     const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
     const uint32_t ready = smem_u32(&C.ready), freed = smem_u32(&C.free);
-    // Before the stages of a CTA's job number jl are filled: the parts of the
-    // job before it have been read, where they share the memory.
-    const auto stages_free = [&](uint32_t jl) {
-        return !S::kShared || jl == 0 || pair::wait_phase(&C.abort, freed, (jl - 1) & 1, p.status, p.wait_limit_ns);
+    // Before the stages of a CTA's job number jl are filled, the parts of the job
+    // before it have been read, where they share the memory.
+    const auto stages_free = [&](uint32_t jl, auto wait) {
+        return !S::kShared || jl == 0 || wait(&C.abort, freed, (jl - 1) & 1, p.status, p.wait_limit_ns);
     };
 
     if (warp == 0) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             bool ok = true;
             for (int job = cluster; job < total && ok; job += clusters, ++jl) {
                 const Job w = job_at(C, job, p.W, R);
-                ok = stages_free(jl);
+                ok = stages_free(jl, pair::wait_phase);
                 if (!ok) break;
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const int s = it % S::kStages;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                 cp_async_wait<0>();
                 hand_over(it);
             }
-            ok = stages_free(jl);
+            ok = stages_free(jl, pair::wait_phase_warp);
             if (!ok) break;
             __syncwarp();
             const int row0 = C.seg.dst[w.expert * p.W], rows = C.seg.dst[(w.expert + 1) * p.W] - row0;
@@ -295,11 +295,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                     cp_async_wait<0>();
                     hand_over(it);
                 }
-                if (!pair::wait_phase(&C.abort, empty0 + 8 * s, par, p.status, p.wait_limit_ns)) {
+                if (!pair::wait_phase_warp(&C.abort, empty0 + 8 * s, par, p.status, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
-                __syncwarp();
                 const uint32_t x_st = base + s * S::kStage + kWBytes + to;
                 const bool in_k = kb * kBK + piece * 8 < p.K;
 #pragma unroll
@@ -366,12 +365,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
             const int row0 = C.seg.dst[w.expert * p.W], rows = C.seg.dst[(w.expert + 1) * p.W] - row0;
             const int live = min(R, rows - w.first);
             const int acc = jl & 1;
-            if (!pair::wait_phase(&C.abort, smem_u32(&C.tfull[acc]), (jl >> 1) & 1, p.status, p.wait_limit_ns)) break;
-            __syncwarp();
+            if (!pair::wait_phase_warp(&C.abort, smem_u32(&C.tfull[acc]), (jl >> 1) & 1, p.status, p.wait_limit_ns)) break;
             tc_fence_after_sync();
             const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * R;
-            if (!pair::wait_phase(&C.abort, freed, (jl & 1) ^ 1, p.status, p.wait_limit_ns)) break;
-            __syncwarp();
+            if (!pair::wait_phase_warp(&C.abort, freed, (jl & 1) ^ 1, p.status, p.wait_limit_ns)) break;
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
                 uint32_t r[16];
@@ -387,8 +384,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
                 mbar_arrive(smem_u32(&C.tempty[acc]));
                 for (int c = 0; c < split; ++c) pair::arrive_cluster(pair::map_to_rank(ready, c));
             }
-            if (!pair::wait_phase(&C.abort, ready, jl & 1, p.status, p.wait_limit_ns)) break;
-            __syncwarp();
+            if (!pair::wait_phase_warp(&C.abort, ready, jl & 1, p.status, p.wait_limit_ns)) break;
             for (int i = tid; i < live * own / 4; i += 4 * 32) {
                 const int r = i / (own / 4), c = rank * own + i % (own / 4) * 4;
                 if (w.col0 + c < p.N) {  // (N is a multiple of 8: all four columns or none)

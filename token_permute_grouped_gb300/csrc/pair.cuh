@@ -71,6 +71,15 @@ static __device__ __noinline__ bool wait_phase(int32_t *abort_flag, uint32_t bar
     }
 }
 
+// The same by a whole warp: its lanes try and give up one by one, so the phase may
+// complete between one lane's last try and another's next.  They leave with one
+// answer, since what follows (votes, tcgen05 loads, the cluster's barrier) needs
+// the whole warp.
+__device__ __forceinline__ bool wait_phase_warp(int32_t *abort_flag, uint32_t bar, uint32_t parity, int32_t *status,
+                                                uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait_phase(abort_flag, bar, parity, status, limit_ns));
+}
+
 // After a wait was given up: a millisecond for the copies and products still in
 // flight, which take microseconds, before shared memory and TMEM are given back.
 static __device__ __noinline__ void let_settle() {
