@@ -796,8 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
             const Tile w = tile_at(t);
             const bool shared = w.g >= e;
             const int acc = tl & 1;
-            if (!wait_phase(&C.abort, &C.tfull[acc], (tl >> 1) & 1, p.status, p.wait_limit_ns)) break;
-            __syncwarp();  // lanes leave the wait independently; tcgen05.ld needs the whole warp
+            // (Lanes leave the wait one by one; what follows needs the whole warp, so one that gave up takes all along.)
+            if (!__all_sync(0xffffffffu, wait_phase(&C.abort, &C.tfull[acc], (tl >> 1) & 1, p.status, p.wait_limit_ns)))
+                break;
             tc_fence_after_sync();
             const int N = shared ? p.N2 : p.N1;
             const int bn = shared ? p.bn2 : p.bn1;

@@ -672,8 +672,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1) grouped_gemm_mx_kernel(const __
             const bool shared = w.g >= e;
             const int acc = S::kAccBufs == 2 ? (tl & 1) : 0;
             const uint32_t use = S::kAccBufs == 2 ? (tl >> 1) : tl;
-            if (!mx_wait(&C.abort, &C.tfull[acc], use & 1, p.status)) break;
-            __syncwarp();  // lanes leave the wait independently; tcgen05.ld needs the whole warp
+            // (Lanes leave the wait one by one; what follows needs the whole warp, so one that gave up takes all along.)
+            if (!__all_sync(0xffffffffu, mx_wait(&C.abort, &C.tfull[acc], use & 1, p.status))) break;
             tc_fence_after_sync();
             const int N = shared ? p.N2 : p.N1;
             const int row = w.m * TILE_M + static_cast<int>(rank) * MX_BM + q * 32 + lane;
