@@ -697,6 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
             if (lane == 0)
                 for (int i = 0; i < STAGES && ok; ++i, ++it)
                     ok = wait_phase(&C.abort, &C.empty[it % STAGES], ((it / STAGES) & 1) ^ 1, p.status, p.wait_limit_ns);
+            // A kernel behind this one that is launched to overlap it waits for
+            // this one's end alone, which has to stand for the permute's too.
+            if (!staged_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
         } else if (GATHER && p.permuteOut != nullptr) {
             // Warps 1-3 write permuteOut for this CTA's rows of the tiles of
             // the first column, straight from ataOut (16-byte vectors, 4 in
