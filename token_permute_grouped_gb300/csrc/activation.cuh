@@ -118,9 +118,13 @@ template <int ACT>
 __device__ __forceinline__ f32x2 act_value_slope(f32x2 g, f32x2 &slope) {
     f32x2 z = g, gdz = g;
     if constexpr (ACT != A2AV_ACT_SILU) {
-        const f32x2 q = mul2(g, g);
-        z = mul2(g, fma2(q, both(kGelu3), both(kGelu1)));
-        gdz = mul2(g, fma2(q, both(3.0f * kGelu3), both(kGelu1)));
+        z = mul2(g, fma2(mul2(g, g), both(kGelu3), both(kGelu1)));
+        // Beyond |g| of 16, s (1 - s) is 0 in fp32, and so is its product with g z',
+        // which is not left to grow out of range.
+        float lo, hi;
+        split(g, lo, hi);
+        const f32x2 c = pair_of(fminf(fmaxf(lo, -16.0f), 16.0f), fminf(fmaxf(hi, -16.0f), 16.0f));
+        gdz = mul2(c, fma2(mul2(c, c), both(3.0f * kGelu3), both(kGelu1)));
     }
     const f32x2 s = sigmoid2(z);
     const f32x2 rest = fma2(s, both(-1.0f), both(1.0f));
