@@ -275,9 +275,10 @@ __global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLa
         float dot, odd;
         split(dot2, dot, odd);
         const float2 total = row_sum(dot + odd, slots[flip] + g * (T / 32), t, T, 1 + g);
-        // dx = dh + rstd (a - n m) = dh + dy gamma rstd - h (rstd^2 m)
+        // dx = dh + rstd (a - n m), in this order: n and m are of the values' own size
+        // for every scale of the row, while rstd^2 may be out of range.
         const float m = (total.x + total.y) / static_cast<float>(p.H);
-        const f32x2 c1 = both(rstd), c2 = both(-rstd * rstd * m);
+        const f32x2 r2 = both(rstd), m2 = both(-m);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = t + k * T;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(MAXT) rms_norm_grad_kernel(const RmsNormGradLa
                 unpack8<BF16>(__ldg(gamma + v), gm);
                 if (p.dh) unpack8<BF16>(d[k], o);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = add2(o[i], fma2(mul2(fa[i], gm[i]), c1, mul2(fn[i], c2)));
+                for (int i = 0; i < 4; ++i) o[i] = fma2(fma2(mul2(fn[i], r2), m2, mul2(fa[i], gm[i])), r2, o[i]);
                 static_cast<uint4 *>(p.dx)[r0 + v] = pack8<BF16>(o);
             }
         }
