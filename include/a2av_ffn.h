@@ -149,9 +149,7 @@ a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const vo
  * Backward, for a gradient dh [A, N] of h:
  *     dG = dh * U * act'(G),  dU = dh * act(G)      rounded to T, the type the
  *                                                   tensor cores multiply (A <= 32:
- *                                                   with the rest of the rounding as
- *                                                   a second T; an infinity of x or
- *                                                   a weight may then end as a NaN)
+ *                                                   to the sum of two Ts)
  *     dPermuteOut = dG x gateWeight^T + dU x upWeight^T
  *     dGate = permuteOut^T x dG,  dUp = permuteOut^T x dU   per expert
  * dAtaOut [A, H1] holds dPermuteOut's rows back in rank-major order; dGate,

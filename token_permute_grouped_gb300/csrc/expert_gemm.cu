@@ -29,7 +29,7 @@
 //   rows' gradient    D: rows x K    K-major     W: out columns x K    K-major
 //   weights' gradient X: K x M       MN-major    D: K x columns        MN-major
 //
-// A D_p may come as two summands (a rounding and what it left over); the second
+// A D_p may come as two summands of the element type; the second
 // ones are further products into the same accumulator.
 //
 // In the weights' gradient K runs over an expert's rows, whose last block is

@@ -66,7 +66,7 @@ struct GluGradLaunch {
     const void *dh;
     const float *gate, *up;
     void *dgate, *dup;
-    int64_t low;      // 16-byte vectors from a slope to what its rounding left over, rounded in turn (0: not kept)
+    int64_t low;      // 16-byte vectors from a slope's first summand to its second (0: one summand, the rounded slope)
     int32_t *pieces;  // counts of finished pieces by 128 rows, zero at the start, for a GEMM that runs beside
                       // this kernel; NULL: not counted, and the kernel takes the SMs for itself
 };

@@ -303,7 +303,7 @@ size_t pieces_bytes(const a2av_gated_desc *d) {
 // Summands a slope is kept in.  One rounding to T adds about as much to a
 // gradient's error as the gradient's own rounding; over a few rows that is the
 // error of a few values, which nothing averages, so there each slope is kept
-// with what its rounding left over.  (The tensor cores then multiply twice as
+// as the sum of two Ts.  (The tensor cores then multiply twice as
 // much, which a few rows do not notice: the weights' bytes bound them.)
 int slope_parts(const a2av_gated_desc *d) { return d->A <= 32 ? 2 : 1; }
 size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU

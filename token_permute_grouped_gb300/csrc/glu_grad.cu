@@ -38,11 +38,39 @@ __device__ __forceinline__ void count_piece(int32_t *count) {
     if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(count) : "memory");
 }
 
-// What a rounding left over; nothing where the value or its rounding is not finite.
-__device__ __forceinline__ f32x2 finite_part(f32x2 v) {
-    float a, b;
-    split(v, a, b);
-    return pair_of(fabsf(a) < __uint_as_float(0x7f800000u) ? a : 0.0f, fabsf(b) < __uint_as_float(0x7f800000u) ? b : 0.0f);
+// v as two summands of the element type that both have its sign (h toward zero,
+// never all of v): the products of an infinity with them are infinities of one
+// sign, as its product with v is, and not a NaN.  Values below the type's
+// smallest are taken for it.
+template <bool BF16>
+__device__ __forceinline__ void two_parts(float v, uint32_t &h, uint32_t &l) {
+    const auto value = [](uint32_t b) {
+        if constexpr (BF16) return __uint_as_float(b << 16);
+        else return __half2float(__ushort_as_half(static_cast<uint16_t>(b)));
+    };
+    if constexpr (BF16) h = __bfloat16_as_ushort(__float2bfloat16_rz(v));
+    else h = __half_as_ushort(__float2half_rz(v));
+    if (value(h) == v && (h & 0x7fffu) > 1) --h;  // the next value toward zero
+    const float rest = v - value(h);
+    if constexpr (BF16) l = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
+    else l = __half_as_ushort(__float2half_rn(rest));
+    if ((l & 0x7fffu) == 0 && v != 0.0f) l = (h & 0x8000u) | 1u;
+}
+template <bool BF16>
+__device__ __forceinline__ void two_parts8(const f32x2 (&v)[4], uint4 &high, uint4 &low) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        uint32_t ha, la, hb, lb;
+        split(v[k], a, b);
+        two_parts<BF16>(a, ha, la);
+        two_parts<BF16>(b, hb, lb);
+        h[k] = ha | hb << 16;
+        l[k] = la | lb << 16;
+    }
+    high = make_uint4(h[0], h[1], h[2], h[3]);
+    low = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 // Counted, a block of 128 rows, which is contiguous in every tensor, is taken in
@@ -81,21 +109,19 @@ __global__ void __launch_bounds__(kGradThreads) glu_grad_kernel(const GluGradLau
                 dg[k] = mul2(mul2(fd[k], u[k]), slope);
                 du[k] = mul2(fd[k], a);
             }
-            const uint4 hg = pack8<BF16>(dg), hu = pack8<BF16>(du);
+            uint4 hg, hu;
+            if (p.low) {
+                uint4 lg, lu;
+                two_parts8<BF16>(dg, hg, lg);
+                two_parts8<BF16>(du, hu, lu);
+                static_cast<uint4 *>(p.dgate)[p.low + v] = lg;
+                static_cast<uint4 *>(p.dup)[p.low + v] = lu;
+            } else {
+                hg = pack8<BF16>(dg);
+                hu = pack8<BF16>(du);
+            }
             static_cast<uint4 *>(p.dgate)[v] = hg;
             static_cast<uint4 *>(p.dup)[v] = hu;
-            if (p.low) {
-                f32x2 rg[4], ru[4];
-                unpack8<BF16>(hg, rg);
-                unpack8<BF16>(hu, ru);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dg[k] = finite_part(fma2(rg[k], both(-1.0f), dg[k]));
-                    du[k] = finite_part(fma2(ru[k], both(-1.0f), du[k]));
-                }
-                static_cast<uint4 *>(p.dgate)[p.low + v] = pack8<BF16>(dg);
-                static_cast<uint4 *>(p.dup)[p.low + v] = pack8<BF16>(du);
-            }
         }
         if (p.pieces) count_piece(p.pieces + block);
     }
