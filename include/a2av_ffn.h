@@ -103,7 +103,7 @@ a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const v
  *   dgamma [H] float32.  dx may be dh or dy itself.  dgamma NULL: not computed.
  * Phase 1 gives the workspace (per-block partial sums of dgamma; 0 bytes for a
  * few rows, workspace may then be NULL).
- * Limits as above (H a multiple of 8).
+ * Limits as above (H a multiple of 8), but dgamma 16-byte aligned.
  */
 a2av_status a2av_rms_norm_backward_workspace_size(int64_t rows, int64_t H, int32_t dtype, size_t *bytes);
 a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const void *dy, const void *dh,
@@ -119,7 +119,8 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
  *   gate, up [rows, N] T, rows `stride` elements apart (>= N; the two halves of
  *   a [rows, 2N] product have stride 2N); h [rows, N] T; codes, scales as above.
  * Limits: 0 <= rows <= 2^31 - 1, 0 < N < 65536, N and stride multiples of 8, N
- * a multiple of 32 (MX) or 128 (GROUP128) with an 8-bit output.
+ * a multiple of 32 (MX) or 128 (GROUP128) with an 8-bit output; alignments as for
+ * a2av_rms_norm.
  */
 typedef struct {
     int64_t rows, N, stride;
@@ -164,7 +165,8 @@ a2av_status a2av_glu_quant(const a2av_glu_desc *desc, const void *gate, const vo
  * Two phases, as in a2av_gmm.h; one workspace serves both directions, and
  * a2av_gmm_read_device_status reads the device status of the last call on it.
  * Limits: those of a2av_gmm.h (W * e <= 256, e <= 32, H1, N < 65536 and
- * multiples of 8, A <= 2^31 - 1).
+ * multiples of 8, A <= 2^31 - 1); T tensors 16-byte, saved 32-byte, recvCounts
+ * 4-byte aligned.
  */
 typedef struct {
     int32_t W, e;
