@@ -452,15 +452,37 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(stream, t):
-    """Handle of the stream to enqueue on: the given one, or the current one of t's device."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # of a device, as a handle
 
 
-def _is(t, name, dtype, shape):
-    """t is a contiguous CUDA tensor of this type and shape."""
+def _enqueue(name, device, stream, *args):
+    """The call `name` on the given stream, or the current one of this device, which is the current device meanwhile: the
+    library asks it for its limits."""
+    if stream is None:
+        handle = _current_stream(device)
+    elif stream.device_index == device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"stream must be of cuda:{device}, got one of cuda:{stream.device_index}")
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return _enqueue(name, device, stream, *args)
+    _call(name, *args, handle)
+
+
+def _beside(t, name, device):
+    """Refuses a tensor of another device."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got cuda:{t.get_device()}")
+
+
+def _is(t, name, dtype, shape, device):
+    """t is a contiguous CUDA tensor of this type and shape on this device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        _beside(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -495,7 +517,7 @@ def _out(t, name, dtype, shape, like, stream):
         if like.shape == shape and like.dtype == dtype and like.is_contiguous():
             return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=like.device)
-    _is(t, name, dtype, shape)
+    _is(t, name, dtype, shape, like.get_device())
     return t
 
 
@@ -532,19 +554,21 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
     Rows of x and residual may be strided; residual may be one row expanded to all.  `out`: an earlier result of the
     same call, whose tensors are written again."""
     code, xs = _rows_of(x, "x")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
     rows, H = shape
-    _is(gamma, "gamma", dtype, (H,))
+    _is(gamma, "gamma", dtype, (H,), device)
     rs = None
     if residual is not None:
         _, rs = _rows_of(residual, "residual")
         if residual.shape != shape or residual.dtype != dtype:
             raise ValueError("residual must have the shape and type of x")
-    key = (shape, dtype, xs, rs, eps, qtype, mode, want_y, want_rstd, x.get_device())
+        if residual.get_device() != device:
+            _beside(residual, "residual", device)
+    key = (shape, dtype, xs, rs, eps, qtype, mode, want_y, want_rstd, device)
     if out is not None and getattr(out, "key", None) == key:  # its tensors and descriptor fit as they are
         h, y, codes, scales, rstd = out
-        _call("a2av_rms_norm", out.desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y), _at(codes),
-              _at(scales), _at(rstd), _on(stream, x))
+        _enqueue("a2av_rms_norm", device, stream, out.desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
+                 _at(codes), _at(scales), _at(rstd))
         return out
     q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
     h = None if residual is None else _out(out.h if out else None, "h", dtype, shape, x, stream)
@@ -556,8 +580,8 @@ def a2av_rms_norm(x, gamma, residual=None, eps=1e-6, qtype=None, mode="mx", want
     if qtype is not None:
         codes, scales = _code_outputs(out, rows, H, mode, x, stream)
     desc = ctypes.byref(RmsNormDesc(rows, H, xs, rs or 0, code, q, m, eps))
-    _call("a2av_rms_norm", desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
-          _at(codes), _at(scales), _at(rstd), _on(stream, x))
+    _enqueue("a2av_rms_norm", device, stream, desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(h), _at(y),
+             _at(codes), _at(scales), _at(rstd))
     result = RmsNormOut(h, y, codes, scales, rstd)
     result.key, result.desc = key, desc
     return result
@@ -572,21 +596,23 @@ def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, wo
     """(dx [rows, H], dgamma float32 [H]) from the gradient dy of the normed rows and, optionally, the gradient dh
     that reaches h directly.  dx is the gradient of x and of the residual."""
     code, _ = _rows_of(dy, "dy")
-    shape, dtype = dy.shape, dy.dtype
+    shape, dtype, device = dy.shape, dy.dtype, dy.get_device()
     rows, H = shape
-    _is(dy, "dy", dtype, shape)
-    _is(h, "h", dtype, shape)
+    _is(dy, "dy", dtype, shape, device)
+    _is(h, "h", dtype, shape, device)
     if dh is not None:
-        _is(dh, "dh", dtype, shape)
-    _is(gamma, "gamma", dtype, (H,))
-    _is(rstd, "rstd", torch.float32, (rows,))
+        _is(dh, "dh", dtype, shape, device)
+    _is(gamma, "gamma", dtype, (H,), device)
+    _is(rstd, "rstd", torch.float32, (rows,), device)
     dx = _out(dx, "dx", dtype, shape, dy, stream)
     dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy, stream)
     need = _norm_backward_size(rows, H, code)
     if workspace is None and need:
         workspace = _out(None, "workspace", torch.uint8, (need,), dy, stream)
-    _call("a2av_rms_norm_backward", rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd), _at(dx),
-          _at(dgamma), _at(workspace), 0 if workspace is None else workspace.numel(), _on(stream, dy))
+    elif workspace is not None:
+        _beside(workspace, "workspace", device)
+    _enqueue("a2av_rms_norm_backward", device, stream, rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd),
+             _at(dx), _at(dgamma), _at(workspace), 0 if workspace is None else workspace.numel())
     return dx, dgamma
 
 
@@ -605,17 +631,17 @@ def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, 
     """act(gate) * up of gate_up [rows, 2N] (gate columns, then up columns) as codes and scales and / or in the
     element type (want_h; by default without a qtype)."""
     code, stride = _rows_of(gate_up, "gate_up")
-    shape = gate_up.shape
+    shape, device = gate_up.shape, gate_up.get_device()
     rows, cols = shape
     N = cols // 2
     if cols != 2 * N:
         raise ValueError("gate_up must have an even number of columns")
     gate = gate_up.data_ptr()
-    key = (shape, gate_up.dtype, stride, act, qtype, mode, want_h, gate_up.get_device())
+    key = (shape, gate_up.dtype, stride, act, qtype, mode, want_h, device)
     if out is not None and getattr(out, "key", None) == key:
         codes, scales, h = out
-        _call("a2av_glu_quant", out.desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
-              _on(stream, gate_up))
+        _enqueue("a2av_glu_quant", device, stream, out.desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes),
+                 _at(scales))
         return out
     q = -1 if qtype is None else _named(QTYPES, qtype, "qtype")
     desc = ctypes.byref(GluDesc(rows, N, stride, code, _named(ACTS, act, "act"), q, _named(QMODES, mode, "mode")))
@@ -624,8 +650,7 @@ def a2av_glu_quant(gate_up, act="silu", qtype="e4m3fn", mode="mx", want_h=None, 
         codes, scales = _code_outputs(out, rows, N, mode, gate_up, stream)
     if want_h or (want_h is None and qtype is None):
         h = _out(out.h if out else None, "h", gate_up.dtype, (rows, N), gate_up, stream)
-    _call("a2av_glu_quant", desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales),
-          _on(stream, gate_up))
+    _enqueue("a2av_glu_quant", device, stream, desc, gate, gate + 2 * N if gate else None, _at(h), _at(codes), _at(scales))
     result = GluQuantOut(codes, scales, h)
     result.key, result.desc = key, desc
     return result
@@ -661,40 +686,40 @@ class GatedPlan:
         self.workspace = torch.empty(_size("a2av_gated_workspace_size", ctypes.byref(self.desc)), dtype=torch.uint8,
                                      device=self.device)
 
-    def _check_shared(self, recvCounts, gateWeight, upWeight):
+    def _check_shared(self, recvCounts, gateWeight, upWeight, device):
         d = self.desc
-        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
-        _is(gateWeight, "gateWeight", self.dtype, (d.e, d.H1, d.N))
-        _is(upWeight, "upWeight", self.dtype, (d.e, d.H1, d.N))
+        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,), device)
+        _is(gateWeight, "gateWeight", self.dtype, (d.e, d.H1, d.N), device)
+        _is(upWeight, "upWeight", self.dtype, (d.e, d.H1, d.N), device)
 
     def run(self, ataOut, recvCounts, gateWeight, upWeight, h=None, saved=None, permuteOut=None,
             stream=None) -> GatedOut:
-        d, dtype, ws = self.desc, self.dtype, self.workspace
+        d, dtype, ws, device = self.desc, self.dtype, self.workspace, self.workspace.get_device()
         A, H1, N = d.A, d.H1, d.N
-        _is(ataOut, "ataOut", dtype, (A, H1))
-        self._check_shared(recvCounts, gateWeight, upWeight)
+        _is(ataOut, "ataOut", dtype, (A, H1), device)
+        self._check_shared(recvCounts, gateWeight, upWeight, device)
         h = _out(h, "h", dtype, (A, N), ws, stream)
         saved = _out(saved, "saved", torch.float32, (2, A, N), ws, stream) if d.save else None
         permuted = _out(permuteOut, "permuteOut", dtype, (A, H1), ataOut, stream) if d.want_permute_out else None
-        _call("a2av_gated_run", ctypes.byref(d), ataOut.data_ptr(), recvCounts.data_ptr(), gateWeight.data_ptr(),
-              upWeight.data_ptr(), _at(permuted), h.data_ptr(), _at(saved), ws.data_ptr(), ws.numel(),
-              _on(stream, ws))
+        _enqueue("a2av_gated_run", device, stream, ctypes.byref(d), ataOut.data_ptr(), recvCounts.data_ptr(),
+                 gateWeight.data_ptr(), upWeight.data_ptr(), _at(permuted), h.data_ptr(), _at(saved), ws.data_ptr(),
+                 ws.numel())
         return GatedOut(h, saved, ataOut if d.W == 1 else permuted)
 
     def backward(self, dh, permuteOut, recvCounts, gateWeight, upWeight, saved, want_rows=True, want_weights=True,
                  dAtaOut=None, dGate=None, dUp=None, stream=None) -> GatedGrads:
-        d, dtype, ws = self.desc, self.dtype, self.workspace
+        d, dtype, ws, device = self.desc, self.dtype, self.workspace, self.workspace.get_device()
         A, H1, N = d.A, d.H1, d.N
-        _is(dh, "dh", dtype, (A, N))
-        _is(permuteOut, "permuteOut", dtype, (A, H1))
-        self._check_shared(recvCounts, gateWeight, upWeight)
-        _is(saved, "saved", torch.float32, (2, A, N))
+        _is(dh, "dh", dtype, (A, N), device)
+        _is(permuteOut, "permuteOut", dtype, (A, H1), device)
+        self._check_shared(recvCounts, gateWeight, upWeight, device)
+        _is(saved, "saved", torch.float32, (2, A, N), device)
         rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut, stream) if want_rows else None
         gate = _out(dGate, "dGate", dtype, (d.e, H1, N), gateWeight, stream) if want_weights else None
         up = _out(dUp, "dUp", dtype, (d.e, H1, N), upWeight, stream) if want_weights else None
-        _call("a2av_gated_backward", ctypes.byref(d), dh.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
-              gateWeight.data_ptr(), upWeight.data_ptr(), saved.data_ptr(), _at(rows), _at(gate), _at(up),
-              ws.data_ptr(), ws.numel(), _on(stream, ws))
+        _enqueue("a2av_gated_backward", device, stream, ctypes.byref(d), dh.data_ptr(), permuteOut.data_ptr(),
+                 recvCounts.data_ptr(), gateWeight.data_ptr(), upWeight.data_ptr(), saved.data_ptr(), _at(rows), _at(gate),
+                 _at(up), ws.data_ptr(), ws.numel())
         return GatedGrads(rows, gate, up)
 
 
@@ -711,14 +736,14 @@ class GmmBackwardPlan:
     def run(self, dY, permuteOut, recvCounts, gmmWeight, want_rows=True, want_weights=True, dAtaOut=None,
             dWeight=None, stream=None):
         """(dAtaOut [A, H1] rank-major, dWeight [e, H1, N1]); either may be left out (None)."""
-        d, dtype, ws = self.desc, self.dtype, self.workspace
+        d, dtype, ws, device = self.desc, self.dtype, self.workspace, self.workspace.get_device()
         A, H1, N1 = d.A, d.H1, d.N1
-        _is(dY, "dY", dtype, (A, N1))
-        _is(permuteOut, "permuteOut", dtype, (A, H1))
-        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,))
-        _is(gmmWeight, "gmmWeight", dtype, (d.e, H1, N1))
+        _is(dY, "dY", dtype, (A, N1), device)
+        _is(permuteOut, "permuteOut", dtype, (A, H1), device)
+        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,), device)
+        _is(gmmWeight, "gmmWeight", dtype, (d.e, H1, N1), device)
         rows = _out(dAtaOut, "dAtaOut", dtype, (A, H1), permuteOut, stream) if want_rows else None
         weights = _out(dWeight, "dWeight", dtype, (d.e, H1, N1), gmmWeight, stream) if want_weights else None
-        _call("a2av_gmm_backward", ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(), recvCounts.data_ptr(),
-              gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel(), _on(stream, ws))
+        _enqueue("a2av_gmm_backward", device, stream, ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(),
+                 recvCounts.data_ptr(), gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel())
         return rows, weights
