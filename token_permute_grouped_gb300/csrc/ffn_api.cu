@@ -9,6 +9,7 @@
 #include "a2av_ffn.h"
 #include "ffn.h"
 #include "kernels.h"
+#include "per_device.h"
 #include "plan.cuh"
 #include "quantise.cuh"
 
@@ -26,7 +27,6 @@ uint64_t wait_limit_ns = kWaitLimitNs;
 #else
 constexpr uint64_t wait_limit_ns = kWaitLimitNs;
 #endif
-constexpr int kMaxDevices = 64;
 // Whether the slopes of a backward pass are computed beside its GEMM, which hides
 // them but leaves them one block an SM: where that GEMM is long, in each of its
 // contractions too.  Measured (us, one after the other / beside; rows x H1 x N of
@@ -49,24 +49,24 @@ bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
+int current_device() {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 int sm_count() {
-    static int cache[kMaxDevices] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        cache[dev] = n;
-    }
-    return cache[dev];
+    static a2av::PerDevice<int> cache;
+    const int dev = current_device();
+    const int *n = cache.get(dev, [dev](int &v) {
+        return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    });
+    return n ? *n : 0;
 }
 
 int gemm_clusters() {
-    static int cache[kMaxDevices] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-    if (cache[dev] == 0) cache[dev] = a2av::expert_gemm_max_clusters();
-    return cache[dev];
+    static a2av::PerDevice<int> cache;
+    const int *n = cache.get(current_device(), [](int &v) { return (v = a2av::expert_gemm_max_clusters()) > 0; });
+    return n ? *n : 0;
 }
 
 // The 8-bit output asked for: its type and mode within the formats, and rows

@@ -33,6 +33,7 @@
 #include "ffn.h"
 #include "pair.cuh"
 #include "pdl.cuh"
+#include "per_device.h"
 #include "segments.cuh"
 
 namespace a2av {
@@ -435,17 +436,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) gated_rows_kernel(const __grid
 // 4096 x 1536: 62 us with 2 to 4, 76 with 0 or 1).
 constexpr double kJobCost = 3.0;
 
-// Clusters of 1, 2, 4 and 8 CTAs resident at once, per device.
+// Clusters of 1, 2, 4 and 8 CTAs resident at once.
+struct Resident {
+    int clusters[4];
+};
 template <int R>
-const int *resident_clusters() {
-    static int cache[64][4] = {};
+const Resident *resident_clusters() {
+    static PerDevice<Resident> cache;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-    int *c = cache[dev];
-    if (c[0] == 0)
-        for (int i = 3; i >= 0; --i)
-            c[i] = max_clusters(gated_rows_kernel<true, A2AV_ACT_SILU, R>, kRowThreads, row_smem<R>(), 1 << i);
-    return c;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    return cache.get(dev, [](Resident &r) {
+        for (int i = 0; i < 4; ++i)
+            r.clusters[i] = max_clusters(gated_rows_kernel<true, A2AV_ACT_SILU, R>, kRowThreads, row_smem<R>(), 1 << i);
+        return r.clusters[0] > 0;
+    });
 }
 
 template <bool BF16, int ACT, int R>
@@ -454,8 +458,9 @@ cudaError_t launch_rows(GatedRowsLaunch &p, cudaStream_t stream) {
     constexpr size_t smem = row_smem<R>();
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    const int *resident = resident_clusters<R>();
-    if (!resident || resident[0] <= 0) return cudaErrorUnknown;
+    const Resident *of_device = resident_clusters<R>();
+    if (!of_device) return cudaErrorUnknown;
+    const int(&resident)[4] = of_device->clusters;
     // The split of K that takes the least time, counted in K blocks a CTA
     // streams plus what a job costs beside them, for the experts that rows
     // spread at random would reach.
