@@ -128,13 +128,10 @@ __global__ void __launch_bounds__(kGradThreads) glu_grad_kernel(const GluGradLau
 }
 
 // An SM's split of L1 and shared memory holds while blocks run on it, and a GEMM
-// CTA needs the largest share, so a kernel that is to share its SMs asks for
-// that share too (otherwise the SM is set for L1, and the GEMM starts only as
-// these blocks end).
-template <typename Kernel>
-cudaError_t beside_gemm(Kernel kern) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-}
+// CTA needs the largest share, so a launch that is to share its SMs asks for that
+// share too (otherwise the SM is set for L1, and the GEMM starts only as these
+// blocks end).
+constexpr int kBesideGemm = cudaSharedmemCarveoutMaxShared;
 
 }  // namespace
 
@@ -151,11 +148,7 @@ cudaError_t launch_glu_grad(const GluGradLaunch &p, bool bf16, int act, int sms,
                                                    : glu_grad_kernel<true, A2AV_ACT_GELU_TANH>)
                            : (act == A2AV_ACT_SILU ? glu_grad_kernel<false, A2AV_ACT_SILU>
                                                    : glu_grad_kernel<false, A2AV_ACT_GELU_TANH>);
-    if (p.pieces) {
-        const cudaError_t err = beside_gemm(kern);
-        if (err != cudaSuccess) return err;
-    }
-    return launch_pdl(kern, grid, kGradThreads, 0, 0, stream, p);
+    return launch_pdl(kern, grid, kGradThreads, 0, PdlShape(0, p.pieces ? kBesideGemm : -1), stream, p);
 }
 
 }  // namespace a2av
