@@ -279,18 +279,25 @@ a2av_status validate(const a2av_gated_desc *d) {
 // Whether the weight-streaming kernel (gated_rows.cu) takes a forward call: the
 // rows its fullest expert is expected to have fit one pass over the weights, or
 // somewhat more where the tile kernel would have tiles for half of the SMs at
-// most and a long way to go or a permute before it.
+// most and a long way to go.
 // Measured (us, streaming / tiles), rows an expert: 4 experts of 4096 x 1024
-// from 8 sources, 16: 20 / 42, 32: 23 / 40, 96: 31 / 39, 128: 42 / 39; one
-// expert of 7168 x 2048, 16: 17 / 42, 128: 21 / 42, 256: 35 / 42; of 2048 x
-// 704, 64: 12 / 14, 128: 14 / 14; 16 experts of 2048 x 1408, 32: 49 / 59, 64: 67
-// / 55; 8 of 1032 x 328 from 2 sources, 64: 15 / 19.
+// from 8 sources, 16: 16 / 23, 32: 18 / 24, 64: 21 / 24, 96: 30 / 25, from one,
+// 72: 21.2 / 21.8, 80: 28 / 22; 2 of 7168 x 2048, 72: 29 / 34, 80: 40 / 34; one
+// of 7168 x 2048, 16: 14 / 32, 128: 18 / 33, 256: 31.8 / 32.7; one of 2048 x
+// 704, 64: 10 / 12, 128: 12.3 / 12.6; 16 of 2048 x 1408, 16: 38 / 44, 32: 44 /
+// 45, 64: 70 / 46; 4 of 2048 x 1024, 40: 12.5 / 13.9, 48: 14.4 / 13.9; 8 of 1032
+// x 328 from 4, 40: 11.0 / 11.5, 48: 12.9 / 11.5.
+// Rows are taken to spread at random.  Where they do not, the fullest expert's
+// weights are read once for each pass (rows of it / all): 16 of 2048 x 1408,
+// 128 / 512: 44 / 45, 512 / 512: 30 / 17; 32 of 4096 x 1536, 256 / 1024: 155 /
+// 157, 512 / 1024: 163 / 156, 1024 / 1024: 79 / 28; 4 of 4096 x 1024, 128 / 128:
+// 17 / 22.
 bool few_rows(const a2av_gated_desc &d) {
     if (d.A == 0) return false;
     const double most = a2av::gated_rows_most(d.A, d.e);
     if (most <= 64.0) return true;
-    if (d.e * ((d.N + 127) / 128) >= 40) return false;
-    return d.e == 1 ? d.A <= 256 && d.H1 >= 4096 : most <= 128.0 && (d.H1 >= 4096 || d.W > 1);
+    if (d.H1 < 4096 || d.e * ((d.N + 127) / 128) >= 40) return false;
+    return d.e == 1 ? d.A <= 256 : most <= 100.0;
 }
 
 size_t staged_bytes(const a2av_gated_desc *d) {

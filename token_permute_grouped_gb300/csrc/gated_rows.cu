@@ -490,10 +490,9 @@ cudaError_t launch_rows_tile(GatedRowsLaunch &p, cudaStream_t stream) {
     const double most = gated_rows_most(p.A, p.e);  // so that one pass over the weights is usual
     if (most <= 16) return launch_rows<BF16, ACT, 16>(p, stream);
     if (most <= 32) return launch_rows<BF16, ACT, 32>(p, stream);
-    // 128 rows where one pass is then likely (fuller experts than expected come
-    // with skewed routing, and a second pass costs this shape more than 64
-    // rows a third: 4 experts x 96 rows of 4096 x 1024, 42 against 31 us).
-    if (most > 64 && (p.e == 1 || most <= 100)) return launch_rows<BF16, ACT, 128>(p, stream);
+    // 128 rows a pass where that one is usual, or where one expert has up to two
+    // (256 rows of 7168 x 2048: 31.8 us).
+    if (most > 64) return launch_rows<BF16, ACT, 128>(p, stream);
     return launch_rows<BF16, ACT, 64>(p, stream);
 }
 
