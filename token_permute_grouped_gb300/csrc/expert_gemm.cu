@@ -58,7 +58,8 @@
 // its MMAs take, so neither a taller nor a wider tile is to be had from this
 // much shared memory.  34,502 rows of 7168 x 2048 (gated): 1172 us, 1730
 // TFLOP/s, the tensor pipe active 82 % of the cycles; both gradients of 16,407
-// rows of 1024 x 4096: 180 us, 1530 TFLOP/s.  Short contractions over uneven
+// rows of 1024 x 4096: 180 us, 1530 TFLOP/s (single launches after a pause; in a
+// loop, at the power limit, they take 4 to 8 % longer).  Short contractions over uneven
 // rows are bound by the outputs' stores and the last wave: 32 experts x 156
 // rows of 1032 x 328, 30 us forward and 51 backward, against 4 and 7 us of
 // tensor time.

@@ -30,20 +30,22 @@ constexpr uint64_t wait_limit_ns = kWaitLimitNs;
 // Whether the slopes of a backward pass are computed beside its GEMM, which hides
 // them but leaves them one block an SM: where that GEMM is long, in each of its
 // contractions too.  Measured (us, one after the other / beside; rows x H1 x N of
-// a whole training step): 20,000 x 2048 x 1408 565 / 531, 20,000 x 768 x 1408 288
-// / 270, 8917 x 2048 x 1408 294 / 289, 2500 x 4096 x 4096 451 / 445; 10,000 x
-// 1024 x 1024 128 / 131, 60,000 x 512 x 1024 493 / 501, 30,000 x 4096 x 256 312 /
-// 320, 60,000 x 256 x 512 213 / 241.
+// a whole training step): 20,000 x 2048 x 1408 526 / 485, 20,000 x 768 x 1408 291
+// / 270, 8917 x 2048 x 1408 270 / 258, 2500 x 4096 x 4096 590 / 586; 10,000 x
+// 1024 x 1024 141 / 139, 60,000 x 512 x 1024 475 / 488, 30,000 x 4096 x 256 378 /
+// 386, 60,000 x 256 x 512 223 / 249.
 bool slopes_beside(int64_t A, int64_t H1, int64_t N) {
     return static_cast<double>(A) * H1 * N >= 2e10 && H1 >= 768 && N >= 512;
 }
 // Mean rows of a (source, expert) run from which whole halves are read in place
-// (us, in place / all rows staged; mean run): 5013 rows of 1032 x 328 (20) 36.7
-// / 32.6, 20,000 of 2048 x 1408 (78) 177 / 169, 34,502 of 7168 x 2048 (135) 1285
-// / 1307, 65,308 of 2048 x 1408 (255) 474 / 484, 16,407 of 4096 x 1024 (513)
-// 168 / 193.
+// (us, in place / all rows staged; mean run): 5013 rows of 1032 x 328 (20) 35.1
+// / 29.2, 20,000 of 2048 x 1408 (78) 175 / 165, 34,502 of 7168 x 2048 (135) 1294
+// / 1286, 65,308 of 2048 x 1408 (255) 473 / 482, 16,407 of 4096 x 1024 (513)
+// 161 / 188.
 constexpr int64_t kLongRun = 96;
-constexpr int64_t kPairs = 76;  // pairs of SMs, each of which has a tile at a time
+// Pairs of SMs, each of which has a tile at a time, of a GB300.  Not asked of the
+// device: the workspace's size depends on it, and is asked for without one.
+constexpr int64_t kPairs = 76;
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 bool mult8(int64_t v) { return v % 8 == 0; }
 bool type16(int32_t dtype) { return dtype == A2AV_BF16 || dtype == A2AV_FP16; }
@@ -150,8 +152,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // SM's 64 bytes a clock from L2 equally busy; a narrower one is bound by the
 // latter (1.6 times the time of a large product), but spreads a small product
 // over more SMs.  Measured (us, 256 / 128 wide): gated, 4 experts x 128 rows of
-// 4096 x 1024 28 / 24, one x 256 of 2048 x 704 15.4 / 14.0, 16 x 128 of
-// 2048 x 1408 (176 tiles of 256) 45 / 50.
+// 4096 x 1024 26 / 22, one x 256 of 2048 x 704 14.2 / 12.7, 16 x 128 of
+// 2048 x 1408 (176 tiles of 256) 44 / 48.
 int pick_bn(int64_t tiles128) { return tiles128 <= std::max(1, gemm_clusters()) ? 128 : 256; }
 
 ExpertGemmLaunch base_launch(int32_t W, int32_t e, int64_t A, int32_t dtype, const int32_t *recvCounts, int32_t *status) {
@@ -181,9 +183,13 @@ int64_t weight_tiles(int32_t e, int64_t H1, int64_t N, int phases, int64_t bn) {
 // and the slices' sums are joined by a second kernel.  Chosen by the blocks of
 // the contraction that the fullest pair of SMs would go through, its tiles being
 // dealt out in turn, plus the joining.  Measured (us, one slice / chosen): one
-// expert, 8386 rows of 448 x 896 47.6 / 26, 16,384 of 1024 x 1024 103.6 / 58.6,
-// 2 rows over 16 experts of 256 x 3456 27.3 / 19.0.  It depends on the shapes
-// alone, since the workspace holds the sums.
+// expert, 8386 rows of 448 x 896 46 / 25, 16,384 of 1024 x 1024 103 / 58, 60,000
+// of 256 x 256 289 / 41; 2 rows over 16 experts of 256 x 3456 27 / 18; 4 experts,
+// 16,407 rows of 1024 x 4096 169 / 169 (not cut).  It depends on the shapes alone,
+// since the workspace holds the sums.
+// The choice hardly depends on the three costs: a third or twice kTileCost, and
+// kJoinCost of 2 or 12, leave ten shapes' times as they are; half of kJoinBytes
+// costs one of them (8386 of 448 x 896, 24.8 to 27.4), twice of it none.
 constexpr double kTileCost = 3.0;       // of a tile beside its blocks, in blocks
 constexpr double kJoinCost = 5.0;       // of the second kernel, in blocks
 constexpr double kJoinBytes = 1.4e6;    // of sums written and read again in a block's time

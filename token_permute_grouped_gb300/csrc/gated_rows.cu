@@ -467,6 +467,10 @@ cudaError_t launch_rows(GatedRowsLaunch &p, cudaStream_t stream) {
     const double reached = p.e * (1.0 - std::pow(1.0 - 1.0 / p.e, static_cast<double>(p.A)));
     const int strips = (p.N + kCols - 1) / kCols;
     const double jobs = std::ceil(reached - 0.5) * strips;
+    // Weights fetched before the rows are counted, where most experts will have some
+    // (us, without / with; share reached): 4 experts of 4096 x 1024, 8 rows (0.90)
+    // 15.7 / 14.7, 32 (1.00) 15.8 / 15.2; 16 experts, 32 rows (0.87) 37.8 / 36.9.
+    // Below, some of what is fetched is not used: 16 rows (0.64) 39.3 / 39.3.
     p.guess = reached > 0.85 * p.e ? p.e : 0;
     const int kblocks = (p.K + kBK - 1) / kBK;
     double best = 0.0;

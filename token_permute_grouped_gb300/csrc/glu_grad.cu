@@ -8,7 +8,8 @@
 // GEMM, and all its blocks are resident before the GEMM starts, so neither can
 // hold up the other.  65,308 x 1408 values: 315 us alone with one block an SM
 // (190 with eight, at the copy rate) and 905 us of GEMM; forward and backward of
-// the gated block together take 1550 us side by side, 1715 one after the other.
+// the gated block together take 1550 us side by side, 1715 one after the other
+// (single calls after a pause; 1717 side by side in a loop, at the power limit).
 #include <algorithm>
 
 #include "activation.cuh"
