@@ -1,8 +1,8 @@
 /*
  * a2av_ffn — the operators around the grouped product of an expert layer, on
- * one GB300: the RMS norm in front of the dispatch, the gated feed-forward
+ * one GB300: the RMS or layer norm in front of the dispatch, the gated feed-forward
  * block of the experts, the gated activation between two block-scaled
- * products, and the gradients of the norm, the block and the grouped product.
+ * products, and the gradients of the norms, the block and the grouped product.
  *
  * Conventions are those of a2av_gmm.h: plain device pointers, row-major
  * layouts, the caller owns every buffer, nothing is allocated, kept or
@@ -110,6 +110,51 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
                                    const void *h, const void *gamma, const float *rstd, void *dx,
                                    float *dgamma, void *workspace, size_t workspace_bytes,
                                    a2av_stream_t stream);
+
+/*
+ * Layer norm with the residual's addition and an 8-bit output:
+ *
+ *     s = x + residual                             (s = x without a residual)
+ *     mean = mean(s), rstd = 1 / sqrt(mean((s - mean)^2) + eps)   over a row
+ *     y = (s - mean) * rstd * gamma + beta         (beta NULL: 0)
+ *
+ * Outputs, strides, codes, in-place h, limits and alignments as for
+ * a2av_rms_norm; beta [H] T, mean [rows] float32.  The squares are summed about
+ * the mean; a row whose squares overflow fp32 gets rstd 0.
+ */
+typedef struct {
+    int64_t rows, H;
+    int64_t x_stride, residual_stride; /* elements from one row to the next */
+    int32_t dtype;                     /* a2av_dtype: bf16 or fp16 */
+    int32_t qtype;                     /* a2av_qtype, or A2AV_Q_NONE */
+    int32_t qmode;                     /* a2av_qmode */
+    float eps;                         /* >= 0 */
+} a2av_layer_norm_desc;
+
+a2av_status a2av_layer_norm(const a2av_layer_norm_desc *desc, const void *x, const void *residual,
+                            const void *gamma, const void *beta, void *h, void *y, void *codes, void *scales,
+                            float *mean, float *rstd, a2av_stream_t stream);
+
+/*
+ * Gradient of y = (h - mean) * rstd * gamma + beta with respect to h, gamma and
+ * beta (mean and rstd functions of h), plus the gradient dh that reaches h
+ * directly:
+ *
+ *     a = dy * gamma,  n = (h - mean) * rstd
+ *     dx = dh + rstd * (a - mean(a) - n * mean(a * n))    (dh = 0 when it is NULL)
+ *     dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy
+ *
+ * dx is the gradient of x and of the residual alike.  Through the 8-bit output
+ * the gradient passes as through y (straight-through).  Tensors, limits and
+ * workspace as for a2av_rms_norm_backward; mean [rows] float32, dbeta [H]
+ * float32, 16-byte aligned.  dgamma and dbeta are both NULL (not computed) or
+ * neither.
+ */
+a2av_status a2av_layer_norm_backward_workspace_size(int64_t rows, int64_t H, int32_t dtype, size_t *bytes);
+a2av_status a2av_layer_norm_backward(int64_t rows, int64_t H, int32_t dtype, const void *dy, const void *dh,
+                                     const void *h, const void *gamma, const float *mean, const float *rstd,
+                                     void *dx, float *dgamma, float *dbeta, void *workspace,
+                                     size_t workspace_bytes, a2av_stream_t stream);
 
 /*
  * Gated activation with an 8-bit output: v = act(gate) * up, written as T

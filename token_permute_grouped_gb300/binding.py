@@ -35,7 +35,9 @@ EXPORTS = ("a2av_gmm_workspace_size", "a2av_gmm_run", "a2av_gmm_read_device_stat
            "a2av_gmm_mx_workspace_size", "a2av_gmm_mx_run", "a2av_gmm_mx_run_profiled",
            "a2av_rms_norm", "a2av_rms_norm_backward", "a2av_rms_norm_backward_workspace_size", "a2av_glu_quant",
            "a2av_gated_workspace_size", "a2av_gated_run", "a2av_gated_backward",
-           "a2av_gmm_backward_workspace_size", "a2av_gmm_backward")
+           "a2av_gmm_backward_workspace_size", "a2av_gmm_backward",
+           "a2av_layer_norm", "a2av_layer_norm_backward", "a2av_layer_norm_backward_workspace_size")
+_FFN_EXPORTS = EXPORTS[EXPORTS.index("a2av_rms_norm"):]
 
 # a2av_qtype / a2av_qmode of include/a2av_quant_reduce.h.
 QTYPES = {"e4m3fn": 0, "e5m2": 1, "int8": 2}
@@ -69,6 +71,10 @@ class RmsNormDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int64), ("x_stride", ctypes.c_int64),
                 ("residual_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("qtype", ctypes.c_int32),
                 ("qmode", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = RmsNormDesc._fields_
 
 
 class GluDesc(ctypes.Structure):
@@ -150,7 +156,10 @@ def load_library(path: str):
     L.a2av_gated_backward.argtypes = [ctypes.POINTER(GatedDesc)] + [p] * 10 + [sz, p]
     L.a2av_gmm_backward_workspace_size.argtypes = [ctypes.POINTER(Desc), psz]
     L.a2av_gmm_backward.argtypes = [ctypes.POINTER(Desc)] + [p] * 7 + [sz, p]
-    for name in EXPORTS[-9:]:
+    L.a2av_layer_norm.argtypes = [ctypes.POINTER(LayerNormDesc)] + [p] * 11
+    L.a2av_layer_norm_backward_workspace_size.argtypes = [i64, i64, i32, psz]
+    L.a2av_layer_norm_backward.argtypes = [i64, i64, i32] + [p] * 10 + [sz, p]
+    for name in _FFN_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
     return L
 
@@ -614,6 +623,95 @@ def a2av_rms_norm_backward(dy, h, gamma, rstd, dh=None, dx=None, dgamma=None, wo
     _enqueue("a2av_rms_norm_backward", device, stream, rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(rstd),
              _at(dx), _at(dgamma), _at(workspace), 0 if workspace is None else workspace.numel())
     return dx, dgamma
+
+
+class _LayerNormFields(NamedTuple):
+    h: Optional[torch.Tensor]       # x + residual, element type (None without a residual)
+    y: Optional[torch.Tensor]       # normed rows, element type
+    codes: Optional[torch.Tensor]   # uint8 codes of the normed rows
+    scales: Optional[torch.Tensor]  # uint8 E8M0 per 32 (mx) or float32 per 128 (group128)
+    mean: Optional[torch.Tensor]    # float32 [rows]
+    rstd: Optional[torch.Tensor]    # float32 [rows]
+
+
+class LayerNormOut(_LayerNormFields):
+    """Also holds what its tensors were made for and the descriptor, as RmsNormOut does."""
+
+
+def a2av_layer_norm(x, gamma, beta=None, residual=None, eps=1e-5, qtype=None, mode="mx", want_y=None, want_stats=False,
+                    out: Optional[LayerNormOut] = None, stream=None) -> LayerNormOut:
+    """Layer norm of x [rows, H] (+ residual), times gamma [H], plus beta [H] where given: the normed rows as codes and
+    scales (qtype "e4m3fn", "e5m2" or "int8"; mode "mx" or "group128") and / or in the element type (want_y; by default
+    without a qtype).  want_stats: mean and rstd too, for the backward pass.  Rows of x and residual may be strided;
+    residual may be one row expanded to all.  `out`: an earlier result of the same call, whose tensors are written
+    again."""
+    code, xs = _rows_of(x, "x")
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    rows, H = shape
+    _is(gamma, "gamma", dtype, (H,), device)
+    if beta is not None:
+        _is(beta, "beta", dtype, (H,), device)
+    rs = None
+    if residual is not None:
+        _, rs = _rows_of(residual, "residual")
+        if residual.shape != shape or residual.dtype != dtype:
+            raise ValueError("residual must have the shape and type of x")
+        if residual.get_device() != device:
+            _beside(residual, "residual", device)
+    key = (shape, dtype, xs, rs, eps, qtype, mode, want_y, want_stats, device)
+    if out is not None and getattr(out, "key", None) == key:  # its tensors and descriptor fit as they are
+        h, y, codes, scales, mean, rstd = out
+        _enqueue("a2av_layer_norm", device, stream, out.desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(beta),
+                 _at(h), _at(y), _at(codes), _at(scales), _at(mean), _at(rstd))
+        return out
+    q, m = -1 if qtype is None else _named(QTYPES, qtype, "qtype"), _named(QMODES, mode, "mode")
+    h = None if residual is None else _out(out.h if out else None, "h", dtype, shape, x, stream)
+    y = codes = scales = mean = rstd = None
+    if want_y or (want_y is None and qtype is None):
+        y = _out(out.y if out else None, "y", dtype, shape, x, stream)
+    if want_stats:
+        mean = _out(out.mean if out else None, "mean", torch.float32, (rows,), x, stream)
+        rstd = _out(out.rstd if out else None, "rstd", torch.float32, (rows,), x, stream)
+    if qtype is not None:
+        codes, scales = _code_outputs(out, rows, H, mode, x, stream)
+    desc = ctypes.byref(LayerNormDesc(rows, H, xs, rs or 0, code, q, m, eps))
+    _enqueue("a2av_layer_norm", device, stream, desc, x.data_ptr(), _at(residual), gamma.data_ptr(), _at(beta), _at(h),
+             _at(y), _at(codes), _at(scales), _at(mean), _at(rstd))
+    result = LayerNormOut(h, y, codes, scales, mean, rstd)
+    result.key, result.desc = key, desc
+    return result
+
+
+@functools.lru_cache(maxsize=256)
+def _layer_norm_backward_size(rows, H, code):
+    return _size("a2av_layer_norm_backward_workspace_size", rows, H, code)
+
+
+def a2av_layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, dx=None, dgamma=None, dbeta=None, workspace=None,
+                             stream=None):
+    """(dx [rows, H], dgamma float32 [H], dbeta float32 [H]) from the gradient dy of the normed rows and, optionally,
+    the gradient dh that reaches h directly.  dx is the gradient of x and of the residual."""
+    code, _ = _rows_of(dy, "dy")
+    shape, dtype, device = dy.shape, dy.dtype, dy.get_device()
+    rows, H = shape
+    _is(dy, "dy", dtype, shape, device)
+    _is(h, "h", dtype, shape, device)
+    if dh is not None:
+        _is(dh, "dh", dtype, shape, device)
+    _is(gamma, "gamma", dtype, (H,), device)
+    _is(mean, "mean", torch.float32, (rows,), device)
+    _is(rstd, "rstd", torch.float32, (rows,), device)
+    dx = _out(dx, "dx", dtype, shape, dy, stream)
+    dgamma = _out(dgamma, "dgamma", torch.float32, (H,), dy, stream)
+    dbeta = _out(dbeta, "dbeta", torch.float32, (H,), dy, stream)
+    need = _layer_norm_backward_size(rows, H, code)
+    if workspace is None and need:
+        workspace = _out(None, "workspace", torch.uint8, (need,), dy, stream)
+    elif workspace is not None:
+        _beside(workspace, "workspace", device)
+    _enqueue("a2av_layer_norm_backward", device, stream, rows, H, code, _at(dy), _at(dh), _at(h), _at(gamma), _at(mean),
+             _at(rstd), _at(dx), _at(dgamma), _at(dbeta), _at(workspace), 0 if workspace is None else workspace.numel())
+    return dx, dgamma, dbeta
 
 
 class _GluQuantFields(NamedTuple):

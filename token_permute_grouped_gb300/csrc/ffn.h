@@ -37,6 +37,33 @@ struct RmsNormGradLaunch {
 int rms_norm_grad_blocks(int64_t rows, int64_t H);
 cudaError_t launch_rms_norm_grad(const RmsNormGradLaunch &p, bool bf16, cudaStream_t stream);
 
+// Layer norm and its gradient (layer_norm.cu).
+struct LayerNormLaunch {
+    int32_t rows, H;
+    int64_t x_stride, r_stride;  // elements
+    const void *x, *residual, *gamma, *beta;
+    void *h, *y;
+    uint8_t *codes;
+    void *scales;
+    float *mean, *rstd;
+    float eps;
+};
+// kind: quant_kind() of the 8-bit output, or -1.
+cudaError_t launch_layer_norm(const LayerNormLaunch &p, bool bf16, int kind, int sms, cudaStream_t stream);
+
+struct LayerNormGradLaunch {
+    int32_t rows, H;
+    const void *dy, *dh, *h, *gamma;
+    const float *mean, *rstd;
+    void *dx;
+    float *dgamma, *dbeta;  // both or neither
+    float *partial;         // [blocks][2][H]
+    int32_t blocks;
+};
+// Blocks the gradient kernel runs for this shape, each with two rows of partial sums.
+int layer_norm_grad_blocks(int64_t rows, int64_t H);
+cudaError_t launch_layer_norm_grad(const LayerNormGradLaunch &p, bool bf16, cudaStream_t stream);
+
 struct GluLaunch {
     int64_t rows;
     int32_t N;

@@ -328,6 +328,25 @@ size_t slope_bytes(const a2av_gated_desc *d) {  // one of dG, dU
     return d->save ? round256(static_cast<size_t>(d->A) * d->N * 2) : 0;
 }
 
+// The checks that the two norms share (their descriptors have the same fields).
+template <typename Desc>
+a2av_status check_norm(const Desc &d, const void *x, const void *residual, const void *gamma, const void *h,
+                       const void *y, const void *codes, const void *scales, bool other_output) {
+    if (d.rows < 0 || d.rows > INT32_MAX || d.H <= 0 || d.H >= 65536 || !type16(d.dtype)) return A2AV_ERR_INVALID;
+    if (!(d.eps >= 0.0f)) return A2AV_ERR_INVALID;
+    if (d.x_stride < d.H || (residual && d.residual_stride != 0 && d.residual_stride < d.H)) return A2AV_ERR_INVALID;
+    const a2av_status q = check_quant(d.qtype, d.qmode, d.H);
+    if (q != A2AV_OK) return q;
+    if (!mult8(d.H) || !mult8(d.x_stride) || (residual && !mult8(d.residual_stride))) return A2AV_ERR_UNSUPPORTED;
+    if (!gamma || (d.rows > 0 && !x)) return A2AV_ERR_NULLPTR;
+    if (d.rows > 0 && !h && !y && !codes && !other_output) return A2AV_ERR_NULLPTR;
+    const a2av_status qo = check_quant_out(d.qtype, d.qmode, codes, scales, d.rows > 0);
+    if (qo != A2AV_OK) return qo;
+    for (const void *p : {x, residual, gamma, h, y})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    return A2AV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -343,18 +362,8 @@ a2av_status a2av_rms_norm(const a2av_rms_norm_desc *desc, const void *x, const v
                           void *h, void *y, void *codes, void *scales, float *rstd, a2av_stream_t stream) {
     if (!desc) return A2AV_ERR_NULLPTR;
     const a2av_rms_norm_desc &d = *desc;
-    if (d.rows < 0 || d.rows > INT32_MAX || d.H <= 0 || d.H >= 65536 || !type16(d.dtype)) return A2AV_ERR_INVALID;
-    if (!(d.eps >= 0.0f)) return A2AV_ERR_INVALID;
-    if (d.x_stride < d.H || (residual && d.residual_stride != 0 && d.residual_stride < d.H)) return A2AV_ERR_INVALID;
-    const a2av_status q = check_quant(d.qtype, d.qmode, d.H);
-    if (q != A2AV_OK) return q;
-    if (!mult8(d.H) || !mult8(d.x_stride) || (residual && !mult8(d.residual_stride))) return A2AV_ERR_UNSUPPORTED;
-    if (!gamma || (d.rows > 0 && !x)) return A2AV_ERR_NULLPTR;
-    if (d.rows > 0 && !h && !y && !codes && !rstd) return A2AV_ERR_NULLPTR;
-    const a2av_status qo = check_quant_out(d.qtype, d.qmode, codes, scales, d.rows > 0);
-    if (qo != A2AV_OK) return qo;
-    for (const void *p : {x, residual, gamma, static_cast<const void *>(h), static_cast<const void *>(y)})
-        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    const a2av_status c = check_norm(d, x, residual, gamma, h, y, codes, scales, rstd != nullptr);
+    if (c != A2AV_OK) return c;
     if (!aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
     if (d.rows == 0) return A2AV_OK;
     const int sms = sm_count();
@@ -394,6 +403,59 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
     a2av::RmsNormGradLaunch p{static_cast<int32_t>(rows), static_cast<int32_t>(H), dy, dh, h, gamma, rstd, dx, dgamma,
                               static_cast<float *>(workspace), a2av::rms_norm_grad_blocks(rows, H)};
     return a2av::launch_rms_norm_grad(p, dtype == A2AV_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? A2AV_OK
+               : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_layer_norm(const a2av_layer_norm_desc *desc, const void *x, const void *residual, const void *gamma,
+                            const void *beta, void *h, void *y, void *codes, void *scales, float *mean, float *rstd,
+                            a2av_stream_t stream) {
+    if (!desc) return A2AV_ERR_NULLPTR;
+    const a2av_layer_norm_desc &d = *desc;
+    const a2av_status c = check_norm(d, x, residual, gamma, h, y, codes, scales, mean || rstd);
+    if (c != A2AV_OK) return c;
+    if (!aligned(beta, 16) || !aligned(mean, 4) || !aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (d.rows == 0) return A2AV_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return A2AV_ERR_CUDA;
+    a2av::LayerNormLaunch p{static_cast<int32_t>(d.rows), static_cast<int32_t>(d.H), d.x_stride, d.residual_stride, x,
+                            residual, gamma, beta, h, y, static_cast<uint8_t *>(codes), scales, mean, rstd, d.eps};
+    return a2av::launch_layer_norm(p, d.dtype == A2AV_BF16, kind_of(d.qtype, d.qmode), sms,
+                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? A2AV_OK
+               : A2AV_ERR_CUDA;
+}
+
+a2av_status a2av_layer_norm_backward_workspace_size(int64_t rows, int64_t H, int32_t dtype, size_t *bytes) {
+    if (!bytes) return A2AV_ERR_NULLPTR;
+    if (rows < 0 || rows > INT32_MAX || H <= 0 || H >= 65536 || !type16(dtype)) return A2AV_ERR_INVALID;
+    if (!mult8(H)) return A2AV_ERR_UNSUPPORTED;
+    const int blocks = a2av::layer_norm_grad_blocks(rows, H);
+    *bytes = blocks > 1 ? round256(static_cast<size_t>(blocks) * H * 8) : 0;
+    return A2AV_OK;
+}
+
+a2av_status a2av_layer_norm_backward(int64_t rows, int64_t H, int32_t dtype, const void *dy, const void *dh,
+                                     const void *h, const void *gamma, const float *mean, const float *rstd, void *dx,
+                                     float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
+                                     a2av_stream_t stream) {
+    size_t need = 0;
+    const a2av_status s = a2av_layer_norm_backward_workspace_size(rows, H, dtype, &need);
+    if (s != A2AV_OK) return s;
+    if (rows > 0 && (!dy || !h || !gamma || !mean || !rstd || !dx)) return A2AV_ERR_NULLPTR;
+    if ((dgamma == nullptr) != (dbeta == nullptr)) return A2AV_ERR_NULLPTR;
+    for (const void *p : {dy, dh, h, gamma, static_cast<const void *>(dx), static_cast<const void *>(dgamma),
+                          static_cast<const void *>(dbeta)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (dgamma && need > 0) {
+        if (!workspace) return A2AV_ERR_NULLPTR;
+        if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    }
+    if (rows == 0 && !dgamma) return A2AV_OK;
+    a2av::LayerNormGradLaunch p{static_cast<int32_t>(rows), static_cast<int32_t>(H), dy, dh, h, gamma, mean, rstd, dx,
+                                dgamma, dbeta, static_cast<float *>(workspace), a2av::layer_norm_grad_blocks(rows, H)};
+    return a2av::launch_layer_norm_grad(p, dtype == A2AV_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? A2AV_OK
                : A2AV_ERR_CUDA;
 }

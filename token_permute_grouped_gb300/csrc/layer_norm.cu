@@ -1,0 +1,424 @@
+// Layer norm with the residual's addition and an 8-bit output, and its gradient.
+//
+//   s = x + residual, mu = mean(s), rstd = 1 / sqrt(mean((s - mu)^2) + eps)
+//   y = (s - mu) rstd gamma + beta
+//   dx = dh + rstd (a - mean(a) - n mean(a n)),  a = dy gamma,  n = (h - mu) rstd
+//   dgamma = sum dy n,  dbeta = sum dy
+//
+// HBM-bound, one pass, laid out as the RMS norm (rms_norm.cu): a row stays in
+// the registers of one block between its sums and the scaling, the next row's
+// values are requested before the current one is reduced.  The squares are
+// summed about the mean, in a second reduction of what the registers hold, so
+// a row's offset costs no digits.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "ffn.h"
+#include "pdl.cuh"
+#include "quantise.cuh"
+#include "rows.cuh"
+
+namespace a2av {
+
+namespace {
+
+// y has three roundings and a cancellation of up to a few digits against beta:
+// its exponent is decided in double within this many units of a power of two.
+constexpr uint32_t kNearUnits = 64;
+
+// |((s - mu) rstd) gamma + beta| >= pw in double, out of line: for the few blocks next to a power of two.
+__device__ __noinline__ bool reaches_wide(float s, float mu, float mu_lo, float rstd, float rstd_lo, float gamma,
+                                          float beta, float pw) {
+    const double d = static_cast<double>(s) - mu - mu_lo;
+    return fabs(d * (static_cast<double>(rstd) + rstd_lo) * gamma + beta) >= pw;
+}
+
+// VPT: vectors of 8 values a thread holds.  KIND: the 8-bit output.
+template <bool BF16, int VPT, int KIND>
+__global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch p) {
+    using Q = Quant<KIND>;
+    constexpr bool PRE = VPT <= 2;
+    __shared__ float2 slots[2][32];  // of the mean's and of the squares' sums
+    const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x;
+    const uint4 *gamma = static_cast<const uint4 *>(p.gamma), *beta = static_cast<const uint4 *>(p.beta);
+    uint4 raw[VPT], res[VPT];
+    const auto load = [&](int row) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + row * p.x_stride);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            if (t + k * T < vecs) raw[k] = ld_once(x + t + k * T);
+        if (p.residual) {
+            const uint4 *r =
+                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + row * p.r_stride);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (t + k * T < vecs) res[k] = ld_once(r + t + k * T);
+        }
+    };
+    const int step = gridDim.x;
+    const int last = p.rows - step;  // rows below it have a next one (row + step may not fit an int)
+    const float H = static_cast<float>(p.H);
+    pdl_trigger();
+    pdl_wait();
+    if (PRE) load(blockIdx.x);
+    for (int row = blockIdx.x; row < p.rows; row = row < last ? row + step : p.rows) {
+        const size_t out0 = static_cast<size_t>(row) * vecs;
+        if (!PRE) load(row);
+        f32x2 s[VPT][4];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[k][i] = 0;
+            if (t + k * T < vecs) {
+                unpack8<BF16>(raw[k], s[k]);
+                if (p.residual) {
+                    f32x2 f[4];
+                    unpack8<BF16>(res[k], f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[k][i] = add2(s[k][i], f[i]);
+                }
+            }
+        }
+        if (PRE && row < last) load(row + step);
+        f32x2 sum2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (p.h && t + k * T < vecs) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
+            sum2 = add2(sum2, add2(add2(s[k][0], s[k][1]), add2(s[k][2], s[k][3])));
+        }
+        float sum, odd;
+        split(sum2, sum, odd);
+        const float2 total = row_sum(sum + odd, slots[0], t, T, 0);
+        // The mean in two parts, its quotient's remainder in the second.
+        const float mu = total.x / H;
+        float mu_lo = (fmaf(-mu, H, total.x) + total.y) / H;
+        if (!(fabsf(mu_lo) < __uint_as_float(0x7f800000u))) mu_lo = 0.0f;  // (of an infinite sum)
+        f32x2 sq2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if (t + k * T < vecs) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 d = add2(add2(s[k][i], both(-mu)), both(-mu_lo));
+                    if constexpr (!Q::kMx) s[k][i] = d;  // (an mx exponent may ask for the values again)
+                    sq2 = fma2(d, d, sq2);
+                }
+            }
+        }
+        float sq, sq_odd;
+        split(sq2, sq, sq_odd);
+        float rstd_lo;
+        const float rstd = inv_rms(row_sum(sq + sq_odd, slots[1], t, T, 0), H, p.eps, rstd_lo);
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mu;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        if (!Q::kAny && !p.y) continue;
+        f32x2 y[VPT][4];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = t + k * T;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[k][i] = 0;
+            if (v < vecs) {
+                f32x2 g[4], b[4] = {0, 0, 0, 0};
+                unpack8<BF16>(__ldg(gamma + v), g);
+                if (beta) unpack8<BF16>(__ldg(beta + v), b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 d = Q::kMx ? add2(add2(s[k][i], both(-mu)), both(-mu_lo)) : s[k][i];
+                    y[k][i] = fma2(mul2(d, both(rstd)), g[i], b[i]);
+                }
+                if (p.y) static_cast<uint4 *>(p.y)[out0 + v] = pack8<BF16>(y[k]);
+            }
+        }
+        if constexpr (Q::kAny) {
+            const auto reaches = [&](int k, float pw) {
+                const int v = t + k * T;
+                if (v >= vecs) return false;
+                f32x2 g2[4], b2[4] = {0, 0, 0, 0};
+                unpack8<BF16>(__ldg(gamma + v), g2);
+                if (beta) unpack8<BF16>(__ldg(beta + v), b2);
+                bool hit = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a[2], g[2], b[2];
+                    split(s[k][i], a[0], a[1]);
+                    split(g2[i], g[0], g[1]);
+                    split(b2[i], b[0], b[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) hit |= reaches_wide(a[j], mu, mu_lo, rstd, rstd_lo, g[j], b[j], pw);
+                }
+                return hit;
+            };
+            quantise<KIND, VPT, kNearUnits>(y, reaches, [&](int k, uint2 codes, uint8_t e8m0, float scale) {
+                const int v = t + k * T;
+                if (v >= vecs) return;
+                reinterpret_cast<uint2 *>(p.codes)[out0 + v] = codes;
+                if (v % Q::kLanes == 0) {
+                    if constexpr (Q::kMx) static_cast<uint8_t *>(p.scales)[(out0 + v) / Q::kLanes] = e8m0;
+                    else static_cast<float *>(p.scales)[(out0 + v) / Q::kLanes] = scale;
+                }
+            });
+        }
+    }
+}
+
+template <bool BF16, int VPT>
+cudaError_t launch_norm_vpt(const LayerNormLaunch &p, int kind, int threads, int grid, cudaStream_t stream) {
+    switch (kind) {
+#define A2AV_KIND(...)                                                                             \
+    case __VA_ARGS__:                                                                              \
+        return launch_pdl(layer_norm_kernel<BF16, VPT, __VA_ARGS__>, grid, threads, 0, 0, stream, p)
+        A2AV_KIND(kQuantNone);
+        A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E4M3FN));
+        A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E5M2));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_E4M3FN));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_E5M2));
+        A2AV_KIND(quant_kind(A2AV_QMODE_GROUP128, A2AV_Q_INT8));
+#undef A2AV_KIND
+    }
+    return cudaErrorInvalidValue;
+}
+
+// Sums over a row's threads of two values, as row_sum; one barrier.
+__device__ __forceinline__ float2 row_sum_two(float a, float b, float4 *slots, int t, int threads, int bar) {
+    float a_lo = 0.0f, b_lo = 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        two_sum(a, a_lo, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, a_lo, off));
+        two_sum(b, b_lo, __shfl_xor_sync(0xffffffffu, b, off), __shfl_xor_sync(0xffffffffu, b_lo, off));
+    }
+    const int warps = threads / 32, lane = t % 32;
+    if (warps > 1) {
+        if (lane == 0) slots[t / 32] = make_float4(a, a_lo, b, b_lo);
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+        const float4 w = lane < warps ? slots[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        a = w.x, a_lo = w.y, b = w.z, b_lo = w.w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            two_sum(a, a_lo, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, a_lo, off));
+            two_sum(b, b_lo, __shfl_xor_sync(0xffffffffu, b, off), __shfl_xor_sync(0xffffffffu, b_lo, off));
+        }
+    }
+    const float inf = __uint_as_float(0x7f800000u);
+    return make_float2(fabsf(a) < inf ? a + a_lo : a, fabsf(b) < inf ? b + b_lo : b);
+}
+
+// A block holds R rows at a time (blockDim = T x R), each walked on by its own
+// T threads, which keep their share of dgamma and dbeta in registers; at the end
+// the block adds its rows' shares in order and stores one row of partial sums
+// (dgamma's H, then dbeta's), and a second kernel adds those in block order.
+template <bool BF16, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) layer_norm_grad_kernel(const LayerNormGradLaunch p) {
+    constexpr bool PRE = VPT <= 2;
+    __shared__ float4 slots[2][32];
+    extern __shared__ float4 share[];
+    const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x, R = blockDim.y, g = threadIdx.y;
+    const uint4 *gamma = static_cast<const uint4 *>(p.gamma);
+    f32x2 dg[VPT][4], db[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dg[k][i] = db[k][i] = 0;
+    uint4 a[VPT], n[VPT], d[VPT], na[VPT], nn[VPT], nd[VPT];  // dy, h, dh of this row and of the next
+    float rstd = 0.0f, nrstd = 0.0f, mu = 0.0f, nmu = 0.0f;
+    const auto load = [&](int row, uint4 (&ra)[VPT], uint4 (&rn)[VPT], uint4 (&rd)[VPT], float &rs, float &rm) {
+        const size_t r0 = static_cast<size_t>(row) * vecs;
+        rs = __ldg(p.rstd + row);
+        rm = __ldg(p.mean + row);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = t + k * T;
+            if (v < vecs) {
+                ra[k] = ld_once(static_cast<const uint4 *>(p.dy) + r0 + v);
+                rn[k] = ld_once(static_cast<const uint4 *>(p.h) + r0 + v);
+                if (p.dh) rd[k] = ld_once(static_cast<const uint4 *>(p.dh) + r0 + v);
+            }
+        }
+    };
+    int flip = 0;
+    const int step = gridDim.x * R, last = p.rows - step;  // as above
+    int row = blockIdx.x * R + g;
+    pdl_wait();
+    if (PRE && row < p.rows) load(row, na, nn, nd, nrstd, nmu);
+    for (; row < p.rows; row = row < last ? row + step : p.rows, flip ^= 1) {
+        const size_t r0 = static_cast<size_t>(row) * vecs;
+        if (PRE) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) a[k] = na[k], n[k] = nn[k], d[k] = nd[k];
+            rstd = nrstd, mu = nmu;
+            if (row < last) load(row + step, na, nn, nd, nrstd, nmu);
+        } else {
+            load(row, a, n, d, rstd, mu);
+        }
+        const f32x2 r2 = both(rstd), mu2 = both(-mu);
+        f32x2 sum2 = 0, dot2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = t + k * T;
+            if (v < vecs) {
+                f32x2 fa[4], fn[4], gm[4];
+                unpack8<BF16>(a[k], fa);
+                unpack8<BF16>(n[k], fn);
+                unpack8<BF16>(__ldg(gamma + v), gm);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x2 u = mul2(fa[i], mul2(add2(fn[i], mu2), r2));
+                    dg[k][i] = add2(dg[k][i], u);
+                    db[k][i] = add2(db[k][i], fa[i]);
+                    dot2 = fma2(u, gm[i], dot2);
+                    sum2 = fma2(fa[i], gm[i], sum2);
+                }
+            }
+        }
+        float sum, sum_odd, dot, dot_odd;
+        split(sum2, sum, sum_odd);
+        split(dot2, dot, dot_odd);
+        const float2 total = row_sum_two(sum + sum_odd, dot + dot_odd, slots[flip] + g * (T / 32), t, T, 1 + g);
+        // dx = dh + rstd (a - mean(a) - n m), in this order: n and m are of the values'
+        // own size for every scale of the row, while rstd^2 may be out of range.
+        const f32x2 ma2 = both(-total.x / static_cast<float>(p.H)), m2 = both(-total.y / static_cast<float>(p.H));
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = t + k * T;
+            if (v < vecs) {
+                f32x2 fa[4], fn[4], gm[4], o[4] = {0, 0, 0, 0};
+                unpack8<BF16>(a[k], fa);
+                unpack8<BF16>(n[k], fn);
+                unpack8<BF16>(__ldg(gamma + v), gm);
+                if (p.dh) unpack8<BF16>(d[k], o);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = fma2(fma2(mul2(add2(fn[i], mu2), r2), m2, fma2(fa[i], gm[i], ma2)), r2, o[i]);
+                static_cast<uint4 *>(p.dx)[r0 + v] = pack8<BF16>(o);
+            }
+        }
+    }
+    pdl_trigger();  // the sum over the blocks may be launched; it waits for this grid's end
+    if (!p.dgamma) return;
+    const bool alone = p.blocks == 1;
+    float *sums = p.partial + static_cast<size_t>(blockIdx.x) * 2 * p.H;
+    float4 *const outs[2] = {reinterpret_cast<float4 *>(alone ? p.dgamma : sums),
+                             reinterpret_cast<float4 *>(alone ? p.dbeta : sums + p.H)};
+    const auto put = [&](int turn, int v, const f32x2 (&s)[4], float4 *shared, float4 *out) {
+        float4 lo, hi;
+        split(s[0], lo.x, lo.y);
+        split(s[1], lo.z, lo.w);
+        split(s[2], hi.x, hi.y);
+        split(s[3], hi.z, hi.w);
+        if (turn > 0) {
+            const float4 l = shared[2 * v], h = shared[2 * v + 1];
+            lo = make_float4(l.x + lo.x, l.y + lo.y, l.z + lo.z, l.w + lo.w);
+            hi = make_float4(h.x + hi.x, h.y + hi.y, h.z + hi.z, h.w + hi.w);
+        }
+        float4 *to = turn == R - 1 ? out : shared;
+        to[2 * v] = lo;
+        to[2 * v + 1] = hi;
+    };
+    for (int turn = 0; turn < R; ++turn) {
+        if (turn == g) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = t + k * T;
+                if (v < vecs) {
+                    put(turn, v, dg[k], share, outs[0]);
+                    put(turn, v, db[k], share + p.H / 4, outs[1]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// out[c] = sum over blocks of partial[block][c], c over dgamma's columns and then
+// dbeta's: 32 columns a block of kSlices slices of the partial sums, each in
+// block order, the slices joined in order: the same sums every time.
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) column_sums_kernel(const float *__restrict__ partial, int blocks, int H,
+                                                                   float *__restrict__ dgamma, float *__restrict__ dbeta) {
+    __shared__ float s[kSlices][33];
+    pdl_trigger();
+    pdl_wait();  // the partial sums are visible
+    const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
+    const int c = blockIdx.x * 32 + lane;
+    float sum = 0.0f;
+    if (c < 2 * H)
+        for (int b = slice; b < blocks; b += kSlices) sum += partial[static_cast<size_t>(b) * 2 * H + c];
+    s[slice][lane] = sum;
+    __syncthreads();
+    if (slice == 0 && c < 2 * H) {
+        for (int k = 1; k < kSlices; ++k) sum += s[k][lane];
+        (c < H ? dgamma : dbeta - H)[c] = sum;
+    }
+}
+
+// Blocks of the gradient and threads of one, one block an SM (as the RMS norm's gradient, rms_norm.cu).
+constexpr int kGradBlocks = 152;
+constexpr int kGradThreads = 512;
+// Resident threads an SM that the norm's grid is made for: 64 registers a thread allow 1024.
+constexpr int kNormThreadsPerSm = 1024;
+
+struct GradShape {
+    int vpt, threads, rows;  // vectors a thread, threads a row, rows a block
+};
+GradShape grad_shape(int64_t H) {
+    const int vecs = static_cast<int>(H / 8);
+    int vpt = 2;
+    while (vpt < 8 && threads_for(vecs, vpt) > 512) vpt *= 2;
+    const int threads = threads_for(vecs, vpt);
+    // (the shares of dgamma and dbeta of a block with several rows meet in at most 32 KB)
+    return {vpt, threads, std::max(1, std::min(kGradThreads / threads, 8))};
+}
+
+template <bool BF16>
+cudaError_t launch_norm_type(const LayerNormLaunch &p, int kind, int sms, cudaStream_t stream) {
+    const int vecs = p.H / 8;
+    const auto go = [&](auto launch, int vpt) {
+        const int threads = threads_for(vecs, vpt);
+        return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, kNormThreadsPerSm / threads)), stream);
+    };
+    // A vector a thread where an SM has one row at most, and no next row's values to hold.
+    if (p.rows <= sms && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
+    if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2>, 2);
+    if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4>, 4);
+    return go(launch_norm_vpt<BF16, 8>, 8);
+}
+
+}  // namespace
+
+cudaError_t launch_layer_norm(const LayerNormLaunch &p, bool bf16, int kind, int sms, cudaStream_t stream) {
+    return bf16 ? launch_norm_type<true>(p, kind, sms, stream) : launch_norm_type<false>(p, kind, sms, stream);
+}
+
+int layer_norm_grad_blocks(int64_t rows, int64_t H) {
+    // Up to two turns of its rows by one block, whose sums are then all of them.
+    const int64_t r = grad_shape(H).rows;
+    return rows <= 2 * r ? static_cast<int>(std::min<int64_t>(rows, 1))
+                         : static_cast<int>(std::min<int64_t>((rows + r - 1) / r, kGradBlocks));
+}
+
+cudaError_t launch_layer_norm_grad(const LayerNormGradLaunch &p, bool bf16, cudaStream_t stream) {
+    const GradShape shape = grad_shape(p.H);
+    if (p.blocks > 0) {
+        const dim3 block(shape.threads, shape.rows);
+        const size_t smem = shape.rows > 1 ? static_cast<size_t>(p.H) * 8 : 0;
+        cudaError_t err;
+        switch (shape.vpt) {
+#define A2AV_GRAD(V, MAXT)                                                                               \
+    err = bf16 ? launch_pdl(layer_norm_grad_kernel<true, V, MAXT>, p.blocks, block, smem, 0, stream, p)  \
+               : launch_pdl(layer_norm_grad_kernel<false, V, MAXT>, p.blocks, block, smem, 0, stream, p); \
+    break
+            case 2: A2AV_GRAD(2, 512);
+            case 4: A2AV_GRAD(4, 512);
+            default: A2AV_GRAD(8, 1024);
+#undef A2AV_GRAD
+        }
+        if (err != cudaSuccess) return err;
+    }
+    if (!p.dgamma || p.blocks == 1) return cudaSuccess;
+    return launch_pdl(column_sums_kernel, (2 * p.H + 31) / 32, 32 * kSlices, 0, 0, stream,
+                      static_cast<const float *>(p.partial), p.blocks, p.H, p.dgamma, p.dbeta);
+}
+
+}  // namespace a2av

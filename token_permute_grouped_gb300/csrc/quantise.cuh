@@ -64,8 +64,9 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // up to 54 units off, but every product of 16-bit factors that comes near a power
 // of two was tried (some hundred mantissa pairs an activation), and none beyond
 // these 8 units falls on the wrong side of it.
+// UNITS: those 8, or what a caller's y needs.
 // group128: one fp32 quotient qmax / m a block.
-template <int KIND, int K, typename Reaches, typename Store>
+template <int KIND, int K, uint32_t UNITS = 8, typename Reaches, typename Store>
 __device__ __forceinline__ void quantise(const f32x2 (&y)[K][4], Reaches reaches, Store store) {
     using Q = Quant<KIND>;
     uint32_t top[K];
@@ -82,7 +83,7 @@ __device__ __forceinline__ void quantise(const f32x2 (&y)[K][4], Reaches reaches
             m = max3_abs(m, o, 0.0f);
         }
         top[k] = __float_as_uint(m) & 0x7fffffffu;  // infinity above every finite value, NaN above that
-        near |= ((top[k] + 8) & 0x7fffffu) < 16 && top[k] - 0x00800001u < 0x7f000000u;  // normal numbers only
+        near |= ((top[k] + UNITS) & 0x7fffffu) < 2 * UNITS && top[k] - 0x00800001u < 0x7f000000u;  // normal numbers only
     }
     int step[K];
 #pragma unroll
@@ -91,8 +92,8 @@ __device__ __forceinline__ void quantise(const f32x2 (&y)[K][4], Reaches reaches
         if (__any_sync(0xffffffffu, near)) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const bool here = ((top[k] + 8) & 0x7fffffu) < 16 && top[k] - 0x00800001u < 0x7f000000u;
-                const uint32_t pw = (top[k] + 8) & 0x7f800000u;
+                const bool here = ((top[k] + UNITS) & 0x7fffffu) < 2 * UNITS && top[k] - 0x00800001u < 0x7f000000u;
+                const uint32_t pw = (top[k] + UNITS) & 0x7f800000u;
                 int hit = here && reaches(k, __uint_as_float(pw)) ? 1 : 0;
 #pragma unroll
                 for (int off = 1; off < Q::kLanes; off <<= 1) hit |= __shfl_xor_sync(0xffffffffu, hit, off);
