@@ -36,7 +36,8 @@ EXPORTS = ("a2av_gmm_workspace_size", "a2av_gmm_run", "a2av_gmm_read_device_stat
            "a2av_rms_norm", "a2av_rms_norm_backward", "a2av_rms_norm_backward_workspace_size", "a2av_glu_quant",
            "a2av_gated_workspace_size", "a2av_gated_run", "a2av_gated_backward",
            "a2av_gmm_backward_workspace_size", "a2av_gmm_backward",
-           "a2av_layer_norm", "a2av_layer_norm_backward", "a2av_layer_norm_backward_workspace_size")
+           "a2av_layer_norm", "a2av_layer_norm_backward", "a2av_layer_norm_backward_workspace_size",
+           "a2av_gmm_g128_workspace_size", "a2av_gmm_g128_run")
 _FFN_EXPORTS = EXPORTS[EXPORTS.index("a2av_rms_norm"):]
 
 # a2av_qtype / a2av_qmode of include/a2av_quant_reduce.h.
@@ -88,6 +89,13 @@ class GatedDesc(ctypes.Structure):
                 ("A", ctypes.c_int64), ("H1", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("want_permute_out", ctypes.c_int32),
                 ("save", ctypes.c_int32)]
+
+
+class G128Desc(ctypes.Structure):
+    """a2av_gmm_g128_desc of include/a2av_gmm_g128.h."""
+    _fields_ = [("W", ctypes.c_int32), ("e", ctypes.c_int32),
+                ("A", ctypes.c_int64), ("H1", ctypes.c_int64), ("N1", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("qtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -159,6 +167,8 @@ def load_library(path: str):
     L.a2av_layer_norm.argtypes = [ctypes.POINTER(LayerNormDesc)] + [p] * 11
     L.a2av_layer_norm_backward_workspace_size.argtypes = [i64, i64, i32, psz]
     L.a2av_layer_norm_backward.argtypes = [i64, i64, i32] + [p] * 10 + [sz, p]
+    L.a2av_gmm_g128_workspace_size.argtypes = [ctypes.POINTER(G128Desc), psz]
+    L.a2av_gmm_g128_run.argtypes = [ctypes.POINTER(G128Desc)] + [p] * 7 + [sz, p]
     for name in _FFN_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
     return L
@@ -845,3 +855,38 @@ class GmmBackwardPlan:
         _enqueue("a2av_gmm_backward", device, stream, ctypes.byref(d), dY.data_ptr(), permuteOut.data_ptr(),
                  recvCounts.data_ptr(), gmmWeight.data_ptr(), _at(rows), _at(weights), ws.data_ptr(), ws.numel())
         return rows, weights
+
+
+# ---- the product of 8-bit rows with a float32 scale per 128 (include/a2av_gmm_g128.h)
+
+
+class G128Plan:
+    """Descriptor + workspace of the grouped product of codes with a float32 scale for each 128, for one shape: rows as
+    a2av_rms_norm, a2av_layer_norm and a2av_glu_quant write them in mode "group128", weights [e, N1, H1] with a scale
+    for 128 columns x 128 codes.  dtype: of the output.  The workspace serves one call at a time: calls of one plan on
+    different streams have to be ordered by the caller."""
+
+    def __init__(self, W, e, A, H1, N1, dtype=torch.bfloat16, qtype="e4m3fn", device=None):
+        if dtype not in DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+        self.desc = G128Desc(W, e, A, H1, N1, DTYPES[dtype], _named(QTYPES, qtype, "qtype"))
+        self.dtype = dtype
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.workspace = torch.empty(_size("a2av_gmm_g128_workspace_size", ctypes.byref(self.desc)), dtype=torch.uint8,
+                                     device=self.device)
+
+    def run(self, ataOut_q, ataOut_s, recvCounts, gmmWeight_q, gmmWeight_s, gmmY=None, stream=None):
+        """gmmY [A, N1], expert-major, from ataOut_q uint8 [A, H1] and ataOut_s float32 [A, H1/128] (rank-major),
+        gmmWeight_q uint8 [e, N1, H1] and gmmWeight_s float32 [e, ceil(N1/128), H1/128]."""
+        d, ws, device = self.desc, self.workspace, self.workspace.get_device()
+        A, H1, N1 = d.A, d.H1, d.N1
+        _is(ataOut_q, "ataOut_q", torch.uint8, (A, H1), device)
+        _is(ataOut_s, "ataOut_s", torch.float32, (A, H1 // 128), device)
+        _is(recvCounts, "recvCounts", torch.int32, (d.W * d.e,), device)
+        _is(gmmWeight_q, "gmmWeight_q", torch.uint8, (d.e, N1, H1), device)
+        _is(gmmWeight_s, "gmmWeight_s", torch.float32, (d.e, -(-N1 // 128), H1 // 128), device)
+        gmmY = _out(gmmY, "gmmY", self.dtype, (A, N1), ws, stream)
+        _enqueue("a2av_gmm_g128_run", device, stream, ctypes.byref(d), ataOut_q.data_ptr(), ataOut_s.data_ptr(),
+                 recvCounts.data_ptr(), gmmWeight_q.data_ptr(), gmmWeight_s.data_ptr(), gmmY.data_ptr(), ws.data_ptr(),
+                 ws.numel())
+        return gmmY

@@ -1,0 +1,171 @@
+// C ABI of the grouped product of 8-bit rows with a float32 scale per 128
+// (declared in include/a2av_gmm_g128.h): argument checks, tensor maps, launches.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "a2av_gmm_g128.h"
+#include "ffn.h"
+#include "g128.h"
+#include "kernels.h"
+#include "per_device.h"
+#include "plan.cuh"
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side wait
+
+bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+size_t round256(size_t b) { return (b + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Device {
+    int sms, clusters;
+};
+const Device *device_of() {
+    static a2av::PerDevice<Device> cache;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+    return cache.get(dev, [dev](Device &d) {
+        return cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+               (d.clusters = a2av::g128_gemm_max_clusters()) > 0;
+    });
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Codes [groups][rows][K]: boxes of 128 codes x box_rows rows, 128-byte swizzled.
+bool codes_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t K, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(groups)};
+    const cuuint64_t pitch = static_cast<cuuint64_t>(K);
+    const cuuint64_t strides[2] = {pitch, groups > 1 ? pitch * rows : pitch};  // (the second is not used with one group)
+    const cuuint32_t box[3] = {128, box_rows, 1}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 16-bit outputs [rows][cols], boxes of 32 x 32, 64-byte swizzled.
+bool out_map(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, bool bf16) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};
+    const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+a2av_status validate(const a2av_gmm_g128_desc *d) {
+    if (!d) return A2AV_ERR_NULLPTR;
+    if (d->W < 1 || d->e < 1 || d->e > a2av::kMaxExperts) return A2AV_ERR_INVALID;
+    if (static_cast<int64_t>(d->W) * d->e > a2av::kMaxSegments) return A2AV_ERR_INVALID;
+    if (d->H1 <= 0 || d->H1 >= 65536 || d->N1 <= 0 || d->N1 >= 65536) return A2AV_ERR_INVALID;
+    if (d->A < 0 || d->A > INT32_MAX) return A2AV_ERR_INVALID;
+    if (d->dtype != A2AV_BF16 && d->dtype != A2AV_FP16) return A2AV_ERR_INVALID;
+    if (d->qtype != A2AV_Q_E4M3FN && d->qtype != A2AV_Q_E5M2) return A2AV_ERR_INVALID;
+    if (d->H1 % 128 != 0 || d->N1 % 8 != 0) return A2AV_ERR_UNSUPPORTED;
+    return A2AV_OK;
+}
+
+size_t staged_bytes(const a2av_gmm_g128_desc *d) {
+    return d->W > 1 ? round256(static_cast<size_t>(d->A) * d->H1) : 0;
+}
+
+// Mean rows of a (source, expert) run from which whole halves are read in place.
+constexpr int64_t kLongRun = 96;
+
+}  // namespace
+
+extern "C" {
+
+a2av_status a2av_gmm_g128_workspace_size(const a2av_gmm_g128_desc *desc, size_t *bytes) {
+    if (!desc || !bytes) return A2AV_ERR_NULLPTR;
+    const a2av_status s = validate(desc);
+    if (s != A2AV_OK) return s;
+    *bytes = kStatusBytes + staged_bytes(desc);
+    return A2AV_OK;
+}
+
+a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut_q, const float *ataOut_s,
+                              const int32_t *recvCounts, const void *gmmWeight_q, const float *gmmWeight_s, void *gmmY,
+                              void *workspace, size_t workspace_bytes, a2av_stream_t stream_handle) {
+    const a2av_status vs = validate(desc);
+    if (vs != A2AV_OK) return vs;
+    const a2av_gmm_g128_desc &d = *desc;
+    if (!recvCounts || !gmmWeight_q || !gmmWeight_s || !workspace) return A2AV_ERR_NULLPTR;
+    if (d.A > 0 && (!ataOut_q || !ataOut_s || !gmmY)) return A2AV_ERR_NULLPTR;
+    for (const void *p : {ataOut_q, gmmWeight_q, static_cast<const void *>(gmmY)})
+        if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
+    for (const void *p : {static_cast<const void *>(ataOut_s), static_cast<const void *>(gmmWeight_s),
+                          static_cast<const void *>(recvCounts)})
+        if (!aligned(p, 4)) return A2AV_ERR_UNSUPPORTED;
+    if (workspace_bytes < kStatusBytes + staged_bytes(desc) || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    const Device *dev = device_of();
+    if (!dev) return A2AV_ERR_CUDA;
+    const bool bf16 = d.dtype == A2AV_BF16;
+
+    a2av::G128Launch g;
+    std::memset(&g, 0, sizeof g);
+    g.recvCounts = recvCounts;
+    g.W = d.W;
+    g.e = d.e;
+    g.A = static_cast<int32_t>(d.A);
+    g.K = static_cast<int32_t>(d.H1);
+    g.N = static_cast<int32_t>(d.N1);
+    g.qtype = d.qtype;
+    g.xs = ataOut_s;
+    g.ws = gmmWeight_s;
+    g.y = gmmY;
+    g.status = static_cast<int32_t *>(workspace);
+    g.write_status = 1;
+    g.wait_limit_ns = kWaitLimitNs;
+    const int64_t row_tiles = ceil_div(d.A, 256);
+    g.bn = (row_tiles + d.e / 2) * ceil_div(d.N1, 128) <= dev->clusters ? 128 : 256;
+    const void *rows = ataOut_q;
+    if (d.W > 1 && d.A > 0) {
+        // Expert-major rows: all of them, or only the 128-row halves of a tile that
+        // straddle a run's end, the others being read in place.  (The copies take the
+        // rows as 16-bit elements.)
+        void *dst = static_cast<uint8_t *>(workspace) + kStatusBytes;
+        g.direct_halves = d.A >= kLongRun * d.W * d.e;
+        const a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status, 1, 1, 8};
+        const a2av::StageRowsLaunch sl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status};
+        if ((g.direct_halves ? a2av::launch_permute(pl, dev->sms, stream) : a2av::launch_stage_rows(sl, dev->sms, stream)) !=
+            cudaSuccess)
+            return A2AV_ERR_CUDA;
+        g.after_permute = 1;
+        g.write_status = 0;
+        rows = dst;
+        if (g.direct_halves && !codes_map(&g.tmDirect, ataOut_q, 1, d.A, d.H1, 128)) return A2AV_ERR_CUDA;
+    }
+    if (d.A > 0 && (!codes_map(&g.tmA, rows, 1, d.A, d.H1, 128) ||
+                    !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, static_cast<uint32_t>(g.bn / 2)) ||
+                    !out_map(&g.tmY, gmmY, d.A, d.N1, bf16)))
+        return A2AV_ERR_CUDA;
+    const int64_t tiles = (row_tiles + d.e) * ceil_div(d.N1, g.bn);
+    g.grid = static_cast<int32_t>(2 * std::max<int64_t>(1, std::min<int64_t>(dev->clusters, tiles)));
+    return a2av::launch_g128_gemm(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,414 @@
+// Grouped GEMM of 8-bit rows with a float32 scale per 128 codes, on tcgen05
+// tensor cores (sm_103a): tiles of 256 rows x 256 (or 128) columns on CTA pairs.
+//
+//   y[i][n] = sum over b of xs[i][b] ws[n / 128][b] sum over k in b of x[i][k] w[n][k]
+//
+// The scales are arbitrary floats, so the tensor cores cannot apply them: each
+// block of 128 codes along K is a product of its own (four MMAs of K = 32 that
+// start a TMEM accumulator afresh), which the epilogue warps multiply by its
+// scales and add to sums in their registers while the next block is multiplied
+// into another accumulator.  A lane's row has one scale and a warp's 128
+// columns one, so a block costs a lane one product and 64 packed FMAs.
+//
+// Per CTA: warp 0 loads (a stage is one K block: 16 KB of rows, 8 or 16 KB of
+// weights, 128-byte swizzle), warp 1 issues the MMAs (even CTA), warps 2-9 sum
+// and store, two for each TMEM lane quarter, half of the columns each.
+// Every wait is bounded, as in the other GEMMs.
+#include <algorithm>
+
+#include "activation.cuh"
+#include "g128.h"
+#include "pair.cuh"
+#include "pdl.cuh"
+#include "segments.cuh"
+
+namespace a2av {
+
+namespace {
+
+constexpr int BM = 128;             // rows of a CTA
+constexpr int TILE_M = 2 * BM;
+constexpr int BK = 128;             // codes of a K block, which has one scale
+constexpr int kMmaWarp = 1;
+constexpr int kEpiWarp0 = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kEpiStageBytes = 32 * 64;  // of a warp: 32 x 32 results
+
+template <int BN>
+struct Shape {
+    static constexpr uint32_t kA = BM * BK, kB = BN / 2 * BK;
+    static constexpr uint32_t kStageBytes = kA + kB;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr int kAccs = kTmemCols / BN;  // accumulators
+    static constexpr int kCols = BN / 2;          // columns of an epilogue warp
+};
+
+struct Group {
+    int32_t row0, rows, tile_start;
+};
+struct Control {
+    uint64_t full[8], empty[8];
+    uint64_t tfull[4], tempty[4];
+    uint32_t tmem_base;
+    int32_t abort;
+    int32_t total_tiles;
+    Group g[kMaxExperts + 1];
+    SegmentTable seg;
+};
+constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
+
+template <int BN>
+constexpr size_t smem_bytes() {
+    return 1024 + Shape<BN>::kStages * Shape<BN>::kStageBytes + kEpiWarps * kEpiStageBytes + kControlBytes;
+}
+static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory per CTA");
+
+struct Tile {
+    int g, m, n;
+};
+__device__ __forceinline__ Tile tile_at(const Control &c, int t, int tn) {
+    int g = 0;
+    while (t >= c.g[g + 1].tile_start) ++g;
+    const int local = t - c.g[g].tile_start;
+    return {g, local / tn, local % tn};
+}
+
+// kind::f8f6f4: fp32 accumulator, both operands of one 8-bit format (0 E4M3, 1
+// E5M2) and K-major, M x N.
+__device__ __forceinline__ uint32_t instr_desc_f8(uint32_t qtype, uint32_t M, uint32_t N) {
+    return (1u << 4) | (qtype << 7) | (qtype << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 lanes x 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// This warp's loads have arrived; r is used only behind this.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// The epilogue's bounded wait, in line (a call would put its sums aside), with
+// one answer for the warp.
+__device__ __forceinline__ bool wait_in_line(int32_t *abort_flag, uint32_t bar, uint32_t parity, int32_t *status,
+                                             uint64_t limit_ns) {
+    bool ok = pair::try_wait_cluster(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        for (int i = 1; !(ok = pair::try_wait_cluster(bar, parity)); ++i) {
+            if (i % 64 != 0) continue;
+            if (*reinterpret_cast<volatile int32_t *>(abort_flag)) break;
+            if (global_timer_ns() - t0 > limit_ns) {
+                *reinterpret_cast<volatile int32_t *>(abort_flag) = 1;
+                atomicOr(status, kStatusTimeout);
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <bool BF16, int BN>
+__global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_constant__ G128Launch p) {
+    using S = Shape<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+    const uint32_t epi0 = base + S::kStages * S::kStageBytes;
+    Control &C = *reinterpret_cast<Control *>(base_ptr + S::kStages * S::kStageBytes + kEpiWarps * kEpiStageBytes);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = pair::cluster_rank();
+    const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
+    const int tn = (p.N + BN - 1) / BN, kblocks = p.K / BK;
+
+    if (warp == 0) {
+        // (A kernel that this one overlaps has waited for all before it.)
+        if (!p.after_permute) pdl_wait();
+        const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, C.seg, lane);
+        int row0 = 0, rows = 0, tiles = 0;
+        if (lane < p.e) {
+            row0 = C.seg.dst[lane * p.W];
+            rows = C.seg.dst[(lane + 1) * p.W] - row0;
+            tiles = good ? blocks_of(rows, TILE_M) * tn : 0;
+        }
+        int inc = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane < p.e) C.g[lane] = Group{row0, rows, inc - tiles};
+        if (lane == 31) {
+            C.g[p.e] = Group{0, 0, inc};
+            C.total_tiles = inc;
+            C.abort = 0;
+            if (blockIdx.x == 0) {
+                if (p.write_status) *p.status = good ? 0 : kStatusBadCounts;
+                else if (!good) atomicOr(p.status, kStatusBadCounts);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
+    } else if (warp == kEpiWarp0) {
+        if (lane == 0) {
+            for (int s = 0; s < S::kStages; ++s) {
+                mbar_init(smem_u32(&C.full[s]), 1);
+                mbar_init(smem_u32(&C.empty[s]), 1);
+            }
+            for (int a = 0; a < S::kAccs; ++a) {
+                mbar_init(smem_u32(&C.tfull[a]), 1);
+                mbar_init(smem_u32(&C.tempty[a]), 2 * kEpiWarps);
+            }
+            fence_barrier_init();
+        }
+    } else if (warp == kEpiWarp0 + 1 && lane == 0) {
+        prefetch_tensormap(&p.tmA);
+        prefetch_tensormap(&p.tmB);
+        prefetch_tensormap(&p.tmY);
+        if (p.direct_halves) prefetch_tensormap(&p.tmDirect);
+    }
+    tc_fence_before_sync();
+    pair::sync_all();
+    tc_fence_after_sync();
+
+    const int total = C.total_tiles;
+    const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
+    const uint32_t tfull0 = smem_u32(&C.tfull[0]), tempty0 = smem_u32(&C.tempty[0]);
+
+    if (warp == 0) {
+        // =========================================================== producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true, all_there = !p.after_permute;
+            for (int t = unit; t < total && ok; t += nunits) {
+                const Tile w = tile_at(C, t, tn);
+                const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
+                // This CTA's first row; without a row of its own, any one (nothing of it is stored).
+                const int from = w.m * TILE_M + static_cast<int>(rank) * BM;
+                const bool live = from < C.g[w.g].rows;
+                int row = C.g[w.g].row0 + (live ? from : 0);
+                const CUtensorMap *ta = &p.tmA;
+                if (p.direct_halves && live && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
+                    ta = &p.tmDirect;
+                    row = source_row(C.seg, p.W, p.e, row);
+                } else if (!all_there) {
+                    pdl_wait();
+                    all_there = true;
+                }
+                const int col = w.n * BN + static_cast<int>(rank) * (BN / 2);
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const int s = it % S::kStages;
+                    if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / S::kStages) & 1) ^ 1, p.status,
+                                          p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t own = full0 + 8 * s, bar = pair::map_to_rank(own, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * S::kStageBytes);
+                    const uint32_t st = base + s * S::kStageBytes;
+                    pair::load_3d(st, ta, bar, kb * BK, row, 0);
+                    pair::load_3d(st + S::kA, &p.tmB, bar, kb * BK, col, w.g);
+                }
+            }
+            pdl_trigger();
+            if (!all_there) pdl_wait();  // (a kernel's end implies that of all before it)
+            for (int i = 0; i < S::kStages && ok; ++i, ++it)
+                ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % S::kStages), ((it / S::kStages) & 1) ^ 1, p.status,
+                                      p.wait_limit_ns);
+            if (!ok) pair::let_settle();
+        }
+    } else if (warp == kMmaWarp) {
+        // =========================================================== MMA issuer
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = instr_desc_f8(static_cast<uint32_t>(p.qtype), TILE_M, BN);
+            const uint64_t a_desc0 = smem_desc(base, 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(base + S::kA, 16, 1024, kSwizzle128B);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = unit; t < total && ok; t += nunits) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    const int s = it % S::kStages, acc = it % S::kAccs;
+                    if (!pair::wait_phase(&C.abort, tempty0 + 8 * acc, ((it / S::kAccs) & 1) ^ 1, p.status,
+                                          p.wait_limit_ns) ||
+                        !pair::wait_phase(&C.abort, full0 + 8 * s, (it / S::kStages) & 1, p.status, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t off = (s * S::kStageBytes) >> 4;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 32; ++kk)
+                        mma_f8_pair(C.tmem_base + acc * BN, a_desc0 + off + 2 * kk, b_desc0 + off + 2 * kk, idesc, kk > 0);
+                    pair::commit(empty0 + 8 * s);
+                    pair::commit(tfull0 + 8 * acc);
+                }
+            }
+        }
+    } else {
+        // =========================================================== sums and stores
+        const int q = warp & 3;
+        const int half = (warp - kEpiWarp0) / 4;
+        const uint32_t stage = epi0 + static_cast<uint32_t>(warp - kEpiWarp0) * kEpiStageBytes;
+        const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * S::kCols;
+        const int scale_rows = (p.N + 127) / 128;  // of an expert's weights
+        const float *xs = p.xs, *ws = p.ws;        // of this lane's row, of this warp's columns
+        float xn[2] = {0, 0}, wn[2] = {0, 0};      // of the next K blocks
+        bool valid = false;
+        // The scales of a tile's first blocks, asked for ahead of the tile.
+        const auto prepare = [&](int t) {
+            const Tile w = tile_at(C, t, tn);
+            const int r = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
+            valid = r < C.g[w.g].rows;
+            const int src = valid ? source_row(C.seg, p.W, p.e, C.g[w.g].row0 + r) : 0;
+            xs = p.xs + static_cast<size_t>(src) * kblocks;
+            const int block = min((w.n * BN + half * S::kCols) / 128, scale_rows - 1);
+            ws = p.ws + (static_cast<size_t>(w.g) * scale_rows + block) * kblocks;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (i < kblocks) {
+                    xn[i] = xs[i];
+                    wn[i] = ws[i];
+                }
+            }
+        };
+        uint32_t it = 0;
+        bool ok = true;
+        if (unit < total) prepare(unit);
+        for (int t = unit; t < total && ok; t += nunits) {
+            f32x2 sum[S::kCols / 2];
+#pragma unroll
+            for (int j = 0; j < S::kCols / 2; ++j) sum[j] = 0;
+            const bool row_valid = valid;
+            for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                const int acc = it % S::kAccs;
+                const f32x2 scale = both(xn[0] * wn[0]);
+                xn[0] = xn[1];
+                wn[0] = wn[1];
+                if (kb + 2 < kblocks) {
+                    xn[1] = xs[kb + 2];
+                    wn[1] = ws[kb + 2];
+                }
+                if (!wait_in_line(&C.abort, tfull0 + 8 * acc, (it / S::kAccs) & 1, p.status, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                uint32_t r[2][16];
+                tmem_ld16(t_base + acc * BN, r[0]);
+#pragma unroll
+                for (int c = 0; c < S::kCols / 16; ++c) {
+                    tmem_ld16_wait(r[c & 1]);
+                    if (c + 1 < S::kCols / 16) {
+                        tmem_ld16(t_base + acc * BN + 16 * (c + 1), r[(c + 1) & 1]);
+                    } else {  // all of it is in registers
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) pair::arrive_reads_done(pair::map_to_rank(tempty0 + 8 * acc, 0));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t *v = &r[c & 1][2 * j];
+                        sum[8 * c + j] =
+                            fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), scale, sum[8 * c + j]);
+                    }
+                }
+            }
+            if (!ok) break;
+            const Tile w = tile_at(C, t, tn);
+            const int row0 = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;
+            const int col0 = w.n * BN + half * S::kCols;
+            if (t + nunits < total) prepare(t + nunits);
+            // Each 32 x 32 block is turned around in this warp's 2 KB (64-byte rows, the
+            // 16-byte chunk index XORed with (row / 2) % 4) and stored by TMA, or row by
+            // row where the group ends inside it.
+            const uint32_t mask = __ballot_sync(0xffffffffu, row_valid);
+            if (mask == 0) continue;
+#pragma unroll
+            for (int i = 0; i < S::kCols / 32; ++i) {
+                const int col = col0 + 32 * i;
+                if (col >= p.N) break;
+                if (lane == 0) bulk_wait_read_0();  // the block before this one has left
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x2(&v)[4] = *reinterpret_cast<const f32x2(*)[4]>(&sum[16 * i + 4 * j]);
+                    st_shared_v4(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8<BF16>(v));
+                }
+                if (mask == 0xffffffffu) {
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&p.tmY, stage, col, row0);
+                        bulk_commit_group();
+                    }
+                } else {
+                    __syncwarp();
+                    const int j = lane & 3;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int rr = 8 * k + (lane >> 2);
+                        const uint4 v = ld_shared_v4(stage + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
+                        if (((mask >> rr) & 1u) && col + 8 * j < p.N)
+                            st_stream_v4(static_cast<uint16_t *>(p.y) + static_cast<size_t>(row0 + rr) * p.N + col + 8 * j,
+                                         v);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) bulk_wait_all();  // this warp's stores have landed
+    }
+
+    __syncwarp();
+    tc_fence_before_sync();
+    pair::sync_all();
+    if (warp == kMmaWarp) {
+        tc_fence_after_sync();
+        pair::tmem_free_pair(C.tmem_base, kTmemCols);
+    }
+}
+
+template <bool BF16, int BN>
+cudaError_t launch_shape(const G128Launch &p, cudaStream_t stream) {
+    auto kern = g128_gemm_kernel<BF16, BN>;
+    const cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<BN>()));
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kern, p.grid, kThreads, smem_bytes<BN>(), 2, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream) {
+    if (p.bn == 256) return bf16 ? launch_shape<true, 256>(p, stream) : launch_shape<false, 256>(p, stream);
+    return bf16 ? launch_shape<true, 128>(p, stream) : launch_shape<false, 128>(p, stream);
+}
+
+// Both widths need nearly all of an SM's shared memory: one CTA an SM.
+int g128_gemm_max_clusters() { return max_clusters(g128_gemm_kernel<true, 256>, kThreads, smem_bytes<256>(), 2); }
+
+}  // namespace a2av
