@@ -37,13 +37,14 @@ EXPORTS = ("a2av_gmm_workspace_size", "a2av_gmm_run", "a2av_gmm_read_device_stat
            "a2av_gated_workspace_size", "a2av_gated_run", "a2av_gated_backward",
            "a2av_gmm_backward_workspace_size", "a2av_gmm_backward",
            "a2av_layer_norm", "a2av_layer_norm_backward", "a2av_layer_norm_backward_workspace_size",
-           "a2av_gmm_g128_workspace_size", "a2av_gmm_g128_run")
+           "a2av_gmm_g128_workspace_size", "a2av_gmm_g128_run", "a2av_moe_workspace_size", "a2av_moe_run")
 _FFN_EXPORTS = EXPORTS[EXPORTS.index("a2av_rms_norm"):]
 
 # a2av_qtype / a2av_qmode of include/a2av_quant_reduce.h.
 QTYPES = {"e4m3fn": 0, "e5m2": 1, "int8": 2}
 QMODES = {"mx": 0, "group128": 1}
 ACTS = {"silu": 0, "gelu_tanh": 1}  # a2av_act of include/a2av_ffn.h
+SCORES = {"softmax": 0, "sigmoid": 1}  # a2av_score of include/a2av_moe.h
 
 
 class A2avError(RuntimeError):
@@ -96,6 +97,14 @@ class G128Desc(ctypes.Structure):
     _fields_ = [("W", ctypes.c_int32), ("e", ctypes.c_int32),
                 ("A", ctypes.c_int64), ("H1", ctypes.c_int64), ("N1", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("qtype", ctypes.c_int32)]
+
+
+class MoeDesc(ctypes.Structure):
+    """a2av_moe_desc of include/a2av_moe.h."""
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("H", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("router_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -169,6 +178,8 @@ def load_library(path: str):
     L.a2av_layer_norm_backward.argtypes = [i64, i64, i32] + [p] * 10 + [sz, p]
     L.a2av_gmm_g128_workspace_size.argtypes = [ctypes.POINTER(G128Desc), psz]
     L.a2av_gmm_g128_run.argtypes = [ctypes.POINTER(G128Desc)] + [p] * 7 + [sz, p]
+    L.a2av_moe_workspace_size.argtypes = [ctypes.POINTER(MoeDesc), psz]
+    L.a2av_moe_run.argtypes = [ctypes.POINTER(MoeDesc)] + [p] * 11 + [sz, p]
     for name in _FFN_EXPORTS:
         getattr(L, name).restype = ctypes.c_int
     return L
@@ -890,3 +901,57 @@ class G128Plan:
                  recvCounts.data_ptr(), gmmWeight_q.data_ptr(), gmmWeight_s.data_ptr(), gmmY.data_ptr(), ws.data_ptr(),
                  ws.numel())
         return gmmY
+
+
+# ---- a whole expert layer for a few tokens (include/a2av_moe.h)
+
+
+class MoeOut(NamedTuple):
+    y: torch.Tensor        # [T, H]
+    experts: torch.Tensor  # int32 [T, K], the largest score (+ bias) first
+    weights: torch.Tensor  # float32 [T, K]
+
+
+class MoePlan:
+    """Descriptor + workspace of a whole expert layer for T tokens (up to 64): the router's choice of K of E experts, their
+    gated blocks and down projections, and the weighted sum.  score: "softmax" or "sigmoid"; renormalise: the chosen scores
+    are divided by their sum; scale: of the weights; router_dtype: dtype or float32.  The workspace serves one call at a
+    time: calls of one plan on different streams have to be ordered by the caller."""
+
+    def __init__(self, T, E, K, H, N, dtype=torch.bfloat16, act="silu", score="softmax", renormalise=True, scale=1.0,
+                 router_dtype=None, device=None):
+        if dtype not in DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float16, got {dtype}")
+        self.router_dtype = dtype if router_dtype is None else router_dtype
+        if self.router_dtype not in (dtype, torch.float32):
+            raise TypeError(f"router_dtype must be {dtype} or float32, got {router_dtype}")
+        self.desc = MoeDesc(T, E, K, H, N, DTYPES[dtype], 2 if self.router_dtype == torch.float32 else DTYPES[dtype],
+                            _named(ACTS, act, "act"), _named(SCORES, score, "score"), int(bool(renormalise)), scale)
+        self.dtype = dtype
+        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.workspace = torch.empty(_size("a2av_moe_workspace_size", ctypes.byref(self.desc)), dtype=torch.uint8,
+                                     device=self.device)
+
+    def run(self, x, router, gate, up, down, bias=None, residual=None, out: Optional[MoeOut] = None,
+            stream=None) -> MoeOut:
+        """x [T, H], router [E, H], gate and up [E, H, N], down [E, N, H], bias float32 [E] (added to the scores for the
+        choice only), residual [T, H] (added to the result).  `out`: an earlier result, whose tensors are written again;
+        its y may be x or the residual."""
+        d, dtype, ws, device = self.desc, self.dtype, self.workspace, self.workspace.get_device()
+        T, E, K, H, N = d.T, d.E, d.K, d.H, d.N
+        _is(x, "x", dtype, (T, H), device)
+        _is(router, "router", self.router_dtype, (E, H), device)
+        _is(gate, "gate", dtype, (E, H, N), device)
+        _is(up, "up", dtype, (E, H, N), device)
+        _is(down, "down", dtype, (E, N, H), device)
+        if bias is not None:
+            _is(bias, "bias", torch.float32, (E,), device)
+        if residual is not None:
+            _is(residual, "residual", dtype, (T, H), device)
+        y = _out(out.y if out else None, "y", dtype, (T, H), x, stream)
+        experts = _out(out.experts if out else None, "experts", torch.int32, (T, K), ws, stream)
+        weights = _out(out.weights if out else None, "weights", torch.float32, (T, K), ws, stream)
+        _enqueue("a2av_moe_run", device, stream, ctypes.byref(d), x.data_ptr(), router.data_ptr(), _at(bias),
+                 gate.data_ptr(), up.data_ptr(), down.data_ptr(), _at(residual), y.data_ptr(), experts.data_ptr(),
+                 weights.data_ptr(), ws.data_ptr(), ws.numel())
+        return MoeOut(y, experts, weights)

@@ -1,10 +1,7 @@
 // C ABI of the grouped product of 8-bit rows with a float32 scale per 128
 // (declared in include/a2av_gmm_g128.h): argument checks, tensor maps, launches.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "a2av_gmm_g128.h"
 #include "ffn.h"
@@ -12,6 +9,7 @@
 #include "kernels.h"
 #include "per_device.h"
 #include "plan.cuh"
+#include "tensor_map.h"
 
 namespace {
 
@@ -35,23 +33,9 @@ const Device *device_of() {
     });
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // Codes [groups][rows][K]: boxes of 128 codes x box_rows rows, 128-byte swizzled.
 bool codes_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t K, uint32_t box_rows) {
-    auto fn = encode_fn();
+    auto fn = a2av::tensor_map_encode();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(groups)};
@@ -65,7 +49,7 @@ bool codes_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, in
 
 // 16-bit outputs [rows][cols], boxes of 32 x 32, 64-byte swizzled.
 bool out_map(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, bool bf16) {
-    auto fn = encode_fn();
+    auto fn = a2av::tensor_map_encode();
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};

@@ -1,0 +1,49 @@
+// Host-side launch descriptions of the expert layer for a few tokens
+// (a2av_moe.h; internal to the library).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "a2av_moe.h"
+
+namespace a2av {
+
+constexpr int kMoeTokens = 64;
+constexpr int kMoeExperts = 256;
+constexpr int kMoeChosen = 8;
+
+struct MoeRouterLaunch {
+    int32_t T, E, H;
+    const void *x, *router;  // [T, H], [E, H]
+    float *logits;           // [T, E]
+    int32_t *status;         // cleared
+};
+cudaError_t launch_moe_router(const MoeRouterLaunch &p, bool bf16, bool router32, cudaStream_t stream);
+
+// What the choice of experts is made from.
+struct MoeChoice {
+    int32_t T, E, K, score, renormalise;
+    float scale;
+    const float *logits, *bias;
+    int32_t *experts;  // [T, K], or NULL
+    float *weights;    // likewise
+};
+
+struct MoeRowsLaunch {
+    MoeChoice choice;
+    int32_t H, N;
+    const void *x, *residual;
+    void *h;             // [2][T * K][N]: the gated block's values, in two summands
+    void *y;
+    int32_t *status;
+    uint64_t wait_limit_ns;
+    int32_t split, grid, stages;  // set by the launch
+    CUtensorMap tmA[2];  // gate and up [E][H][N], or down [E][N][H] (the first): box 64 columns x 64
+};
+cudaError_t launch_moe_gated(MoeRowsLaunch p, bool bf16, int act, cudaStream_t stream);
+cudaError_t launch_moe_down(MoeRowsLaunch p, bool bf16, cudaStream_t stream);
+
+}  // namespace a2av
