@@ -35,14 +35,17 @@ struct MoeChoice {
 struct MoeRowsLaunch {
     MoeChoice choice;
     int32_t H, N;
-    const void *x, *residual;
-    void *h;             // [2][T * K][N]: the gated block's values, in two summands
+    const void *residual;
+    void *h;             // [2][T * K][N]: the gated block's values, expert after expert, in two summands
     void *y;
     int32_t *status;
     uint64_t wait_limit_ns;
     int32_t split, grid, stages;  // set by the launch
     CUtensorMap tmA[2];  // gate and up [E][H][N], or down [E][N][H] (the first): box 64 columns x 64
+    CUtensorMap tmX;     // x [1][T][H], or h [2][T * K][N]: box 64 x moe_unit_rows() x all
 };
+// Rows that a product takes at a time: 16, 32 or 64.
+int moe_unit_rows(int T, int E, int K, bool down);
 cudaError_t launch_moe_gated(MoeRowsLaunch p, bool bf16, int act, cudaStream_t stream);
 cudaError_t launch_moe_down(MoeRowsLaunch p, bool bf16, cudaStream_t stream);
 

@@ -15,15 +15,17 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bound on every device-side 
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Weights [groups][rows][cols]: boxes of 64 columns x 64 rows, 128-byte swizzled.
-bool weight_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t cols, bool bf16) {
+// [groups][rows][cols]: boxes of 64 columns x box_rows rows x box_groups, 128-byte swizzled.
+bool tile_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, int64_t cols, bool bf16, int box_rows,
+              int box_groups) {
     auto fn = a2av::tensor_map_encode();
     if (!fn) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(groups)};
     const cuuint64_t pitch = static_cast<cuuint64_t>(cols) * 2;
     const cuuint64_t strides[2] = {pitch, groups > 1 ? pitch * rows : pitch};  // (the second is not used with one group)
-    const cuuint32_t box[3] = {64, 64, 1}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_groups)};
+    const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(ptr),
               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -82,15 +84,17 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
     g.choice = a2av::MoeChoice{d.T, d.E, d.K, d.score, d.renormalise != 0, d.scale, r.logits, bias, experts, weights};
     g.H = static_cast<int32_t>(d.H);
     g.N = static_cast<int32_t>(d.N);
-    g.x = x;
     g.residual = residual;
     g.h = at + kStatusBytes + logit_bytes(d);
     g.y = y;
     g.status = r.status;
     g.wait_limit_ns = kWaitLimitNs;
     a2av::MoeRowsLaunch o = g;
-    if (d.T > 0 && (!weight_map(&g.tmA[0], gate, d.E, d.H, d.N, bf16) || !weight_map(&g.tmA[1], up, d.E, d.H, d.N, bf16) ||
-                    !weight_map(&o.tmA[0], down, d.E, d.N, d.H, bf16)))
+    if (d.T > 0 && (!tile_map(&g.tmA[0], gate, d.E, d.H, d.N, bf16, 64, 1) ||
+                    !tile_map(&g.tmA[1], up, d.E, d.H, d.N, bf16, 64, 1) ||
+                    !tile_map(&g.tmX, x, 1, d.T, d.H, bf16, a2av::moe_unit_rows(d.T, d.E, d.K, false), 1) ||
+                    !tile_map(&o.tmA[0], down, d.E, d.N, d.H, bf16, 64, 1) ||
+                    !tile_map(&o.tmX, g.h, 2, d.T * d.K, d.N, bf16, a2av::moe_unit_rows(d.T, d.E, d.K, true), 2)))
         return A2AV_ERR_CUDA;
     if (a2av::launch_moe_router(r, bf16, d.router_dtype == A2AV_FP32, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     if (d.T == 0) return A2AV_OK;  // (the status is stored)
