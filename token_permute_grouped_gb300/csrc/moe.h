@@ -15,11 +15,16 @@ constexpr int kMoeTokens = 64;
 constexpr int kMoeExperts = 256;
 constexpr int kMoeChosen = 8;
 
+// CTAs of the products: one an SM of a GB300.  Not asked of the device: the
+// workspace's size depends on it, and is asked for without one.
+constexpr int kMoeCtas = 152;
+
 struct MoeRouterLaunch {
     int32_t T, E, H;
     const void *x, *router;  // [T, H], [E, H]
     float *logits;           // [T, E]
     int32_t *status;         // cleared
+    int32_t *arrivals;       // [2][kMoeCtas], cleared
 };
 cudaError_t launch_moe_router(const MoeRouterLaunch &p, bool bf16, bool router32, cudaStream_t stream);
 
@@ -40,7 +45,9 @@ struct MoeRowsLaunch {
     void *y;
     int32_t *status;
     uint64_t wait_limit_ns;
-    int32_t split, grid, stages;  // set by the launch
+    int32_t stages;      // set by the launch
+    float *sums;         // [kMoeCtas][2][T][256 or 128]: shares of jobs that several CTAs have
+    int32_t *arrivals;   // [kMoeCtas], 0: of those CTAs, by the first
     CUtensorMap tmA[2];  // gate and up [E][H][N], or down [E][N][H] (the first): box 64 columns x 64
     CUtensorMap tmX;     // x [1][T][H], or h [2][T * K][N]: box 64 x moe_unit_rows() x all
 };

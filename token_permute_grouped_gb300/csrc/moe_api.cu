@@ -46,7 +46,14 @@ a2av_status validate(const a2av_moe_desc *d) {
 }
 
 size_t logit_bytes(const a2av_moe_desc &d) { return round256(static_cast<size_t>(d.T) * d.E * 4); }
+constexpr size_t kArrivalBytes = 2 * a2av::kMoeCtas * 4;
+// Shares of jobs; the second product's, half as large, take the place of the first's.
+size_t sum_bytes(const a2av_moe_desc &d) { return static_cast<size_t>(a2av::kMoeCtas) * 2 * d.T * 1024; }
 size_t value_bytes(const a2av_moe_desc &d) { return round256(static_cast<size_t>(d.T) * d.K * d.N * 4); }
+
+size_t workspace_bytes_of(const a2av_moe_desc &d) {
+    return kStatusBytes + round256(kArrivalBytes) + logit_bytes(d) + value_bytes(d) + sum_bytes(d);
+}
 
 }  // namespace
 
@@ -56,7 +63,7 @@ a2av_status a2av_moe_workspace_size(const a2av_moe_desc *desc, size_t *bytes) {
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + logit_bytes(*desc) + value_bytes(*desc);
+    *bytes = workspace_bytes_of(*desc);
     return A2AV_OK;
 }
 
@@ -71,25 +78,29 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
     for (const void *p : {x, router, static_cast<const void *>(bias), gate, up, down, residual, static_cast<const void *>(y)})
         if (!aligned(p, 16)) return A2AV_ERR_UNSUPPORTED;
     if (!aligned(experts, 4) || !aligned(weights, 4)) return A2AV_ERR_UNSUPPORTED;
-    if (workspace_bytes < kStatusBytes + logit_bytes(d) + value_bytes(d) || !aligned(workspace, 256))
+    if (workspace_bytes < workspace_bytes_of(d) || !aligned(workspace, 256))
         return A2AV_ERR_WORKSPACE;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     const bool bf16 = d.dtype == A2AV_BF16;
-    uint8_t *at = static_cast<uint8_t *>(workspace);
+    uint8_t *const arrivals = static_cast<uint8_t *>(workspace) + kStatusBytes;
+    uint8_t *const logits = arrivals + round256(kArrivalBytes), *const values = logits + logit_bytes(d);
 
-    a2av::MoeRouterLaunch r{d.T, d.E, static_cast<int32_t>(d.H), x, router, reinterpret_cast<float *>(at + kStatusBytes),
-                            static_cast<int32_t *>(workspace)};
+    a2av::MoeRouterLaunch r{d.T, d.E, static_cast<int32_t>(d.H), x, router, reinterpret_cast<float *>(logits),
+                            static_cast<int32_t *>(workspace), reinterpret_cast<int32_t *>(arrivals)};
     a2av::MoeRowsLaunch g;
     std::memset(&g, 0, sizeof g);
     g.choice = a2av::MoeChoice{d.T, d.E, d.K, d.score, d.renormalise != 0, d.scale, r.logits, bias, experts, weights};
     g.H = static_cast<int32_t>(d.H);
     g.N = static_cast<int32_t>(d.N);
     g.residual = residual;
-    g.h = at + kStatusBytes + logit_bytes(d);
+    g.h = values;
+    g.sums = reinterpret_cast<float *>(values + value_bytes(d));
+    g.arrivals = r.arrivals;
     g.y = y;
     g.status = r.status;
     g.wait_limit_ns = kWaitLimitNs;
     a2av::MoeRowsLaunch o = g;
+    o.arrivals += a2av::kMoeCtas;
     if (d.T > 0 && (!tile_map(&g.tmA[0], gate, d.E, d.H, d.N, bf16, 64, 1) ||
                     !tile_map(&g.tmA[1], up, d.E, d.H, d.N, bf16, 64, 1) ||
                     !tile_map(&g.tmX, x, 1, d.T, d.H, bf16, a2av::moe_unit_rows(d.T, d.E, d.K, false), 1) ||

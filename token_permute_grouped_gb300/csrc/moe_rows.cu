@@ -4,12 +4,12 @@
 // Both are bound by the bytes of the weights, which stream from HBM through
 // shared memory into the tensor cores as the 128-row operand of tcgen05.mma
 // (M, MN-major as they lie in memory); the few rows are the narrow one (N: 16 to
-// 64, K-major).  The first kernel's tile is 64 columns of Wg and the same of Wu;
-// the second's 128 columns of Wd.  A contraction is cut over the CTAs of a
-// cluster, whose sums are joined in order through distributed shared memory: the
-// same result every time.
+// 64, K-major).  A tile is 128 columns of a matrix: CTAs beside each other read
+// different places, and 256 bytes of a weight's row at a time come at 6.8 TB/s
+// from HBM where 128 come at 5.5.
 //
-//   first:  a job is (expert, 64 columns); its contraction is H.  All tokens are
+//   first:  a job is (expert, 128 columns); its contraction is H, each K block one
+//           of Wg and one of Wu, into an accumulator each.  All tokens are
 //           multiplied, which costs nothing beside the weights and needs no
 //           gathering; the rows of those that chose the expert are kept, and
 //           stored expert after expert.
@@ -21,11 +21,16 @@
 //           summands of the element type, each multiplied into the same
 //           accumulator.
 //
-// Half of an SM's shared memory at most, so that the second kernel's CTAs stand
-// beside the first's while those finish: their weights do not depend on h, and
+// How many experts are reached is known on the device only, so the K blocks of
+// all jobs, one behind the other, are cut into one equal piece a CTA.  A job that
+// several CTAs share has its sums put into the workspace by each; the last of
+// them to come adds all in order: the same result every time, whoever it is.
+//
+// For few tokens a CTA takes half of an SM's shared memory, so that the second
+// kernel's CTAs stand beside the first's: their weights do not depend on h, and
 // are in their stages when the first kernel ends.
-// Per CTA: warp 0 loads, warp 1 issues the MMAs, warps 2-5 are the epilogue (all
-// eight make the plan).  Every wait is bounded.
+// Per CTA: warps 0, 6 and 7 load, warp 1 issues the MMAs, warps 2-5 are the
+// epilogue (all eight make the plan).  Every wait is bounded.
 #include <algorithm>
 #include <cmath>
 
@@ -34,7 +39,6 @@
 #include "moe_plan.cuh"
 #include "pair.cuh"
 #include "pdl.cuh"
-#include "per_device.h"
 #include "two_parts.cuh"
 
 namespace a2av {
@@ -45,47 +49,42 @@ constexpr int kThreads = 8 * 32;
 constexpr int kMmaWarp = 1;
 constexpr int kEpiWarp0 = 2;
 constexpr int kEpiWarps = 4;
-constexpr int kGroup = 16;                    // rows that the first kernel finishes at a time
-constexpr int kMaxStages = 6;
+constexpr int kLoadWarp1 = kEpiWarp0 + kEpiWarps;  // loads beside warp 0, and the one behind it
+constexpr int kLoadWarps = 3;
+constexpr int kGroup = 8;                     // rows that the first kernel finishes at a time
+constexpr int kMaxStages = 10;
 constexpr int kBK = 64;                       // contraction elements a stage
 constexpr uint32_t kAtom = kBK * 128;         // 64 k-rows x 64 columns of weights
 constexpr uint32_t kWBytes = 2 * kAtom;
-constexpr size_t kSmem = 114688;              // two CTAs an SM
+constexpr size_t kHalfSmem = 114688, kFullSmem = 231424;  // two CTAs an SM, or one
+constexpr int kHalfTokens = 32;               // up to which two are to fit
 static_assert(kThreads >= kMoeExperts, "a thread an expert in the plan");
 
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t tfull[2], tempty[2];
-    uint64_t ready;   // every CTA of the cluster has its part of the sums in shared memory
-    uint64_t free;    // every CTA of the cluster has read this CTA's part
     uint32_t tmem_base;
     int32_t abort;
+    int32_t arrived;  // what this CTA's arrival at a shared job found
     MoePlan plan;
 };
 constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
-// A stage's rows: R of 64 elements, twice where they come as two summands.
+// A stage's rows: R of 64 elements, twice where they come as two summands.  A K
+// block is a stage of each matrix.
 template <bool DOWN, int R>
 struct Shape {
+    static constexpr int kMats = DOWN ? 1 : 2;
     static constexpr int kParts = DOWN ? 2 : 1;
     static constexpr uint32_t kXAtom = R * 128;
     static constexpr uint32_t kStage = kWBytes + kParts * kXAtom;
-    static constexpr uint32_t kTmemCols = 2 * R < 32 ? 32 : 2 * R;
-    // Rows of the part: a group's, or the tokens'.
-    static int stages(int T) {
-        const size_t part = static_cast<size_t>(DOWN ? T : kGroup) * 512;
-        return static_cast<int>(std::min<size_t>(kMaxStages, (kSmem - 1024 - kControlBytes - part) / kStage));
+    static constexpr uint32_t kAccCols = kMats * R;  // of an accumulator, of which there are two
+    static constexpr uint32_t kTmemCols = 2 * kAccCols;
+    static int stages(int T, size_t smem) {
+        const size_t part = DOWN ? static_cast<size_t>(T) * 512 : 0;  // the tokens' sums
+        return static_cast<int>(std::min<size_t>(kMaxStages, (smem - 1024 - kControlBytes - part) / kStage));
     }
 };
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -113,13 +112,25 @@ __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
 }
 
-// Steps (K blocks) of a job, and the part of them that this CTA takes.
-struct Span {
-    int begin, end;
+// A K block among all jobs'.
+struct Cursor {
+    int job, unit, block;
 };
-__device__ __forceinline__ Span span_of(int steps, int rank, int split) {
-    return {static_cast<int>(static_cast<int64_t>(steps) * rank / split),
-            static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / split)};
+
+// All threads of the epilogue.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
+// The same, and whether all of them say yes: a warp whose wait was given up takes the others along.
+__device__ __forceinline__ bool epilogue_all(bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 2, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(static_cast<uint32_t>(yes)), "n"(kEpiWarps * 32)
+        : "memory");
+    return all != 0;
 }
 
 template <bool BF16, bool DOWN, int ACT, int R>
@@ -131,15 +142,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
     uint8_t *base_ptr = smem_raw + (base - raw);
     const int stages = p.stages, T = p.choice.T, topk = p.choice.K;
     Control &C = *reinterpret_cast<Control *>(base_ptr + stages * S::kStage);
-    float *part = reinterpret_cast<float *>(base_ptr + stages * S::kStage + kControlBytes);  // [kGroup or T][128]
+    float *part = reinterpret_cast<float *>(base_ptr + stages * S::kStage + kControlBytes);  // second: [T][128]
     MoePlan &plan = C.plan;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const int split = p.split;  // CTAs of a cluster
-    const int rank = static_cast<int>(pair::cluster_rank());
-    const int cluster = blockIdx.x / split, clusters = gridDim.x / split;
-    const int K = DOWN ? p.N : p.H, cols = DOWN ? p.H : p.N;     // of one product
-    constexpr int kJobCols = DOWN ? 128 : 64;
+    const int K = DOWN ? p.N : p.H, cols = DOWN ? p.H : p.N;  // of one product
+    constexpr int kJobCols = 128;
     const int kblocks = (K + kBK - 1) / kBK, strips = (cols + kJobCols - 1) / kJobCols;
 
     if (warp == kMmaWarp) {
@@ -148,15 +156,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
     } else if (warp == kEpiWarp0) {
         if (lane == 0) {
             for (int s = 0; s < stages; ++s) {
-                mbar_init(smem_u32(&C.full[s]), 1);
+                mbar_init(smem_u32(&C.full[s]), kLoadWarps);
                 mbar_init(smem_u32(&C.empty[s]), 1);
             }
             for (int a = 0; a < 2; ++a) {
                 mbar_init(smem_u32(&C.tfull[a]), 1);
                 mbar_init(smem_u32(&C.tempty[a]), kEpiWarps);
             }
-            mbar_init(smem_u32(&C.ready), kEpiWarps * split);
-            mbar_init(smem_u32(&C.free), kEpiWarps * split);
             C.abort = 0;
             fence_barrier_init();
         }
@@ -172,19 +178,33 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         pdl_trigger();
     }
     moe_plan(p.choice, plan, DOWN ? R : kMoeTokens, !DOWN && blockIdx.x == 0);
-    if (DOWN)
-        for (int i = threadIdx.x; i < T * 32; i += kThreads) reinterpret_cast<float4 *>(part)[i] = make_float4(0, 0, 0, 0);
     tc_fence_before_sync();
-    pair::sync_all();
+    __syncthreads();
     tc_fence_after_sync();
 
     const int units = __shfl_sync(0xffffffffu, plan.units, 0);
-    const int jobs = DOWN ? strips : units * strips;
-    const Span span = span_of(DOWN ? units * kblocks : kblocks, rank, split);  // the same of every job
-    const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
-    const uint32_t ready = smem_u32(&C.ready), freed = smem_u32(&C.free);
-    const auto unit_of = [&](int job, int step) { return DOWN ? step / kblocks : job / strips; };
+    // The K blocks of all jobs, and this CTA's.
+    const int length = DOWN ? units * kblocks : kblocks;  // of a job
+    const int64_t total = static_cast<int64_t>(DOWN ? strips : units * strips) * length;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total)), me = blockIdx.x;
+    const auto begin_of = [&](int cta) { return static_cast<int>(total * cta / ctas); };
+    const auto owner_of = [&](int step) { return static_cast<int>(((step + 1ll) * ctas - 1) / total); };
+    const int begin = me < ctas ? begin_of(me) : 0, end = me < ctas ? begin_of(me + 1) : 0;
+    Cursor first;
+    first.job = begin / length;
+    first.unit = DOWN ? begin % length / kblocks : first.job / strips;
+    first.block = begin % kblocks;
+    const auto advance = [&](Cursor &c) {
+        if (++c.block < kblocks) return;
+        c.block = 0;
+        if (DOWN) {
+            if (++c.unit == units) c.unit = 0, ++c.job;
+        } else {
+            c.unit = ++c.job / strips;
+        }
+    };
     const auto col_of = [&](int job) { return (DOWN ? job : job % strips) * kJobCols; };
+    const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
     // A ring's place: stage and how often it has been gone round.
     struct Place {
         int s = 0, turn = 0;
@@ -193,66 +213,50 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         }
     };
 
-    if (warp == 0) {
-        // =========================================================== producer
-        // (The whole warp goes along and one lane issues, which leaves the operands in
-        // uniform registers: an MMA or a load that a branch on the lane issues costs
-        // two to four times the slots.)
+    if (warp == 0 || warp >= kLoadWarp1) {
+        // =========================================================== producers
+        // Three warps issue a load a stage each (a warp takes about 240 clocks for one):
+        // the two atoms of weights, and the rows.  A whole warp goes along and one lane
+        // issues, which leaves the operands in uniform registers: an MMA that a branch
+        // on the lane issues costs two to four times the slots.
+        const int what = warp == 0 ? 0 : warp - kLoadWarp1 + 1;
         const bool leader = elect();
-        constexpr uint32_t kXBytes = S::kParts * S::kXAtom;
-        const auto weights = [&](const Place &at, int job, int unit, int block) {
-            const uint32_t st = base + at.s * S::kStage, bar = full0 + 8 * at.s;
-            const int expert = plan.unit[unit].expert, col = col_of(job), k = block * kBK;
-            if (leader) {
-                mbar_arrive_expect_tx(bar, kWBytes + kXBytes);
-                tma_load_3d(st, &p.tmA[0], bar, col, k, expert);
-                if (DOWN) tma_load_3d(st + kAtom, &p.tmA[0], bar, col + 64, k, expert);
-                else tma_load_3d(st + kAtom, &p.tmA[1], bar, col, k, expert);
-            }
-        };
-        const auto rows = [&](const Place &at, int unit, int block) {
-            const uint32_t st = base + at.s * S::kStage, bar = full0 + 8 * at.s;
-            const int first = DOWN ? plan.unit[unit].first : 0;
-            if (leader) tma_load_3d(st + kWBytes, &p.tmX, bar, block * kBK, first, 0);
-        };
-        bool ok = true;
+        const uint32_t bytes = what == 2 ? S::kParts * S::kXAtom : kAtom, to = base + what * kAtom;
+        const int shift = what == 1 ? 64 : 0;  // of the columns
         // The second kernel's first stages: their weights before the first kernel's
         // end, the rows behind it.  (The time that a wait may take starts there.)
-        const int first_unit = DOWN ? span.begin / kblocks : 0, first_block = DOWN ? span.begin % kblocks : span.begin;
-        const int ahead = DOWN && cluster < jobs ? min(stages, span.end - span.begin) : 0;
-        if (DOWN) {
-            for (int pass = 0; pass < 2; ++pass) {
-                if (pass == 1) pdl_wait();
-                Place at;
-                int unit = first_unit, block = first_block;
-                for (int i = 0; i < ahead; ++i) {
-                    if (pass == 0) weights(at, cluster, unit, block);
-                    else rows(at, unit, block);
-                    at.next(stages);
-                    if (++block == kblocks) block = 0, ++unit;
-                }
-            }
-        }
+        const int ahead = DOWN && what != 2 ? min(stages, end - begin) : 0;
+        bool ok = true;
         Place at;
-        int filled = 0;
-        for (int job = cluster; job < jobs && ok; job += clusters) {
-            int unit = DOWN ? first_unit : job / strips, block = first_block;
-            for (int step = span.begin; step < span.end; ++step) {
-                if (filled >= ahead) {
-                    if (at.turn > 0 && !pair::wait_phase_warp(&C.abort, empty0 + 8 * at.s, (at.turn & 1) ^ 1, p.status,
-                                                              p.wait_limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    weights(at, job, unit, block);
-                    rows(at, unit, block);
+        Cursor c = first;
+        int col = col_of(c.job) + shift, group = what == 2 ? 0 : plan.unit[c.unit].expert;
+        int row = what == 2 && DOWN ? plan.unit[c.unit].first : 0;
+        for (int step = begin; step < end && ok; ++step) {
+            if (DOWN && step == begin + ahead) pdl_wait();
+#pragma unroll
+            for (int m = 0; m < S::kMats; ++m) {
+                if (at.turn > 0 && !pair::wait_phase_warp(&C.abort, empty0 + 8 * at.s, (at.turn & 1) ^ 1, p.status,
+                                                          p.wait_limit_ns)) {
+                    ok = false;
+                    break;
                 }
-                ++filled;
+                const uint32_t bar = full0 + 8 * at.s, dst = to + at.s * S::kStage;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (what == 2) tma_load_3d(dst, &p.tmX, bar, c.block * kBK, row, 0);
+                    else tma_load_3d(dst, &p.tmA[m], bar, col, c.block * kBK, group);
+                }
+                __syncwarp();
                 at.next(stages);
-                if (++block == kblocks) block = 0, ++unit;
+            }
+            advance(c);
+            if (c.block == 0 && step + 1 < end) {
+                if (what != 2) col = col_of(c.job) + shift, group = plan.unit[c.unit].expert;
+                else if (DOWN) row = plan.unit[c.unit].first;
             }
         }
-        if (DOWN) pdl_trigger();
+        if (DOWN && end - begin <= ahead) pdl_wait();
+        if (DOWN && what == 0) pdl_trigger();
         // The stages that were filled have been read.
         for (int i = 0; i < stages && ok; ++i) {
             const int turns = at.s > i ? at.turn + 1 : at.turn;  // fills of stage i
@@ -273,54 +277,56 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem_base, 0);
         Place at;
         int seg = 0;  // accumulators
+        int block = first.block;
         bool ok = true;
-        for (int job = cluster; job < jobs && ok; job += clusters) {
-            int block = DOWN ? span.begin % kblocks : span.begin;
-            for (int step = span.begin; step < span.end; ++step) {
-                const bool first = step == span.begin || (DOWN && block == 0);
-                const bool last = step == span.end - 1 || (DOWN && block == kblocks - 1);
-                const int acc = seg & 1;
-                if ((first && !pair::wait_phase_warp(&C.abort, smem_u32(&C.tempty[acc]), ((seg >> 1) & 1) ^ 1, p.status,
-                                                     p.wait_limit_ns)) ||
-                    !pair::wait_phase_warp(&C.abort, full0 + 8 * at.s, at.turn & 1, p.status, p.wait_limit_ns)) {
+        for (int step = begin; step < end && ok; ++step) {
+            const bool starts = step == begin || block == 0, ends = step == end - 1 || block == kblocks - 1;
+            const int acc = seg & 1;
+            if (starts && !pair::wait_phase_warp(&C.abort, smem_u32(&C.tempty[acc]), ((seg >> 1) & 1) ^ 1, p.status,
+                                                 p.wait_limit_ns))
+                break;
+            const int ksteps = (min(kBK, K - block * kBK) + 15) / 16;
+#pragma unroll
+            for (int m = 0; m < S::kMats; ++m) {
+                if (!pair::wait_phase_warp(&C.abort, full0 + 8 * at.s, at.turn & 1, p.status, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
                 const uint64_t off = static_cast<uint32_t>(at.s * S::kStage) >> 4;
-                const int ksteps = (min(kBK, K - block * kBK) + 15) / 16;
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk) {
                         if (kk < ksteps) {
 #pragma unroll
                             for (int q = 0; q < S::kParts; ++q)
-                                mma_f16(tmem + acc * R, a_desc0 + off + 128 * kk,
-                                        b_desc0 + off + ((q * S::kXAtom + kk * 32) >> 4), idesc, !first || kk > 0 || q > 0);
+                                mma_f16(tmem + acc * S::kAccCols + m * R, a_desc0 + off + 128 * kk,
+                                        b_desc0 + off + ((q * S::kXAtom + kk * 32) >> 4), idesc, !starts || kk > 0 || q > 0);
                         }
                     }
                     mma_commit(empty0 + 8 * at.s);
-                    if (last) mma_commit(smem_u32(&C.tfull[acc]));
+                    if (ends && m == S::kMats - 1) mma_commit(smem_u32(&C.tfull[acc]));
                 }
                 __syncwarp();
-                if (last) ++seg;
                 at.next(stages);
-                if (++block == kblocks) block = 0;
             }
+            if (ends) ++seg;
+            if (++block == kblocks) block = 0;
         }
     } else if (warp < kEpiWarp0 + kEpiWarps) {
         // =========================================================== epilogue
         if (DOWN) pdl_wait();
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int tid = threadIdx.x - kEpiWarp0 * 32;
-        const int own = kJobCols / split;  // columns this CTA finishes
         const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         float *const column = part + q * 32 + lane;
-        int round = 0, seg = 0;  // exchanges over the cluster, accumulators
-        bool ok = true;
-        const auto wait = [&](uint32_t bar, int parity) {
-            ok = ok && pair::wait_phase_warp(&C.abort, bar, static_cast<uint32_t>(parity), p.status, p.wait_limit_ns);
-            return ok;
+        int seg = 0;  // accumulators
+        const auto filled = [&]() {
+            if (!epilogue_all(pair::wait_phase_warp(&C.abort, smem_u32(&C.tfull[seg & 1]), (seg >> 1) & 1, p.status,
+                                                    p.wait_limit_ns)))
+                return false;
+            tc_fence_after_sync();
+            return true;
         };
         const auto released = [&]() {  // an accumulator has been read
             tc_fence_before_sync();
@@ -328,89 +334,95 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(smem_u32(&C.tempty[seg & 1]));
             ++seg;
         };
-        // Every CTA's part is there.
-        const auto exchanged = [&]() {
-            __syncwarp();
-            if (lane == 0)
-                for (int c = 0; c < split; ++c) pair::arrive_cluster(pair::map_to_rank(ready, c));
-            return wait(ready, round & 1);
+        // The sums of a CTA's share of a job: its first (begun by a CTA before it) or its last one.
+        const size_t slot = static_cast<size_t>(T) * S::kMats * 128;
+        const auto share_of = [&](int cta, int owner) { return p.sums + (2 * static_cast<size_t>(cta) + (cta == owner)) * slot; };
+        // Whether this CTA is the last of a job's to have stored its share; all of the epilogue calls it.
+        const auto last_of = [&](int owner, int count) {
+            __threadfence();
+            epilogue_sync();
+            if (tid == 0) C.arrived = atomicAdd(p.arrivals + owner, 1);
+            epilogue_sync();
+            const bool last = C.arrived == count - 1;
+            if (last) __threadfence();
+            return last;
         };
-        const auto parts_read = [&]() {
-            __syncwarp();
-            if (lane == 0)
-                for (int c = 0; c < split; ++c) pair::arrive_reads_done(pair::map_to_rank(freed, c));
-            ++round;
-        };
-        for (int job = cluster; job < jobs && ok; job += clusters) {
-            const int col0 = col_of(job);
+        Cursor c = first;
+        for (int step = begin; step < end;) {
+            const int job_begin = c.job * length, job_end = job_begin + length;
+            const bool whole = step == job_begin && end >= job_end;
+            const int owner = whole ? me : owner_of(job_begin), count = whole ? 1 : owner_of(job_end - 1) - owner + 1;
+            float *const share = share_of(me, owner) + q * 32 + lane;
+            const int col0 = col_of(c.job);
+            bool ok = true;
             if constexpr (!DOWN) {
-                const MoeUnit w = plan.unit[unit_of(job, 0)];
-                const bool any = span.begin < span.end;
-                if (any) {
-                    if (!wait(smem_u32(&C.tfull[seg & 1]), (seg >> 1) & 1)) break;
-                    tc_fence_after_sync();
-                }
+                // A thread has a column of Wg's and of Wu's product: a row's value is its own.
+                const MoeUnit w = plan.unit[c.unit];
+                const int col = col0 + q * 32 + lane;
+                const auto finish = [&](int r, float gate, float up) {
+                    if (col >= cols) return;
+                    float f, unused;
+                    a2av::split(mul2(act_value<ACT>(pair_of(gate, 0.0f)), pair_of(up, 0.0f)), f, unused);
+                    uint32_t h, l;
+                    two_parts<BF16>(f, h, l);
+                    uint16_t *to = static_cast<uint16_t *>(p.h) + static_cast<size_t>(w.first + r) * p.N + col;
+                    to[0] = static_cast<uint16_t>(h);
+                    to[static_cast<size_t>(T) * topk * p.N] = static_cast<uint16_t>(l);
+                };
+                if (!filled()) break;
                 for (int g = 0; g < w.rows; g += kGroup) {
-                    const int live = min(kGroup, w.rows - g);
-                    uint32_t v[kGroup];
-                    if (any) {
+                    uint32_t v[kGroup][2];
 #pragma unroll
-                        for (int i = 0; i < kGroup; ++i)
-                            if (i < live) tmem_ld1(t_base + (seg & 1) * R + plan.pairs[w.first + g + i] / topk, v[i]);
-                        tmem_ld_wait();
-                    }
-                    // This CTA's part has been read (before it is written again).
-                    if (!wait(freed, (round & 1) ^ 1)) break;
-#pragma unroll
-                    for (int i = 0; i < kGroup; ++i)
-                        if (i < live) column[i * 128] = any ? __uint_as_float(v[i]) : 0.0f;
-                    if (any && g + kGroup >= w.rows) released();
-                    if (!exchanged()) break;
-                    // This CTA's columns of every row: the parts added in order.
-                    for (int i = tid; i < live * own / 4; i += kEpiWarps * 32) {
-                        const int r = i / (own / 4), c = rank * own + i % (own / 4) * 4;
-                        if (col0 + c >= cols) continue;  // (a multiple of 8: all four columns or none)
-                        const uint32_t at = smem_u32(part + r * 128 + c);
-                        f32x2 s[4] = {0, 0, 0, 0};
-                        for (int k = 0; k < split; ++k) {
-                            const uint32_t a = pair::map_to_rank(at, k);
-                            const float4 b = ld_cluster_f32x4(a), d = ld_cluster_f32x4(a + 256);
-                            s[0] = add2(s[0], pair_of(b.x, b.y));
-                            s[1] = add2(s[1], pair_of(b.z, b.w));
-                            s[2] = add2(s[2], pair_of(d.x, d.y));
-                            s[3] = add2(s[3], pair_of(d.z, d.w));
+                    for (int i = 0; i < kGroup; ++i) {
+                        if (g + i < w.rows) {
+                            const uint32_t at = t_base + (seg & 1) * S::kAccCols + plan.pairs[w.first + g + i] / topk;
+                            tmem_ld1(at, v[i][0]);
+                            tmem_ld1(at + R, v[i][1]);
                         }
-                        float f[4];
-                        a2av::split(mul2(act_value<ACT>(s[0]), s[2]), f[0], f[1]);
-                        a2av::split(mul2(act_value<ACT>(s[1]), s[3]), f[2], f[3]);
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) two_parts<BF16>(f[k], h[k], l[k]);
-                        uint16_t *to = static_cast<uint16_t *>(p.h) + static_cast<size_t>(w.first + g + r) * p.N + col0 + c;
-                        *reinterpret_cast<uint2 *>(to) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-                        *reinterpret_cast<uint2 *>(to + static_cast<size_t>(T) * topk * p.N) =
-                            make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
                     }
-                    parts_read();
-                }
-            } else {
-                if (!wait(freed, (round & 1) ^ 1)) break;
-                if (round > 0)
-                    for (int t = 0; t < T; ++t) column[t * 128] = 0.0f;
-                for (int step = span.begin; step < span.end; step = min(span.end, (step / kblocks + 1) * kblocks)) {
-                    const MoeUnit w = plan.unit[unit_of(job, step)];
-                    if (!wait(smem_u32(&C.tfull[seg & 1]), (seg >> 1) & 1)) break;
-                    tc_fence_after_sync();
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < R; c += 16) {
-                        if (c < w.rows) {
+                    for (int i = 0; i < kGroup; ++i) {
+                        if (g + i < w.rows) {
+                            const float gate = __uint_as_float(v[i][0]), up = __uint_as_float(v[i][1]);
+                            if (whole) {
+                                finish(g + i, gate, up);
+                            } else {
+                                share[(g + i) * 256] = gate;
+                                share[(g + i) * 256 + 128] = up;
+                            }
+                        }
+                    }
+                }
+                released();
+                if (!whole && last_of(owner, count)) {
+                    for (int r = 0; r < w.rows; ++r) {
+                        float gate = 0.0f, up = 0.0f;
+                        for (int k = owner; k < owner + count; ++k) {
+                            const float *at = share_of(k, owner) + q * 32 + lane + r * 256;
+                            gate += __ldcg(at);
+                            up += __ldcg(at + 128);
+                        }
+                        finish(r, gate, up);
+                    }
+                }
+                c.unit = ++c.job / strips;
+                step = min(end, job_end);
+            } else {
+                for (int t = 0; t < T; ++t) column[t * 128] = 0.0f;
+                for (const int until = min(end, job_end); step < until;) {
+                    if (!(ok = filled())) break;
+                    const MoeUnit w = plan.unit[c.unit];
+#pragma unroll
+                    for (int g = 0; g < R; g += 16) {
+                        if (g < w.rows) {
                             uint32_t r[16];
-                            tmem_ld16(t_base + (seg & 1) * R + c, r);
+                            tmem_ld16(t_base + (seg & 1) * S::kAccCols + g, r);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                if (c + i < w.rows) {
-                                    const int pair = plan.pairs[w.first + c + i];
+                                if (g + i < w.rows) {
+                                    const int pair = plan.pairs[w.first + g + i];
                                     float *to = column + pair / topk * 128;
                                     *to = fmaf(plan.weight[pair], __uint_as_float(r[i]), *to);
                                 }
@@ -418,19 +430,29 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
                         }
                     }
                     released();
+                    step = min(until, step - c.block + kblocks);
+                    c.block = 0;
+                    if (++c.unit == units) c.unit = 0, ++c.job;
                 }
-                if (!ok || !exchanged()) break;
-                for (int i = tid; i < T * own / 4; i += kEpiWarps * 32) {
-                    const int r = i / (own / 4), c = rank * own + i % (own / 4) * 4;
-                    if (col0 + c >= cols) continue;
-                    const uint32_t at = smem_u32(part + r * 128 + c);
+                if (!ok) break;
+                bool mine = whole;
+                if (whole) {
+                    epilogue_sync();
+                } else {
+                    for (int t = 0; t < T; ++t) share[t * 128] = column[t * 128];
+                    mine = last_of(owner, count);
+                }
+                for (int i = tid; mine && i < T * 32; i += kEpiWarps * 32) {
+                    const int r = i / 32, col = i % 32 * 4;
+                    if (col0 + col >= cols) continue;
                     f32x2 s[2] = {0, 0};
-                    for (int k = 0; k < split; ++k) {
-                        const float4 b = ld_cluster_f32x4(pair::map_to_rank(at, k));
+                    for (int k = owner; k < owner + count; ++k) {
+                        const float4 b = whole ? *reinterpret_cast<const float4 *>(part + r * 128 + col)
+                                               : __ldcg(reinterpret_cast<const float4 *>(share_of(k, owner) + r * 128 + col));
                         s[0] = add2(s[0], pair_of(b.x, b.y));
                         s[1] = add2(s[1], pair_of(b.z, b.w));
                     }
-                    const size_t o = static_cast<size_t>(r) * p.H + col0 + c;
+                    const size_t o = static_cast<size_t>(r) * p.H + col0 + col;
                     if (p.residual) {
                         const uint2 res = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + o);
                         s[0] = add2(s[0], unpack2<BF16>(res.x));
@@ -439,72 +461,29 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) =
                         make_uint2(pack2<BF16>(s[0]), pack2<BF16>(s[1]));
                 }
-                parts_read();
+                epilogue_sync();  // the sums have been read
             }
         }
     }
 
     __syncwarp();
     tc_fence_before_sync();
-    pair::sync_all();  // no CTA leaves while another may read its part
+    __syncthreads();
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc(C.tmem_base, S::kTmemCols);
     }
 }
 
-// What a job costs beside its K blocks, in K blocks.
-constexpr double kJobCost = 6.0;
-
-// Clusters of 1, 2, 4 and 8 CTAs resident at once: twice what the query answers,
-// which takes a kernel with TMEM to have an SM for itself (two CTAs of up to 256
-// columns do share one).
-struct Resident {
-    int clusters[4];
-};
-template <bool DOWN, int R>
-const Resident *resident_clusters() {
-    static PerDevice<Resident> cache;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-    return cache.get(dev, [](Resident &r) {
-        for (int i = 0; i < 4; ++i)
-            r.clusters[i] = 2 * max_clusters(moe_rows_kernel<true, DOWN, A2AV_ACT_SILU, R>, kThreads, kSmem, 1 << i);
-        return r.clusters[0] > 0;
-    });
-}
-
 template <bool BF16, bool DOWN, int ACT, int R>
 cudaError_t launch_rows(MoeRowsLaunch &p, cudaStream_t stream) {
     auto kern = moe_rows_kernel<BF16, DOWN, ACT, R>;
+    const size_t smem = p.choice.T <= kHalfTokens ? kHalfSmem : kFullSmem;
     const cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFullSmem));
     if (err != cudaSuccess) return err;
-    const Resident *of_device = resident_clusters<DOWN, R>();
-    if (!of_device) return cudaErrorUnknown;
-    const MoeChoice &c = p.choice;
-    p.stages = Shape<DOWN, R>::stages(c.T);
-    // The split of the contraction that takes the least time, counted in K blocks a
-    // CTA streams plus what a job costs beside them, for the experts that choices
-    // at random would reach.
-    const double reached = c.E * (1.0 - std::pow(1.0 - static_cast<double>(c.K) / c.E, static_cast<double>(c.T)));
-    const int strips = DOWN ? (p.H + 127) / 128 : (p.N + 63) / 64;
-    const double jobs = DOWN ? strips : std::ceil(reached - 0.5) * strips;
-    const double steps = DOWN ? std::ceil(reached - 0.5) * ((p.N + kBK - 1) / kBK) : (p.H + kBK - 1) / kBK;
-    double best = 0.0;
-    for (int i = 0; i < 4; ++i) {
-        const int resident = of_device->clusters[i];
-        if (resident <= 0) continue;
-        const double cost = std::ceil(jobs / resident) * (std::ceil(steps / (1 << i)) + kJobCost);
-        if (p.split == 0 || cost < best) {
-            best = cost;
-            p.split = 1 << i;
-            p.grid = resident << i;
-        }
-    }
-    const int64_t most_jobs = DOWN ? strips : static_cast<int64_t>(c.T) * c.K * strips;
-    p.grid = static_cast<int>(std::min<int64_t>(p.grid, most_jobs * p.split));
-    return launch_pdl(kern, dim3(p.grid), dim3(kThreads), kSmem, p.split, stream, p);
+    p.stages = Shape<DOWN, R>::stages(p.choice.T, smem);
+    return launch_pdl(kern, dim3(kMoeCtas), dim3(kThreads), smem, 0, stream, p);
 }
 
 // Rows multiplied: all tokens, or a unit's: what the fullest expert is expected
@@ -526,7 +505,6 @@ int moe_unit_rows(int T, int E, int K, bool down) {
 }
 
 cudaError_t launch_moe_gated(MoeRowsLaunch p, bool bf16, int act, cudaStream_t stream) {
-    p.split = 0;
     if (bf16)
         return act == A2AV_ACT_SILU ? launch_unit<true, false, A2AV_ACT_SILU>(p, stream)
                                     : launch_unit<true, false, A2AV_ACT_GELU_TANH>(p, stream);
@@ -535,7 +513,6 @@ cudaError_t launch_moe_gated(MoeRowsLaunch p, bool bf16, int act, cudaStream_t s
 }
 
 cudaError_t launch_moe_down(MoeRowsLaunch p, bool bf16, cudaStream_t stream) {
-    p.split = 0;
     return bf16 ? launch_unit<true, true, A2AV_ACT_SILU>(p, stream) : launch_unit<false, true, A2AV_ACT_SILU>(p, stream);
 }
 
