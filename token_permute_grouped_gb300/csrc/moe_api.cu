@@ -46,13 +46,15 @@ a2av_status validate(const a2av_moe_desc *d) {
 }
 
 size_t logit_bytes(const a2av_moe_desc &d) { return round256(static_cast<size_t>(d.T) * d.E * 4); }
+size_t chosen_bytes(const a2av_moe_desc &d) { return round256(static_cast<size_t>(d.T) * d.K * sizeof(int2)); }
 constexpr size_t kArrivalBytes = 2 * a2av::kMoeCtas * 4;
 // Shares of jobs; the second product's, half as large, take the place of the first's.
 size_t sum_bytes(const a2av_moe_desc &d) { return static_cast<size_t>(a2av::kMoeCtas) * 2 * d.T * 1024; }
 size_t value_bytes(const a2av_moe_desc &d) { return round256(static_cast<size_t>(d.T) * d.K * d.N * 4); }
 
 size_t workspace_bytes_of(const a2av_moe_desc &d) {
-    return kStatusBytes + round256(kArrivalBytes) + logit_bytes(d) + value_bytes(d) + sum_bytes(d);
+    return kStatusBytes + round256(kArrivalBytes) + logit_bytes(d) + chosen_bytes(d) + value_bytes(d) +
+           sum_bytes(d);
 }
 
 }  // namespace
@@ -83,13 +85,15 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     const bool bf16 = d.dtype == A2AV_BF16;
     uint8_t *const arrivals = static_cast<uint8_t *>(workspace) + kStatusBytes;
-    uint8_t *const logits = arrivals + round256(kArrivalBytes), *const values = logits + logit_bytes(d);
+    uint8_t *const logits = arrivals + round256(kArrivalBytes), *const chosen = logits + logit_bytes(d);
+    uint8_t *const values = chosen + chosen_bytes(d);
 
     a2av::MoeRouterLaunch r{d.T, d.E, static_cast<int32_t>(d.H), x, router, reinterpret_cast<float *>(logits),
                             static_cast<int32_t *>(workspace), reinterpret_cast<int32_t *>(arrivals)};
     a2av::MoeRowsLaunch g;
     std::memset(&g, 0, sizeof g);
-    g.choice = a2av::MoeChoice{d.T, d.E, d.K, d.score, d.renormalise != 0, d.scale, r.logits, bias, experts, weights};
+    g.choice = a2av::MoeChoice{d.T, d.E, d.K, d.score, d.renormalise != 0, d.scale, r.logits, bias, experts, weights,
+                                d.T > a2av::kMoeFewTokens ? reinterpret_cast<int2 *>(chosen) : nullptr};
     g.H = static_cast<int32_t>(d.H);
     g.N = static_cast<int32_t>(d.N);
     g.residual = residual;
@@ -109,6 +113,7 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
         return A2AV_ERR_CUDA;
     if (a2av::launch_moe_router(r, bf16, d.router_dtype == A2AV_FP32, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     if (d.T == 0) return A2AV_OK;  // (the status is stored)
+    if (g.choice.chosen && a2av::launch_moe_choose(g.choice, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     if (a2av::launch_moe_gated(g, bf16, d.act, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     return a2av::launch_moe_down(o, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }

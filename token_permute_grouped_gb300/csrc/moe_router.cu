@@ -8,6 +8,7 @@
 // latency for few tokens, by the reads of the rows from L2 for many.
 #include "activation.cuh"
 #include "moe.h"
+#include "moe_plan.cuh"
 #include "pdl.cuh"
 #include "rows.cuh"
 
@@ -132,7 +133,31 @@ cudaError_t launch_type(const MoeRouterLaunch &p, cudaStream_t stream) {
                : launch_pdl(moe_router_kernel<BF16, R32, 4, 4>, grid, kRouterThreads, 0, 0, stream, p, split);
 }
 
+// The choice, a warp a token: for more tokens than a CTA has warps (64 tokens over
+// 256 experts, one after the other in every CTA, would take 18 us).
+__global__ void __launch_bounds__(32) moe_choose_kernel(const MoeChoice c) {
+    __shared__ float logits[kMoeExperts];
+    const int t = blockIdx.x, lane = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    for (int e = lane; e < c.E; e += 32) logits[e] = __ldcg(c.logits + t * c.E + e);
+    __syncwarp();
+    int expert;
+    float weight;
+    moe_choose(c, logits, lane, expert, weight);
+    if (lane < c.K) {
+        const int pair = t * c.K + lane;
+        c.chosen[pair] = make_int2(expert, __float_as_int(weight));
+        if (c.experts) c.experts[pair] = expert;
+        if (c.weights) c.weights[pair] = weight;
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_moe_choose(const MoeChoice &c, cudaStream_t stream) {
+    return launch_pdl(moe_choose_kernel, dim3(c.T), 32, 0, 0, stream, c);
+}
 
 cudaError_t launch_moe_router(const MoeRouterLaunch &p, bool bf16, bool router32, cudaStream_t stream) {
     if (router32) return bf16 ? launch_type<true, true>(p, stream) : launch_type<false, true>(p, stream);

@@ -171,13 +171,20 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         prefetch_tensormap(&p.tmX);
         if (!DOWN) prefetch_tensormap(&p.tmA[1]);
     }
-    // The logits are there: the first kernel waits for the router's, and lets the
-    // second one start only behind that.
-    if (!DOWN) {
-        pdl_wait();
-        pdl_trigger();
+    // The logits (or the choice) are there: the first kernel waits for them, and lets
+    // the second one start only behind that.  While it waits it makes a plan of
+    // nothing, which brings the instructions in: its first loads wait for the plan.
+    float *const logits = reinterpret_cast<float *>(base_ptr);  // (no stage is filled yet)
+    for (int pass = DOWN ? 1 : 0; pass < 2; ++pass) {
+        if (pass == 1 && !DOWN) {
+            pdl_wait();
+            pdl_trigger();
+        }
+        if (!p.choice.chosen)
+            for (int i = threadIdx.x; i < T * p.choice.E; i += kThreads) logits[i] = pass == 1 ? __ldcg(p.choice.logits + i) : 0.0f;
+        if (pass == 1 || !p.choice.chosen) moe_plan(p.choice, plan, logits, DOWN ? R : kMoeTokens, pass == 1 && !DOWN && blockIdx.x == 0);
     }
-    moe_plan(p.choice, plan, DOWN ? R : kMoeTokens, !DOWN && blockIdx.x == 0);
+    fence_proxy_async_smem();  // (TMA writes over the logits)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
