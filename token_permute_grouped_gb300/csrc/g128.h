@@ -25,7 +25,6 @@ struct G128Launch {
     CUtensorMap tmA;        // expert-major codes [A, K], box 128 x 128 rows
     CUtensorMap tmDirect;   // ataOut codes, likewise
     CUtensorMap tmB;        // weight codes [e, N, K], box 128 x bn / 2 columns
-    CUtensorMap tmY;        // y, box 32 x 32, 64-byte swizzle
 };
 cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream);
 int g128_gemm_max_clusters();

@@ -47,18 +47,6 @@ bool codes_map(CUtensorMap *m, const void *ptr, int64_t groups, int64_t rows, in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 16-bit outputs [rows][cols], boxes of 32 x 32, 64-byte swizzled.
-bool out_map(CUtensorMap *m, void *ptr, int64_t rows, int64_t cols, bool bf16) {
-    auto fn = a2av::tensor_map_encode();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * 2)};
-    const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 a2av_status validate(const a2av_gmm_g128_desc *d) {
     if (!d) return A2AV_ERR_NULLPTR;
     if (d->W < 1 || d->e < 1 || d->e > a2av::kMaxExperts) return A2AV_ERR_INVALID;
@@ -144,8 +132,7 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
         if (g.direct_halves && !codes_map(&g.tmDirect, ataOut_q, 1, d.A, d.H1, 128)) return A2AV_ERR_CUDA;
     }
     if (d.A > 0 && (!codes_map(&g.tmA, rows, 1, d.A, d.H1, 128) ||
-                    !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, static_cast<uint32_t>(g.bn / 2)) ||
-                    !out_map(&g.tmY, gmmY, d.A, d.N1, bf16)))
+                    !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, static_cast<uint32_t>(g.bn / 2))))
         return A2AV_ERR_CUDA;
     const int64_t tiles = (row_tiles + d.e) * ceil_div(d.N1, g.bn);
     g.grid = static_cast<int32_t>(2 * std::max<int64_t>(1, std::min<int64_t>(dev->clusters, tiles)));

@@ -7,13 +7,16 @@
 // block of 128 codes along K is a product of its own (four MMAs of K = 32 that
 // start a TMEM accumulator afresh), which the epilogue warps multiply by its
 // scales and add to sums in their registers while the next block is multiplied
-// into another accumulator.  A lane's row has one scale and a warp's 128
-// columns one, so a block costs a lane one product and 64 packed FMAs.
+// into another accumulator.  A lane's row has one scale and a warp's 128 columns
+// one, so a block costs a lane one product and 64 packed FMAs.
 //
-// Per CTA: warp 0 loads (a stage is one K block: 16 KB of rows, 8 or 16 KB of
-// weights, 128-byte swizzle), warp 1 issues the MMAs (even CTA), warps 2-9 sum
-// and store, two for each TMEM lane quarter, half of the columns each.
-// Every wait is bounded, as in the other GEMMs.
+// Per CTA: warps 0 and 2 load (a stage is one K block: 16 KB of rows, 8 or 16 KB
+// of weights, 128-byte swizzle), warp 1 issues the MMAs (even CTA), warps 4-11 sum
+// and store, two for each TMEM lane quarter, half of the columns each.  They take
+// the registers that the first four warps leave.
+// A warp that loads or issues goes along as a whole and one lane issues, which
+// leaves the operands in uniform registers: a branch on the lane costs two to four
+// times the slots.  Every wait is bounded, as in the other GEMMs.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -30,11 +33,14 @@ constexpr int BM = 128;             // rows of a CTA
 constexpr int TILE_M = 2 * BM;
 constexpr int BK = 128;             // codes of a K block, which has one scale
 constexpr int kMmaWarp = 1;
-constexpr int kEpiWarp0 = 2;
+constexpr int kLoadWarpB = 2;
+constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+// Registers of a thread: 384 x 168 at the launch, as many after the split.
+constexpr int kRegsAtLaunch = 168, kRegsFew = 56, kRegsMany = 224;
+static_assert(kEpiWarp0 * kRegsFew + kEpiWarps * kRegsMany <= (kEpiWarp0 + kEpiWarps) * kRegsAtLaunch, "registers of a CTA");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kEpiStageBytes = 32 * 64;  // of a warp: 32 x 32 results
 
 template <int BN>
 struct Shape {
@@ -44,6 +50,8 @@ struct Shape {
     static constexpr int kAccs = kTmemCols / BN;  // accumulators
     static constexpr int kCols = BN / 2;          // columns of an epilogue warp
 };
+
+constexpr uint32_t kTurnBytes = 32 * 64;  // of an epilogue warp: 32 x 32 results
 
 struct Group {
     int32_t row0, rows, tile_start;
@@ -61,7 +69,7 @@ constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
 template <int BN>
 constexpr size_t smem_bytes() {
-    return 1024 + Shape<BN>::kStages * Shape<BN>::kStageBytes + kEpiWarps * kEpiStageBytes + kControlBytes;
+    return 1024 + Shape<BN>::kStages * Shape<BN>::kStageBytes + kEpiWarps * kTurnBytes + kControlBytes;
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory per CTA");
 
@@ -91,7 +99,21 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// 32 lanes x 16 consecutive columns.
+// This warp's loads have arrived; r is used only behind this.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+    asm volatile(""  // (behind the wait as well: an asm takes 30 operands)
+                 : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -101,7 +123,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
-// This warp's loads have arrived; r is used only behind this.
 __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -109,9 +130,8 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-
-// The epilogue's bounded wait, in line (a call would put its sums aside), with
-// one answer for the warp.
+// A warp's bounded wait, in line (a call would put an epilogue's sums aside, and
+// does not fit the split of registers), with one answer for the warp.
 __device__ __forceinline__ bool wait_in_line(int32_t *abort_flag, uint32_t bar, uint32_t parity, int32_t *status,
                                              uint64_t limit_ns) {
     bool ok = pair::try_wait_cluster(bar, parity);
@@ -137,10 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
-    const uint32_t epi0 = base + S::kStages * S::kStageBytes;
-    Control &C = *reinterpret_cast<Control *>(base_ptr + S::kStages * S::kStageBytes + kEpiWarps * kEpiStageBytes);
+    const uint32_t turn0 = base + S::kStages * S::kStageBytes;
+    Control &C = *reinterpret_cast<Control *>(base_ptr + S::kStages * S::kStageBytes + kEpiWarps * kTurnBytes);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = pair::cluster_rank();
     const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
     const int tn = (p.N + BN - 1) / BN, kblocks = p.K / BK;
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
     } else if (warp == kEpiWarp0) {
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
-                mbar_init(smem_u32(&C.full[s]), 1);
+                mbar_init(smem_u32(&C.full[s]), 2);
                 mbar_init(smem_u32(&C.empty[s]), 1);
             }
             for (int a = 0; a < S::kAccs; ++a) {
@@ -188,92 +208,116 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
     } else if (warp == kEpiWarp0 + 1 && lane == 0) {
         prefetch_tensormap(&p.tmA);
         prefetch_tensormap(&p.tmB);
-        prefetch_tensormap(&p.tmY);
         if (p.direct_halves) prefetch_tensormap(&p.tmDirect);
     }
     tc_fence_before_sync();
     pair::sync_all();
     tc_fence_after_sync();
 
-    const int total = C.total_tiles;
+    const int total = __shfl_sync(0xffffffffu, C.total_tiles, 0);
     const uint32_t full0 = smem_u32(&C.full[0]), empty0 = smem_u32(&C.empty[0]);
     const uint32_t tfull0 = smem_u32(&C.tfull[0]), tempty0 = smem_u32(&C.tempty[0]);
+    // A ring's place: stage (or accumulator) and how often it has been gone round.
+    struct Place {
+        int s = 0, turn = 0;
+        __device__ __forceinline__ void next(int n) {
+            if (++s == n) s = 0, ++turn;
+        }
+    };
 
-    if (warp == 0) {
-        // =========================================================== producer
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true, all_there = !p.after_permute;
-            for (int t = unit; t < total && ok; t += nunits) {
-                const Tile w = tile_at(C, t, tn);
+    const auto give_up_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew)); };
+    if (warp == 0 || warp == kLoadWarpB) {
+        // =========================================================== producers: rows, weights
+        give_up_registers();
+        const bool rows = warp == 0, leader = elect_one();
+        const uint32_t bytes = rows ? S::kA : S::kB, to = base + (rows ? 0 : S::kA);
+        Place at;
+        bool ok = true, all_there = !p.after_permute || !rows;
+        for (int t = unit; t < total && ok; t += nunits) {
+            const Tile w = tile_at(C, t, tn);
+            const CUtensorMap *map = &p.tmB;
+            int y = w.n * BN + static_cast<int>(rank) * (BN / 2), z = w.g;
+            if (rows) {
                 const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
                 // This CTA's first row; without a row of its own, any one (nothing of it is stored).
                 const int from = w.m * TILE_M + static_cast<int>(rank) * BM;
                 const bool live = from < C.g[w.g].rows;
-                int row = C.g[w.g].row0 + (live ? from : 0);
-                const CUtensorMap *ta = &p.tmA;
-                if (p.direct_halves && live && half_in_one_segment(C.seg, p.W, p.e, row, g_end)) {
-                    ta = &p.tmDirect;
-                    row = source_row(C.seg, p.W, p.e, row);
+                y = C.g[w.g].row0 + (live ? from : 0);
+                z = 0;
+                map = &p.tmA;
+                if (p.direct_halves && live && half_in_one_segment(C.seg, p.W, p.e, y, g_end)) {
+                    map = &p.tmDirect;
+                    y = source_row(C.seg, p.W, p.e, y);
                 } else if (!all_there) {
                     pdl_wait();
                     all_there = true;
                 }
-                const int col = w.n * BN + static_cast<int>(rank) * (BN / 2);
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const int s = it % S::kStages;
-                    if (!pair::wait_phase(&C.abort, empty0 + 8 * s, ((it / S::kStages) & 1) ^ 1, p.status,
-                                          p.wait_limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t own = full0 + 8 * s, bar = pair::map_to_rank(own, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * S::kStageBytes);
-                    const uint32_t st = base + s * S::kStageBytes;
-                    pair::load_3d(st, ta, bar, kb * BK, row, 0);
-                    pair::load_3d(st + S::kA, &p.tmB, bar, kb * BK, col, w.g);
-                }
             }
+            for (int kb = 0; kb < kblocks; ++kb, at.next(S::kStages)) {
+                if (at.turn > 0 && !wait_in_line(&C.abort, empty0 + 8 * at.s, (at.turn & 1) ^ 1, p.status,
+                                                          p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t own = full0 + 8 * at.s, bar = pair::map_to_rank(own, 0);
+                if (leader) {
+                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * bytes);
+                    pair::load_3d(to + at.s * S::kStageBytes, map, bar, kb * BK, y, z);
+                }
+                __syncwarp();
+            }
+        }
+        if (rows) {
             pdl_trigger();
             if (!all_there) pdl_wait();  // (a kernel's end implies that of all before it)
-            for (int i = 0; i < S::kStages && ok; ++i, ++it)
-                ok = pair::wait_phase(&C.abort, empty0 + 8 * (it % S::kStages), ((it / S::kStages) & 1) ^ 1, p.status,
-                                      p.wait_limit_ns);
-            if (!ok) pair::let_settle();
         }
+        // The stages that were filled have been read.
+        for (int i = 0; i < S::kStages && ok; ++i) {
+            const int turns = at.s > i ? at.turn + 1 : at.turn;  // fills of stage i
+            if (turns > 0)
+                ok = wait_in_line(&C.abort, empty0 + 8 * i, (turns - 1) & 1, p.status, p.wait_limit_ns);
+        }
+        if (!ok) pair::let_settle();
     } else if (warp == kMmaWarp) {
         // =========================================================== MMA issuer
-        if (lane == 0 && rank == 0) {
+        give_up_registers();
+        if (rank == 0) {
+            const bool leader = elect_one();
             const uint32_t idesc = instr_desc_f8(static_cast<uint32_t>(p.qtype), TILE_M, BN);
             const uint64_t a_desc0 = smem_desc(base, 16, 1024, kSwizzle128B);
             const uint64_t b_desc0 = smem_desc(base + S::kA, 16, 1024, kSwizzle128B);
-            uint32_t it = 0;
+            const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem_base, 0);
+            Place at, acc;
             bool ok = true;
             for (int t = unit; t < total && ok; t += nunits) {
-                for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    const int s = it % S::kStages, acc = it % S::kAccs;
-                    if (!pair::wait_phase(&C.abort, tempty0 + 8 * acc, ((it / S::kAccs) & 1) ^ 1, p.status,
-                                          p.wait_limit_ns) ||
-                        !pair::wait_phase(&C.abort, full0 + 8 * s, (it / S::kStages) & 1, p.status, p.wait_limit_ns)) {
+                for (int kb = 0; kb < kblocks; ++kb, at.next(S::kStages), acc.next(S::kAccs)) {
+                    if (!wait_in_line(&C.abort, full0 + 8 * at.s, at.turn & 1, p.status, p.wait_limit_ns) ||
+                        !wait_in_line(&C.abort, tempty0 + 8 * acc.s, (acc.turn & 1) ^ 1, p.status, p.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint64_t off = (s * S::kStageBytes) >> 4;
+                    const uint64_t off = static_cast<uint32_t>(at.s * S::kStageBytes) >> 4;
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)
-                        mma_f8_pair(C.tmem_base + acc * BN, a_desc0 + off + 2 * kk, b_desc0 + off + 2 * kk, idesc, kk > 0);
-                    pair::commit(empty0 + 8 * s);
-                    pair::commit(tfull0 + 8 * acc);
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            mma_f8_pair(tmem + acc.s * BN, a_desc0 + off + 2 * kk, b_desc0 + off + 2 * kk, idesc, kk > 0);
+                        pair::commit(empty0 + 8 * at.s);
+                        pair::commit(tfull0 + 8 * acc.s);
+                    }
+                    __syncwarp();
                 }
             }
         }
+    } else if (warp < kEpiWarp0) {
+        give_up_registers();
     } else {
         // =========================================================== sums and stores
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
         const int q = warp & 3;
-        const int half = (warp - kEpiWarp0) / 4;
-        const uint32_t stage = epi0 + static_cast<uint32_t>(warp - kEpiWarp0) * kEpiStageBytes;
-        const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * S::kCols;
+        const int part = (warp - kEpiWarp0) / 4;  // of the columns
+        const uint32_t turn = turn0 + static_cast<uint32_t>(warp - kEpiWarp0) * kTurnBytes;
+        const uint32_t t_base = C.tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * S::kCols;
         const int scale_rows = (p.N + 127) / 128;  // of an expert's weights
         const float *xs = p.xs, *ws = p.ws;        // of this lane's row, of this warp's columns
         float xn[2] = {0, 0}, wn[2] = {0, 0};      // of the next K blocks
@@ -285,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
             valid = r < C.g[w.g].rows;
             const int src = valid ? source_row(C.seg, p.W, p.e, C.g[w.g].row0 + r) : 0;
             xs = p.xs + static_cast<size_t>(src) * kblocks;
-            const int block = min((w.n * BN + half * S::kCols) / 128, scale_rows - 1);
+            const int block = min((w.n * BN + part * S::kCols) / 128, scale_rows - 1);
             ws = p.ws + (static_cast<size_t>(w.g) * scale_rows + block) * kblocks;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -295,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
                 }
             }
         };
-        uint32_t it = 0;
+        Place acc;
         bool ok = true;
         if (unit < total) prepare(unit);
         for (int t = unit; t < total && ok; t += nunits) {
@@ -303,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < S::kCols / 2; ++j) sum[j] = 0;
             const bool row_valid = valid;
-            for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                const int acc = it % S::kAccs;
+            for (int kb = 0; kb < kblocks; ++kb, acc.next(S::kAccs)) {
                 const f32x2 scale = both(xn[0] * wn[0]);
                 xn[0] = xn[1];
                 wn[0] = wn[1];
@@ -312,75 +355,57 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
                     xn[1] = xs[kb + 2];
                     wn[1] = ws[kb + 2];
                 }
-                if (!wait_in_line(&C.abort, tfull0 + 8 * acc, (it / S::kAccs) & 1, p.status, p.wait_limit_ns)) {
+                const uint32_t from = t_base + acc.s * BN, empty = pair::map_to_rank(tempty0 + 8 * acc.s, 0);
+                if (!wait_in_line(&C.abort, tfull0 + 8 * acc.s, acc.turn & 1, p.status, p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
                 uint32_t r[2][16];
-                tmem_ld16(t_base + acc * BN, r[0]);
+                tmem_ld16(from, r[0]);
 #pragma unroll
                 for (int c = 0; c < S::kCols / 16; ++c) {
                     tmem_ld16_wait(r[c & 1]);
                     if (c + 1 < S::kCols / 16) {
-                        tmem_ld16(t_base + acc * BN + 16 * (c + 1), r[(c + 1) & 1]);
+                        tmem_ld16(from + 16 * (c + 1), r[(c + 1) & 1]);
                     } else {  // all of it is in registers
                         tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) pair::arrive_reads_done(pair::map_to_rank(tempty0 + 8 * acc, 0));
+                        if (lane == 0) pair::arrive_reads_done(empty);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t *v = &r[c & 1][2 * j];
-                        sum[8 * c + j] =
-                            fma2(pair_of(__uint_as_float(v[0]), __uint_as_float(v[1])), scale, sum[8 * c + j]);
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        sum[8 * c + j] = fma2(pair_of(__uint_as_float(r[c & 1][2 * j]), __uint_as_float(r[c & 1][2 * j + 1])),
+                                              scale, sum[8 * c + j]);
                 }
             }
             if (!ok) break;
             const Tile w = tile_at(C, t, tn);
             const int row0 = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;
-            const int col0 = w.n * BN + half * S::kCols;
+            const int rows = __popc(__ballot_sync(0xffffffffu, row_valid));  // (the first of the 32)
+            const int col0 = w.n * BN + part * S::kCols;
             if (t + nunits < total) prepare(t + nunits);
             // Each 32 x 32 block is turned around in this warp's 2 KB (64-byte rows, the
-            // 16-byte chunk index XORed with (row / 2) % 4) and stored by TMA, or row by
-            // row where the group ends inside it.
-            const uint32_t mask = __ballot_sync(0xffffffffu, row_valid);
-            if (mask == 0) continue;
+            // 16-byte chunk index XORed with (row / 2) % 4), so that a store takes 64 bytes
+            // of eight rows, not 16 of 32: the next blocks' MMAs wait for these.
 #pragma unroll
             for (int i = 0; i < S::kCols / 32; ++i) {
-                const int col = col0 + 32 * i;
-                if (col >= p.N) break;
-                if (lane == 0) bulk_wait_read_0();  // the block before this one has left
-                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const f32x2(&v)[4] = *reinterpret_cast<const f32x2(*)[4]>(&sum[16 * i + 4 * j]);
-                    st_shared_v4(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8<BF16>(v));
+                    st_shared_v4(turn + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack8<BF16>(v));
                 }
-                if (mask == 0xffffffffu) {
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&p.tmY, stage, col, row0);
-                        bulk_commit_group();
-                    }
-                } else {
-                    __syncwarp();
-                    const int j = lane & 3;
+                __syncwarp();
+                const int j = lane & 3, col = col0 + 32 * i + 8 * j;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int rr = 8 * k + (lane >> 2);
-                        const uint4 v = ld_shared_v4(stage + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
-                        if (((mask >> rr) & 1u) && col + 8 * j < p.N)
-                            st_stream_v4(static_cast<uint16_t *>(p.y) + static_cast<size_t>(row0 + rr) * p.N + col + 8 * j,
-                                         v);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    const uint4 v = ld_shared_v4(turn + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+                    if (r < rows && col < p.N)
+                        st_stream_v4(static_cast<uint16_t *>(p.y) + static_cast<size_t>(row0 + r) * p.N + col, v);
                 }
                 __syncwarp();
             }
         }
-        if (lane == 0) bulk_wait_all();  // this warp's stores have landed
     }
 
     __syncwarp();

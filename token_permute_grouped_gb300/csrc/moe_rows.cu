@@ -96,17 +96,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-// One lane of the (whole) warp.
-__device__ __forceinline__ bool elect() {
-    uint32_t is;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(is));
-    return is != 0;
-}
-
 // One column.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
@@ -227,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         // issues, which leaves the operands in uniform registers: an MMA that a branch
         // on the lane issues costs two to four times the slots.
         const int what = warp == 0 ? 0 : warp - kLoadWarp1 + 1;
-        const bool leader = elect();
+        const bool leader = elect_one();
         const uint32_t bytes = what == 2 ? S::kParts * S::kXAtom : kAtom, to = base + what * kAtom;
         const int shift = what == 1 ? 64 : 0;  // of the columns
         // The second kernel's first stages: their weights before the first kernel's
@@ -274,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
     } else if (warp == kMmaWarp) {
         // =========================================================== MMA issuer
         if (DOWN) pdl_wait();
-        const bool leader = elect();
+        const bool leader = elect_one();
         // A: the weights, MN-major (atoms of 64 columns kAtom apart, 8-row K groups 1024 B apart, a K step of 16
         // rows 2 KB).  B: the rows, K-major (8-row groups 1024 B apart, a K step of 16 elements 32 B).
         constexpr uint32_t idesc = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | (1u << 15) |
