@@ -83,6 +83,36 @@ def test_few_rows_of_one_expert(rows, W):
     run(W, 3, split(8, W, 3, [0, rows, 1]), 768, 392, "bf16", "e4m3fn")
 
 
+@pytest.mark.parametrize("W,e,sizes,K,N", [
+    (1, 1, [1], 4096, 3080), (1, 1, [16], 2048, 6152), (3, 4, [0, 12, 0, 0], 2048, 1672), (5, 8, [0, 0, 30, 0, 0, 0, 0, 0], 1152, 1640),
+    (2, 8, [1, 0, 3, 5, 0, 2, 16, 1], 1280, 1288), (4, 2, [7, 6], 7168, 1024), (8, 32, [1] * 32, 1024, 520), (1, 2, [0, 1], 128, 60000)])
+@pytest.mark.parametrize("dt,qtype", [("bf16", "e4m3fn"), ("fp16", "e5m2")])
+def test_few_rows_of_large_weights(W, e, sizes, K, N, dt, qtype):
+    """Weights that take longest: streamed, the K blocks of all columns cut evenly over the SMs; rows as they spread at
+    random, all at one expert, at experts between empty ones."""
+    run(W, e, split(17, W, e, sizes), K, N, dt, qtype)
+
+
+def test_few_rows_of_large_weights_inconsistent_counts():
+    W, e, A, K, N = 2, 4, 8, 4096, 1024
+    plan = binding.G128Plan(W, e, A, K, N)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = lambda *s: torch.randint(0, 100, s, dtype=torch.uint8, device="cuda", generator=g)
+    args = (codes(A, K), torch.ones(A, K // 128, device="cuda"))
+    w = (codes(e, N, K), torch.ones(e, N // 128, K // 128, device="cuda"))
+    counts = lambda *c: torch.tensor(c, dtype=torch.int32, device="cuda")
+    good = counts(1, 1, 1, 1, 1, 1, 1, 1)
+    want = plan.run(*args, good, *w)
+    for bad in (counts(1, 1, 1, 1, 1, 1, 1, 2), counts(9, -1, 0, 0, 0, 0, 0, 0)):
+        y = torch.full((A, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        plan.run(*args, bad, *w, gmmY=y)
+        assert binding.STATUS_NAMES[binding.a2av_gmm_read_device_status(plan.workspace)[0]] == "A2AV_ERR_DEVICE_CHECK"
+        assert bool((y == 5.0).all())
+    plan.workspace.fill_(255)  # (nothing in it is kept from call to call)
+    assert torch.equal(plan.run(*args, good, *w), want)
+    assert binding.a2av_gmm_read_device_status(plan.workspace) == (0, 0)
+
+
 def test_all_rows_at_one_of_many_experts():
     run(4, 16, split(9, 4, 16, [0] * 5 + [290] + [0] * 10), 512, 256, "bf16", "e4m3fn")
 

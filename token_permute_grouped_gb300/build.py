@@ -20,7 +20,7 @@ CHECKS_LIB = os.path.join(PKG, "liba2av_gmm_checks.so")
 CHECKS_SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu", "ffn_api.cu"]
 SOURCES = ["api.cu", "permute.cu", "grouped_gemm.cu", "grouped_gemm_mx.cu", "amp.cu", "quant_reduce.cu", "ffn_api.cu",
            "rms_norm.cu", "glu.cu", "expert_gemm.cu", "gated_rows.cu", "glu_grad.cu", "stage_rows.cu",
-           "layer_norm.cu", "g128_gemm.cu", "g128_api.cu", "moe_router.cu", "moe_rows.cu", "moe_api.cu"]
+           "layer_norm.cu", "g128_gemm.cu", "g128_rows.cu", "g128_api.cu", "moe_router.cu", "moe_rows.cu", "moe_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

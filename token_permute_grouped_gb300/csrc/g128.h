@@ -9,6 +9,11 @@
 
 namespace a2av {
 
+// CTAs of the few-row kernel: one an SM of a GB300.  Not asked of the device: the
+// workspace's size depends on it, and is asked for without one.
+constexpr int kG128Ctas = 152;
+constexpr int kG128UnitRows = 16;  // rows that it takes at a time
+
 struct G128Launch {
     const int32_t *recvCounts;
     int32_t W, e, A, K, N;
@@ -22,11 +27,18 @@ struct G128Launch {
     int32_t bn;             // columns of a tile: 256 or 128
     int32_t grid;           // CTAs, two a cluster
     uint64_t wait_limit_ns;
-    CUtensorMap tmA;        // expert-major codes [A, K], box 128 x 128 rows
+    // The few-row kernel's:
+    float *sums;            // [kG128Ctas][2][kG128UnitRows][128]: shares of jobs that several CTAs have
+    int32_t *arrivals;      // [kG128Ctas], 0: of those CTAs, by the first
+    CUtensorMap tmA;        // expert-major codes [A, K], box 128 x 128 (few-row kernel: 16) rows
     CUtensorMap tmDirect;   // ataOut codes, likewise
-    CUtensorMap tmB;        // weight codes [e, N, K], box 128 x bn / 2 columns
+    CUtensorMap tmB;        // weight codes [e, N, K], box 128 x bn / 2 (few-row kernel: 128) columns
 };
 cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream);
 int g128_gemm_max_clusters();
+
+// For few rows an expert (g128_rows.cu); behind launch_stage_rows, which clears the
+// arrivals.
+cudaError_t launch_g128_rows(const G128Launch &p, bool bf16, cudaStream_t stream);
 
 }  // namespace a2av

@@ -1,6 +1,7 @@
 // C ABI of the grouped product of 8-bit rows with a float32 scale per 128
 // (declared in include/a2av_gmm_g128.h): argument checks, tensor maps, launches.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "a2av_gmm_g128.h"
@@ -59,6 +60,26 @@ a2av_status validate(const a2av_gmm_g128_desc *d) {
     return A2AV_OK;
 }
 
+// Whether the weight-streaming kernel (g128_rows.cu) takes a call: the rows of the
+// fullest expert, if they spread at random, fit one pass over the weights, and the
+// weights of the experts that they reach are long to read.
+// Measured (us, streaming / tiles, weights from HBM; rows over experts of H1 x N1):
+// 1 over 1 of 7168 x 4096 17.5 / 23.4, 8 over 4 of 4096 x 2048 14.0 / 18.9, 16
+// over 2 of 7168 x 2048 18 / 22, 32 over 16 of 2048 x 2816 28 / 32, 16 over 32 of
+// 4096 x 1536 27 / 32; less to read: 16 over 1 of 4096 x 2048 13.1 / 12.7, of
+// 2048 x 1408 13.1 / 8.3; with 32 rows at a time: 32 over 1 of 7168 x 4096 20.4 /
+// 20.5, 64 over 4 of 4096 x 2048 20.9 / 17.5.
+bool few_rows(const a2av_gmm_g128_desc &d) {
+    if (d.A == 0 || a2av::gated_rows_most(d.A, d.e) > a2av::kG128UnitRows) return false;
+    const double reached = d.e * (1.0 - std::pow(1.0 - 1.0 / d.e, static_cast<double>(d.A)));
+    return reached * d.H1 * d.N1 >= 1.2e7;
+}
+constexpr size_t kArrivalBytes = (a2av::kG128Ctas * 4 + 255) / 256 * 256;
+// Behind the status: arrivals and shares of sums (few rows), staged rows.
+size_t sum_bytes(const a2av_gmm_g128_desc &d) {
+    return few_rows(d) ? kArrivalBytes + static_cast<size_t>(a2av::kG128Ctas) * 2 * a2av::kG128UnitRows * 128 * 4 : 0;
+}
+
 size_t staged_bytes(const a2av_gmm_g128_desc *d) {
     return d->W > 1 ? round256(static_cast<size_t>(d->A) * d->H1) : 0;
 }
@@ -74,7 +95,7 @@ a2av_status a2av_gmm_g128_workspace_size(const a2av_gmm_g128_desc *desc, size_t 
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + staged_bytes(desc);
+    *bytes = kStatusBytes + sum_bytes(*desc) + staged_bytes(desc);
     return A2AV_OK;
 }
 
@@ -91,7 +112,9 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
     for (const void *p : {static_cast<const void *>(ataOut_s), static_cast<const void *>(gmmWeight_s),
                           static_cast<const void *>(recvCounts)})
         if (!aligned(p, 4)) return A2AV_ERR_UNSUPPORTED;
-    if (workspace_bytes < kStatusBytes + staged_bytes(desc) || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
+    size_t need = 0;
+    a2av_gmm_g128_workspace_size(desc, &need);
+    if (workspace_bytes < need || !aligned(workspace, 256)) return A2AV_ERR_WORKSPACE;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     const Device *dev = device_of();
     if (!dev) return A2AV_ERR_CUDA;
@@ -112,6 +135,18 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
     g.status = static_cast<int32_t *>(workspace);
     g.write_status = 1;
     g.wait_limit_ns = kWaitLimitNs;
+    uint8_t *const arrivals = static_cast<uint8_t *>(workspace) + kStatusBytes, *const staged = arrivals + sum_bytes(d);
+    if (few_rows(d)) {
+        void *const dst = d.W > 1 ? staged : nullptr;  // (from one source the rows are expert-major as they arrive)
+        g.arrivals = reinterpret_cast<int32_t *>(arrivals);
+        g.sums = reinterpret_cast<float *>(arrivals + kArrivalBytes);
+        const a2av::StageRowsLaunch sl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status, g.arrivals, a2av::kG128Ctas};
+        if (!codes_map(&g.tmA, dst ? dst : ataOut_q, 1, d.A, d.H1, a2av::kG128UnitRows) ||
+            !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, 128))
+            return A2AV_ERR_CUDA;
+        if (a2av::launch_stage_rows(sl, dev->sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        return a2av::launch_g128_rows(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
+    }
     const int64_t row_tiles = ceil_div(d.A, 256);
     g.bn = (row_tiles + d.e / 2) * ceil_div(d.N1, 128) <= dev->clusters ? 128 : 256;
     const void *rows = ataOut_q;
@@ -119,7 +154,7 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
         // Expert-major rows: all of them, or only the 128-row halves of a tile that
         // straddle a run's end, the others being read in place.  (The copies take the
         // rows as 16-bit elements.)
-        void *dst = static_cast<uint8_t *>(workspace) + kStatusBytes;
+        void *dst = staged;
         g.direct_halves = d.A >= kLongRun * d.W * d.e;
         const a2av::PermuteLaunch pl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status, 1, 1, 8};
         const a2av::StageRowsLaunch sl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status};

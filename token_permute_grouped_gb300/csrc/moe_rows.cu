@@ -392,14 +392,21 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
                 }
                 released();
                 if (!whole && last_of(owner, count)) {
-                    for (int r = 0; r < w.rows; ++r) {
-                        float gate = 0.0f, up = 0.0f;
+                    for (int g = 0; g < w.rows; g += 4) {
+                        float gate[4] = {0, 0, 0, 0}, up[4] = {0, 0, 0, 0};
                         for (int k = owner; k < owner + count; ++k) {
-                            const float *at = share_of(k, owner) + q * 32 + lane + r * 256;
-                            gate += __ldcg(at);
-                            up += __ldcg(at + 128);
+                            const float *at = share_of(k, owner) + q * 32 + lane + g * 256;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (g + i < w.rows) {
+                                    gate[i] += __ldcg(at + i * 256);
+                                    up[i] += __ldcg(at + i * 256 + 128);
+                                }
+                            }
                         }
-                        finish(r, gate, up);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (g + i < w.rows) finish(g + i, gate[i], up[i]);
                     }
                 }
                 c.unit = ++c.job / strips;
