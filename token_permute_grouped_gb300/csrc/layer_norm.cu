@@ -7,9 +7,11 @@
 //
 // HBM-bound, one pass, laid out as the RMS norm (rms_norm.cu): a row stays in
 // the registers of one block between its sums and the scaling, the next row's
-// values are requested before the current one is reduced.  The squares are
-// summed about the mean, in a second reduction of what the registers hold, so
-// a row's offset costs no digits.
+// values are requested before the current one is reduced.  Values and squares are
+// summed in one reduction; where the mean is more than half of the deviation, the
+// squares are summed again about the mean, from what the registers hold, so that
+// a row's offset costs no digits.  (12,288 x 7168 bf16 rows to codes: 127 us with
+// both reductions in every row.)
 #include <algorithm>
 
 #include "activation.cuh"
@@ -22,15 +24,62 @@ namespace a2av {
 
 namespace {
 
-// y has three roundings and a cancellation of up to a few digits against beta:
-// its exponent is decided in double within this many units of a power of two.
+// y has three roundings and may lose a few digits against beta: its exponent is
+// decided with its errors carried along within this many units of a power of two.
 constexpr uint32_t kNearUnits = 64;
 
-// |((s - mu) rstd) gamma + beta| >= pw in double, out of line: for the few blocks next to a power of two.
-__device__ __noinline__ bool reaches_wide(float s, float mu, float mu_lo, float rstd, float rstd_lo, float gamma,
-                                          float beta, float pw) {
-    const double d = static_cast<double>(s) - mu - mu_lo;
-    return fabs(d * (static_cast<double>(rstd) + rstd_lo) * gamma + beta) >= pw;
+// Sums over a row's threads of two values, each in two parts, as row_sum; one
+// barrier.  The lower half of a warp looks after the first value, the upper half
+// after the second: half the instructions of two sums, which would be a third of
+// the kernel's.
+__device__ __forceinline__ void row_sums(float a, float b, float4 *slots, int t, int threads, float2 &sa, float2 &sb) {
+    const int warps = threads / 32, lane = t % 32;
+    const bool upper = lane >= 16;
+    float v = upper ? b : a, lo = 0.0f;
+    two_sum(v, lo, __shfl_xor_sync(0xffffffffu, upper ? a : b, 16), 0.0f);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+        two_sum(v, lo, __shfl_xor_sync(0xffffffffu, v, off), __shfl_xor_sync(0xffffffffu, lo, off));
+    if (warps > 1) {
+        float2 *const mine = reinterpret_cast<float2 *>(slots) + (upper ? 1 : 0);  // of warp w: at 2 w
+        if (lane % 16 == 0) mine[2 * (t / 32)] = make_float2(v, lo);
+        __syncthreads();
+        const int w = lane % 16;
+        const float2 x = w < warps ? mine[2 * w] : make_float2(0.0f, 0.0f);
+        v = x.x, lo = x.y;
+        if (warps > 16) {
+            const float2 y = w + 16 < warps ? mine[2 * (w + 16)] : make_float2(0.0f, 0.0f);
+            two_sum(v, lo, y.x, y.y);
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1)
+            two_sum(v, lo, __shfl_xor_sync(0xffffffffu, v, off), __shfl_xor_sync(0xffffffffu, lo, off));
+    }
+    if (!(fabsf(v) < __uint_as_float(0x7f800000u))) lo = 0.0f;  // (an infinite sum's error is a NaN)
+    sa = make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, lo, 0));
+    sb = make_float2(__shfl_sync(0xffffffffu, v, 16), __shfl_sync(0xffffffffu, lo, 16));
+}
+
+// sum / H of a sum of two parts, in two parts; inv = 1 / H.
+__device__ __forceinline__ float mean_of(float2 sum, float H, float inv, float &lo) {
+    const float q = sum.x * inv;
+    lo = (fmaf(-q, H, sum.x) + sum.y) * inv;
+    return q;
+}
+
+// 1 / sqrt(v + eps) for a v of two parts: one Newton step on the hardware's
+// reciprocal root, and in `lo` what is missing from it.
+__device__ __forceinline__ float inv_root(float v_hi, float v_part, float eps, float &lo) {
+    const float v = v_hi + eps, z = v - v_hi;
+    const float v_lo = (v_hi - (v - z)) + (eps - z) + v_part;
+    float r = rsqrtf(v);
+    lo = 0.0f;
+    if (v > 0.0f && v < __uint_as_float(0x7f800000u)) {
+        r = fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+        const float w = v * r, e = fmaf(v, r, -w);  // v r^2 = (w + e) r
+        lo = -0.5f * r * (fmaf(w, r, -1.0f) + (e + v_lo * r) * r);
+    }
+    return r;
 }
 
 // VPT: vectors of 8 values a thread holds.  KIND: the 8-bit output.
@@ -38,7 +87,8 @@ template <bool BF16, int VPT, int KIND>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch p) {
     using Q = Quant<KIND>;
     constexpr bool PRE = VPT <= 2;
-    __shared__ float2 slots[2][32];  // of the mean's and of the squares' sums
+    __shared__ float4 slots[2][32];  // of both sums, by row
+    __shared__ float2 again[32];     // of the squares about the mean
     const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x;
     const uint4 *gamma = static_cast<const uint4 *>(p.gamma), *beta = static_cast<const uint4 *>(p.beta);
     uint4 raw[VPT], res[VPT];
@@ -55,13 +105,14 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
                 if (t + k * T < vecs) res[k] = ld_once(r + t + k * T);
         }
     };
+    int flip = 0;
     const int step = gridDim.x;
     const int last = p.rows - step;  // rows below it have a next one (row + step may not fit an int)
-    const float H = static_cast<float>(p.H);
+    const float H = static_cast<float>(p.H), inv = 1.0f / H;
     pdl_trigger();
     pdl_wait();
     if (PRE) load(blockIdx.x);
-    for (int row = blockIdx.x; row < p.rows; row = row < last ? row + step : p.rows) {
+    for (int row = blockIdx.x; row < p.rows; row = row < last ? row + step : p.rows, flip ^= 1) {
         const size_t out0 = static_cast<size_t>(row) * vecs;
         if (!PRE) load(row);
         f32x2 s[VPT][4];
@@ -80,40 +131,54 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
             }
         }
         if (PRE && row < last) load(row + step);
-        f32x2 sum2 = 0;
+        f32x2 sum2 = 0, sq2 = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             if (p.h && t + k * T < vecs) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
             sum2 = add2(sum2, add2(add2(s[k][0], s[k][1]), add2(s[k][2], s[k][3])));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq2 = fma2(s[k][i], s[k][i], sq2);
         }
-        float sum, odd;
+        float sum, odd, sq, sq_odd;
         split(sum2, sum, odd);
-        const float2 total = row_sum(sum + odd, slots[0], t, T, 0);
-        // The mean in two parts, its quotient's remainder in the second.
-        const float mu = total.x / H;
-        float mu_lo = (fmaf(-mu, H, total.x) + total.y) / H;
-        if (!(fabsf(mu_lo) < __uint_as_float(0x7f800000u))) mu_lo = 0.0f;  // (of an infinite sum)
-        f32x2 sq2 = 0;
+        split(sq2, sq, sq_odd);
+        float2 total, squares;
+        row_sums(sum + odd, sq + sq_odd, slots[flip], t, T, total, squares);
+        const float inf = __uint_as_float(0x7f800000u);
+        float mu_lo, mu = mean_of(total, H, inv, mu_lo);
+        if (!(fabsf(mu_lo) < inf)) mu_lo = 0.0f;  // (of an infinite sum)
+        const float mean = mu;
+        // The squares about the mean are those about 0 less H mu^2 = mu total, each in
+        // two parts.  Where that is more than a quarter of what is left, the values are
+        // taken about the mean, and the squares summed anew.
+        const float m = mu * total.x, m_lo = fmaf(mu, total.x, -m) + (mu * total.y + mu_lo * total.x);
+        if (squares.x - m > 4.0f * m) {
+            two_sum(squares.x, squares.y, -m, -m_lo);
+        } else {
+            sq2 = 0;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            if (t + k * T < vecs) {
+            for (int k = 0; k < VPT; ++k) {
+                if (t + k * T < vecs) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x2 d = add2(add2(s[k][i], both(-mu)), both(-mu_lo));
-                    if constexpr (!Q::kMx) s[k][i] = d;  // (an mx exponent may ask for the values again)
-                    sq2 = fma2(d, d, sq2);
+                    for (int i = 0; i < 4; ++i) {
+                        s[k][i] = add2(add2(s[k][i], both(-mu)), both(-mu_lo));
+                        sq2 = fma2(s[k][i], s[k][i], sq2);
+                    }
                 }
             }
+            mu = mu_lo = 0.0f;
+            split(sq2, sq, sq_odd);
+            squares = row_sum(sq + sq_odd, again, t, T, 0);
         }
-        float sq, sq_odd;
-        split(sq2, sq, sq_odd);
-        float rstd_lo;
-        const float rstd = inv_rms(row_sum(sq + sq_odd, slots[1], t, T, 0), H, p.eps, rstd_lo);
+        float var_lo, rstd_lo;
+        const float var = mean_of(squares, H, inv, var_lo);
+        const float rstd = inv_root(var, fabsf(var_lo) < inf ? var_lo : 0.0f, p.eps, rstd_lo);
         if (t == 0) {
-            if (p.mean) p.mean[row] = mu;
+            if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
         if (!Q::kAny && !p.y) continue;
+        const f32x2 scale = both(rstd), shift = both(-fmaf(mu, rstd, mu_lo * rstd));  // (mu is below half of the deviation)
         f32x2 y[VPT][4];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -125,14 +190,13 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
                 unpack8<BF16>(__ldg(gamma + v), g);
                 if (beta) unpack8<BF16>(__ldg(beta + v), b);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x2 d = Q::kMx ? add2(add2(s[k][i], both(-mu)), both(-mu_lo)) : s[k][i];
-                    y[k][i] = fma2(mul2(d, both(rstd)), g[i], b[i]);
-                }
+                for (int i = 0; i < 4; ++i) y[k][i] = fma2(fma2(s[k][i], scale, shift), g[i], b[i]);
                 if (p.y) static_cast<uint4 *>(p.y)[out0 + v] = pack8<BF16>(y[k]);
             }
         }
         if constexpr (Q::kAny) {
+            // y's roundings and those of the mean and of rstd, each with its error: near pw,
+            // the difference of the sum's head from it is exact.
             const auto reaches = [&](int k, float pw) {
                 const int v = t + k * T;
                 if (v >= vecs) return false;
@@ -147,7 +211,14 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
                     split(g2[i], g[0], g[1]);
                     split(b2[i], b[0], b[1]);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) hit |= reaches_wide(a[j], mu, mu_lo, rstd, rstd_lo, g[j], b[j], pw);
+                    for (int j = 0; j < 2; ++j) {
+                        float d = a[j], rest = 0.0f;
+                        two_sum(d, rest, -mu, -mu_lo);  // a - mu
+                        const float n = d * rstd, n_lo = fmaf(d, rstd, -n) + (d * rstd_lo + rest * rstd);
+                        float z = n * g[j], z_lo = fmaf(n, g[j], -z) + n_lo * g[j];
+                        two_sum(z, z_lo, b[j], 0.0f);
+                        hit |= fabsf(z) - pw + copysignf(1.0f, z) * z_lo >= 0.0f;
+                    }
                 }
                 return hit;
             };
@@ -181,28 +252,26 @@ cudaError_t launch_norm_vpt(const LayerNormLaunch &p, int kind, int threads, int
     return cudaErrorInvalidValue;
 }
 
-// Sums over a row's threads of two values, as row_sum; one barrier.
-__device__ __forceinline__ float2 row_sum_two(float a, float b, float4 *slots, int t, int threads, int bar) {
-    float a_lo = 0.0f, b_lo = 0.0f;
+// Sums over a row's threads of two values; one barrier.
+__device__ __forceinline__ float2 row_sum_two(float a, float b, float2 *slots, int t, int threads, int bar) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        two_sum(a, a_lo, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, a_lo, off));
-        two_sum(b, b_lo, __shfl_xor_sync(0xffffffffu, b, off), __shfl_xor_sync(0xffffffffu, b_lo, off));
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        b += __shfl_xor_sync(0xffffffffu, b, off);
     }
     const int warps = threads / 32, lane = t % 32;
     if (warps > 1) {
-        if (lane == 0) slots[t / 32] = make_float4(a, a_lo, b, b_lo);
+        if (lane == 0) slots[t / 32] = make_float2(a, b);
         asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-        const float4 w = lane < warps ? slots[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        a = w.x, a_lo = w.y, b = w.z, b_lo = w.w;
+        const float2 w = lane < warps ? slots[lane] : make_float2(0.0f, 0.0f);
+        a = w.x, b = w.y;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
-            two_sum(a, a_lo, __shfl_xor_sync(0xffffffffu, a, off), __shfl_xor_sync(0xffffffffu, a_lo, off));
-            two_sum(b, b_lo, __shfl_xor_sync(0xffffffffu, b, off), __shfl_xor_sync(0xffffffffu, b_lo, off));
+            a += __shfl_xor_sync(0xffffffffu, a, off);
+            b += __shfl_xor_sync(0xffffffffu, b, off);
         }
     }
-    const float inf = __uint_as_float(0x7f800000u);
-    return make_float2(fabsf(a) < inf ? a + a_lo : a, fabsf(b) < inf ? b + b_lo : b);
+    return make_float2(a, b);
 }
 
 // A block holds R rows at a time (blockDim = T x R), each walked on by its own
@@ -212,7 +281,7 @@ __device__ __forceinline__ float2 row_sum_two(float a, float b, float4 *slots, i
 template <bool BF16, int VPT, int MAXT>
 __global__ void __launch_bounds__(MAXT) layer_norm_grad_kernel(const LayerNormGradLaunch p) {
     constexpr bool PRE = VPT <= 2;
-    __shared__ float4 slots[2][32];
+    __shared__ float2 slots[2][32];
     extern __shared__ float4 share[];
     const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x, R = blockDim.y, g = threadIdx.y;
     const uint4 *gamma = static_cast<const uint4 *>(p.gamma);
