@@ -6,8 +6,8 @@ Training (`ExpertBlock`), on the rows an exchange delivered (rank-major, with re
     y = h Wd                    a2av_gmm_run          (one matrix per expert)
 
 and backward from dy: a2av_gmm_backward, then a2av_gated_backward.  In front of the exchange,
-binding.a2av_rms_norm makes the rows (y in the element type, or codes with scales) and the residual stream;
-binding.a2av_rms_norm_backward takes the gradient back through both.
+binding.a2av_rms_norm or binding.a2av_layer_norm makes the rows (y in the element type, or codes with scales) and the
+residual stream; binding.a2av_rms_norm_backward or a2av_layer_norm_backward takes the gradient back through both.
 
 Serving in 8 bits (`MxExpertBlock`), on rows that arrive as the codes and scales a2av_rms_norm wrote:
 
@@ -15,7 +15,14 @@ Serving in 8 bits (`MxExpertBlock`), on rows that arrive as the codes and scales
     h   = act(g) * u            a2av_glu_quant        (codes and scales out)
     y   = h Wd                  a2av_gmm_mx_run
 
-Rows of h and y are expert-major.  Plans hold the workspaces, so one object serves every call of its shape.
+`G128ExpertBlock` is the same with a float32 scale per 128 codes (a2av_gmm_g128_run), as other checkpoints are kept.
+
+A decode step of a few tokens on one GPU (`TokenLayer`), with all experts of the layer:
+
+    n, s = norm(x + residual)   a2av_rms_norm or a2av_layer_norm (s: the residual stream)
+    y    = s + experts(n)       a2av_moe_run          (router, choice, experts, weighted sum)
+
+Rows of h and y are expert-major (TokenLayer's: the tokens').  Plans hold the workspaces, so one object serves every call of its shape.
 """
 
 from __future__ import annotations
@@ -77,3 +84,37 @@ class MxExpertBlock:
         h = binding.a2av_glu_quant(gu, self.act, self.qtype, "mx")
         y, _, _, _ = self.down.run(h.codes, h.scales, expert_counts(recvCounts, self.W, self.e), down_q, down_s)
         return y
+
+
+class G128ExpertBlock:
+    """MxExpertBlock with float32 scales: one for 128 codes of a row, one for 128 columns x 128 codes of a weight.  Weights as
+    a2av_gmm_g128_run takes them: gate_up [e, 2N, H] (an expert's gate columns, then its up columns) and down [e, H, N].
+    H and N are multiples of 128; y [A, H] is of type dtype."""
+
+    def __init__(self, W, e, A, H, N, dtype=torch.bfloat16, act="silu", qtype="e4m3fn", device=None):
+        self.W, self.e, self.act, self.qtype = W, e, act, qtype
+        self.first = binding.G128Plan(W, e, A, H, 2 * N, dtype, qtype, device=device)
+        self.down = binding.G128Plan(1, e, A, N, H, dtype, qtype, device=self.first.device)
+
+    def forward(self, rows_q, rows_s, recvCounts, gate_up_q, gate_up_s, down_q, down_s):
+        gu = self.first.run(rows_q, rows_s, recvCounts, gate_up_q, gate_up_s)
+        h = binding.a2av_glu_quant(gu, self.act, self.qtype, "group128")
+        return self.down.run(h.codes, h.scales, expert_counts(recvCounts, self.W, self.e), down_q, down_s)
+
+
+class TokenLayer:
+    """A decode step's norm and expert layer for T tokens (up to 64): y = s + experts(norm(s)), s = x + residual, which is
+    the next layer's residual stream with y taken as its x.  beta given: layer norm; else RMS norm."""
+
+    def __init__(self, T, E, K, H, N, dtype=torch.bfloat16, act="silu", score="softmax", renormalise=True, scale=1.0,
+                 router_dtype=None, eps=1e-6, device=None):
+        self.eps = eps
+        self.moe = binding.MoePlan(T, E, K, H, N, dtype, act, score, renormalise, scale, router_dtype, device)
+
+    def forward(self, x, residual, gamma, router, gate, up, down, beta=None, bias=None) -> binding.MoeOut:
+        if beta is None:
+            n = binding.a2av_rms_norm(x, gamma, residual, self.eps, want_y=True)
+        else:
+            n = binding.a2av_layer_norm(x, gamma, beta, residual, self.eps, want_y=True)
+        s = x if residual is None else n.h
+        return self.moe.run(n.y, router, gate, up, down, bias=bias, residual=s)
