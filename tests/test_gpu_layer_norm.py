@@ -173,7 +173,8 @@ def test_mx_exponents_next_to_a_power_of_two(qtype):
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("rows,H,with_dh", [(1, 8, True), (1, 7168, True), (7, 1000, False), (700, 256, True),
                                             (3000, 136, True), (650, 4096, False), (20, 9000, True), (20, 20000, True),
-                                            (3, 65528, True)])
+                                            (3, 65528, True), (9, 2048, True), (61, 4096, True), (128, 2048, False), (129, 2048, True),
+                                            (32, 8192, True), (33, 8192, True), (256, 64, True), (20, 8200, True)])
 def test_backward(rows, H, with_dh, dt):
     dtype = DT[dt]
     h, dy = rnd(20, rows, H, dtype=dtype, std=2.0, mean=1.0), rnd(21, rows, H, dtype=dtype, std=0.1)

@@ -57,11 +57,13 @@ struct LayerNormGradLaunch {
     const float *mean, *rstd;
     void *dx;
     float *dgamma, *dbeta;  // both or neither
-    float *partial;         // [blocks][2][H]
+    float *partial;         // [blocks][2][H], where there are several blocks that are not one cluster
     int32_t blocks;
+    int32_t clustered;
 };
-// Blocks the gradient kernel runs for this shape, each with two rows of partial sums.
+// Blocks the gradient kernel runs for this shape, and whether they are one cluster.
 int layer_norm_grad_blocks(int64_t rows, int64_t H);
+bool layer_norm_grad_clustered(int64_t rows, int64_t H);
 cudaError_t launch_layer_norm_grad(const LayerNormGradLaunch &p, bool bf16, cudaStream_t stream);
 
 struct GluLaunch {

@@ -431,7 +431,7 @@ a2av_status a2av_layer_norm_backward_workspace_size(int64_t rows, int64_t H, int
     if (rows < 0 || rows > INT32_MAX || H <= 0 || H >= 65536 || !type16(dtype)) return A2AV_ERR_INVALID;
     if (!mult8(H)) return A2AV_ERR_UNSUPPORTED;
     const int blocks = a2av::layer_norm_grad_blocks(rows, H);
-    *bytes = blocks > 1 ? round256(static_cast<size_t>(blocks) * H * 8) : 0;
+    *bytes = blocks > 1 && !a2av::layer_norm_grad_clustered(rows, H) ? round256(static_cast<size_t>(blocks) * H * 8) : 0;
     return A2AV_OK;
 }
 
@@ -454,7 +454,8 @@ a2av_status a2av_layer_norm_backward(int64_t rows, int64_t H, int32_t dtype, con
     }
     if (rows == 0 && !dgamma) return A2AV_OK;
     a2av::LayerNormGradLaunch p{static_cast<int32_t>(rows), static_cast<int32_t>(H), dy, dh, h, gamma, mean, rstd, dx,
-                                dgamma, dbeta, static_cast<float *>(workspace), a2av::layer_norm_grad_blocks(rows, H)};
+                                dgamma, dbeta, static_cast<float *>(workspace), a2av::layer_norm_grad_blocks(rows, H),
+                                a2av::layer_norm_grad_clustered(rows, H)};
     return a2av::launch_layer_norm_grad(p, dtype == A2AV_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? A2AV_OK
                : A2AV_ERR_CUDA;
