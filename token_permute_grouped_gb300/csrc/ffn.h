@@ -79,16 +79,13 @@ struct GluLaunch {
 };
 cudaError_t launch_glu_quant(GluLaunch p, bool bf16, int act, int kind, cudaStream_t stream);
 
-// All rows in expert-major order (dst NULL: none); clears the status word, and
-// `zeros` words behind `zero` (stage_rows.cu).
+// All rows in expert-major order; clears the status word (stage_rows.cu).
 struct StageRowsLaunch {
     const int32_t *recvCounts;
     int32_t W, e, A, H1;
     const void *src;
     void *dst;
     int32_t *status;
-    int32_t *zero;
-    int32_t zeros;
 };
 cudaError_t launch_stage_rows(const StageRowsLaunch &p, int sms, cudaStream_t stream);
 

@@ -18,7 +18,7 @@ struct G128Launch {
     const int32_t *recvCounts;
     int32_t W, e, A, K, N;
     int32_t qtype;          // 0 E4M3FN, 1 E5M2
-    const float *xs, *ws;   // scales of the arrival rows and of the weights
+    const float *xs, *ws;   // scales of the arrival rows (few-row kernel: those of G128Stage) and of the weights
     void *y;
     int32_t *status;
     int32_t write_status;
@@ -37,8 +37,18 @@ struct G128Launch {
 cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream);
 int g128_gemm_max_clusters();
 
-// For few rows an expert (g128_rows.cu); behind launch_stage_rows, which clears the
-// arrivals.
+// For few rows an expert (g128_rows.cu), behind the kernel that stages them.
+struct G128Stage {
+    const int32_t *recvCounts;
+    int32_t W, e, A, K;
+    const void *src;    // arrival rows' codes
+    const float *xs;    // and scales
+    void *dst;          // codes in expert-major order, or NULL: not wanted
+    float *scales;      // [K / 128][A], rows in expert-major order
+    int32_t *status;    // cleared
+    int32_t *arrivals;  // likewise
+};
+cudaError_t launch_g128_stage(const G128Stage &p, cudaStream_t stream);
 cudaError_t launch_g128_rows(const G128Launch &p, bool bf16, cudaStream_t stream);
 
 }  // namespace a2av

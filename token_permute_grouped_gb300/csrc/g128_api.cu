@@ -64,21 +64,24 @@ a2av_status validate(const a2av_gmm_g128_desc *d) {
 // fullest expert, if they spread at random, fit one pass over the weights, and the
 // weights of the experts that they reach are long to read.
 // Measured (us, streaming / tiles, weights from HBM; rows over experts of H1 x N1):
-// 1 over 1 of 7168 x 4096 17.5 / 23.4, 8 over 4 of 4096 x 2048 14.0 / 18.9, 16
-// over 2 of 7168 x 2048 18 / 22, 32 over 16 of 2048 x 2816 28 / 32, 16 over 32 of
-// 4096 x 1536 27 / 32; less to read: 16 over 1 of 4096 x 2048 13.1 / 12.7, of
-// 2048 x 1408 13.1 / 8.3; with 32 rows at a time: 32 over 1 of 7168 x 4096 20.4 /
-// 20.5, 64 over 4 of 4096 x 2048 20.9 / 17.5.
+// 1 over 1 of 7168 x 4096 14.6 / 23.9, 8 over 4 of 4096 x 2048 15.4 / 17.5, 16 over
+// 4 19.4 / 23.3, 8 over 16 of 2048 x 2816 17.4 / 18.5, 32 over 16 27 / 32, 64 over
+// 32 of 4096 x 1536 50 / 54, 16 over 1 of 4096 x 2048 12.6 / 13.4; less to read: 8
+// over 1 of 2048 x 2048 10.2 / 8.6, 1 over 1 of 1024 x 1024 7.9 / 6.0.  More rows at
+// a time: 32 over 1 of 7168 x 4096 20.4 / 20.5, 64 over 4 of 4096 x 2048 20.5 / 17.5,
+// 128 over 4 28 / 17.5 (a warp's 64 sums and their exchange cost more than the padded
+// rows of a tile).
 bool few_rows(const a2av_gmm_g128_desc &d) {
     if (d.A == 0 || a2av::gated_rows_most(d.A, d.e) > a2av::kG128UnitRows) return false;
     const double reached = d.e * (1.0 - std::pow(1.0 - 1.0 / d.e, static_cast<double>(d.A)));
-    return reached * d.H1 * d.N1 >= 1.2e7;
+    return reached * d.H1 * d.N1 >= 8e6;
 }
+// Behind the status, for few rows: arrivals, shares of sums, the rows' scales; then
+// the staged rows.
 constexpr size_t kArrivalBytes = (a2av::kG128Ctas * 4 + 255) / 256 * 256;
-// Behind the status: arrivals and shares of sums (few rows), staged rows.
-size_t sum_bytes(const a2av_gmm_g128_desc &d) {
-    return few_rows(d) ? kArrivalBytes + static_cast<size_t>(a2av::kG128Ctas) * 2 * a2av::kG128UnitRows * 128 * 4 : 0;
-}
+constexpr size_t kSumBytes = static_cast<size_t>(a2av::kG128Ctas) * 2 * a2av::kG128UnitRows * 128 * 4;
+size_t scale_bytes(const a2av_gmm_g128_desc &d) { return round256(static_cast<size_t>(d.A) * (d.H1 / 128) * 4); }
+size_t few_bytes(const a2av_gmm_g128_desc &d) { return few_rows(d) ? kArrivalBytes + kSumBytes + scale_bytes(d) : 0; }
 
 size_t staged_bytes(const a2av_gmm_g128_desc *d) {
     return d->W > 1 ? round256(static_cast<size_t>(d->A) * d->H1) : 0;
@@ -95,7 +98,7 @@ a2av_status a2av_gmm_g128_workspace_size(const a2av_gmm_g128_desc *desc, size_t 
     if (!desc || !bytes) return A2AV_ERR_NULLPTR;
     const a2av_status s = validate(desc);
     if (s != A2AV_OK) return s;
-    *bytes = kStatusBytes + sum_bytes(*desc) + staged_bytes(desc);
+    *bytes = kStatusBytes + few_bytes(*desc) + staged_bytes(desc);
     return A2AV_OK;
 }
 
@@ -135,16 +138,18 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
     g.status = static_cast<int32_t *>(workspace);
     g.write_status = 1;
     g.wait_limit_ns = kWaitLimitNs;
-    uint8_t *const arrivals = static_cast<uint8_t *>(workspace) + kStatusBytes, *const staged = arrivals + sum_bytes(d);
+    uint8_t *const arrivals = static_cast<uint8_t *>(workspace) + kStatusBytes, *const staged = arrivals + few_bytes(d);
     if (few_rows(d)) {
         void *const dst = d.W > 1 ? staged : nullptr;  // (from one source the rows are expert-major as they arrive)
         g.arrivals = reinterpret_cast<int32_t *>(arrivals);
         g.sums = reinterpret_cast<float *>(arrivals + kArrivalBytes);
-        const a2av::StageRowsLaunch sl{recvCounts, d.W, d.e, g.A, g.K / 2, ataOut_q, dst, g.status, g.arrivals, a2av::kG128Ctas};
+        float *const scales = reinterpret_cast<float *>(arrivals + kArrivalBytes + kSumBytes);
+        g.xs = scales;
+        const a2av::G128Stage st{recvCounts, d.W, d.e, g.A, g.K, ataOut_q, ataOut_s, dst, scales, g.status, g.arrivals};
         if (!codes_map(&g.tmA, dst ? dst : ataOut_q, 1, d.A, d.H1, a2av::kG128UnitRows) ||
             !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, 128))
             return A2AV_ERR_CUDA;
-        if (a2av::launch_stage_rows(sl, dev->sms, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+        if (a2av::launch_g128_stage(st, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         return a2av::launch_g128_rows(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
     }
     const int64_t row_tiles = ceil_div(d.A, 256);

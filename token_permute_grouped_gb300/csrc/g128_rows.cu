@@ -16,12 +16,16 @@
 // put into the workspace by each; the last of them to come adds all in order: the
 // same result every time, whoever it is.
 //
-// Per CTA: warp 0 loads the weights, from before the rows are staged; warp 2 the
-// rows; warp 1 issues the MMAs; warps 4-11 are the epilogue, two for each TMEM lane
+// A kernel before it puts the rows' scales in expert-major order, a K block's next
+// to each other, and the rows themselves where they come from several sources.
+// Per CTA: warp 0 loads the weights, from before that kernel's end; warp 2 the rows;
+// warp 1 issues the MMAs; warps 4-11 are the epilogue, two for each TMEM lane
 // quarter, half of the rows each.  Every wait is bounded.
 //
-// 8 rows over 4 experts of 4096 x 2048 (34 MB of weights where all have rows): 14 us
-// a call; a kernel that does nothing but read as much from HBM takes 12.5.
+// 8 rows over 4 experts of 4096 x 2048 (34 MB of weights where all have rows): 14 to
+// 15 us a call; a kernel that does nothing but read as much from HBM takes 12.5.
+#include <algorithm>
+
 #include "activation.cuh"
 #include "g128.h"
 #include "pair.cuh"
@@ -117,6 +121,41 @@ struct Unit {
     int expert, first, rows;
 };
 
+// Scales (and rows) in expert-major order; clears the status and the arrivals.  A
+// warp a row.
+constexpr int kStageWarps = 8;
+__global__ void __launch_bounds__(kStageWarps * 32) g128_stage_kernel(const __grid_constant__ G128Stage p) {
+    __shared__ SegmentTable table;
+    __shared__ int ok;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    pdl_wait();
+    if (blockIdx.x == 0) {  // before the kernel behind this one can set bits of the status
+        if (threadIdx.x == 0) *p.status = 0;
+        for (int i = threadIdx.x; i < kG128Ctas; i += kStageWarps * 32) p.arrivals[i] = 0;
+        __threadfence();
+        __syncthreads();
+    }
+    pdl_trigger();
+    if (warp == 0) {
+        const bool good = build_segments(p.recvCounts, p.W, p.e, p.A, table, lane);
+        if (lane == 0) ok = good;
+    }
+    __syncthreads();
+    if (!ok) return;  // (the kernel behind this one reports it)
+    const int kblocks = p.K / kBK, vecs = p.K / 16;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kStageWarps + warp; row < p.A;
+         row += static_cast<int64_t>(gridDim.x) * kStageWarps) {
+        const int64_t from = source_row(table, p.W, p.e, static_cast<int32_t>(row));
+        if (p.dst) {
+            const uint4 *in = static_cast<const uint4 *>(p.src) + from * vecs;
+            uint4 *out = static_cast<uint4 *>(p.dst) + row * vecs;
+#pragma unroll 4
+            for (int v = lane; v < vecs; v += 32) out[v] = in[v];
+        }
+        for (int b = lane; b < kblocks; b += 32) p.scales[static_cast<int64_t>(b) * p.A + row] = p.xs[from * kblocks + b];
+    }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) g128_rows_kernel(const __grid_constant__ G128Launch p) {
     extern __shared__ uint8_t smem_raw[];
@@ -169,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1) g128_rows_kernel(const __grid_con
     __syncthreads();
     tc_fence_after_sync();
 
-    // The K blocks of all jobs, and this CTA's.
+    // The K blocks of all jobs, and this CTA's (each has one at least: a job's shares
+    // are those of consecutive CTAs).
     const int units = __shfl_sync(0xffffffffu, C.units, 0);
     const int64_t total = static_cast<int64_t>(units) * strips * kblocks;
     const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total)), me = blockIdx.x;
@@ -271,32 +311,31 @@ __global__ void __launch_bounds__(kThreads, 1) g128_rows_kernel(const __grid_con
         const auto share_of = [&](int cta, int owner) { return p.sums + (2 * static_cast<size_t>(cta) + (cta == owner)) * slot; };
         Place acc;
         int unit = unit0, strip = strip0, block = block0;
-        Unit u{0, 0, 0};
-        const float *ws = p.ws, *xs = nullptr;  // scales of the job's columns, and of this lane's row (NULL: none)
-        float x = 0.0f, w = 0.0f;               // of the next K block
+        Unit u = count > 0 ? unit_at(unit) : Unit{0, 0, 0};
+        const float *ws = p.ws, *xs = p.xs;  // scales of the job's columns, and of this warp's rows, of the next K block
+        float x = 0.0f, w = 0.0f;
+        const auto fetch = [&]() {
+            w = *ws;
+            x = lane < kOwn && half * kOwn + lane < u.rows ? xs[lane] : 0.0f;
+            ++ws;
+            xs += p.A;
+        };
         const auto prepare = [&]() {
-            u = unit_at(unit);
             ws = p.ws + (static_cast<size_t>(u.expert) * strips + strip) * kblocks + block;
-            w = ws[0];
-            const int r = half * kOwn + lane;
-            const bool live = lane < kOwn && r < u.rows;
-            xs = live ? p.xs + static_cast<size_t>(source_row(C.seg, p.W, p.e, u.first + r)) * kblocks + block : nullptr;
-            x = live ? xs[0] : 0.0f;
+            xs = p.xs + static_cast<size_t>(block) * p.A + u.first + half * kOwn;
+            fetch();
         };
         if (count > 0) prepare();
         for (int i = 0; i < count;) {
             const int blocks = min(kblocks - block, count - i);  // of this job
-            const int col = strip * kCols + q * 32 + lane, row0 = u.first + half * kOwn, rows = u.rows - half * kOwn;
+            const int col0 = strip * kCols + q * 32, row0 = u.first + half * kOwn, rows = min(kOwn, u.rows - half * kOwn);
             f32x2 sum[kOwn / 2];
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) sum[j] = 0;
             bool ok = true;
             for (int b = 0; b < blocks; ++b, acc.next(kAccs)) {
                 if (lane < kOwn) scales[lane] = x * w;
-                if (b + 1 < blocks) {
-                    w = ws[b + 1];
-                    if (xs) x = xs[b + 1];
-                }
+                if (b + 1 < blocks) fetch();
                 __syncwarp();
                 if (!pair::wait_phase_warp(&C.abort, tfull0 + 8 * acc.s, acc.turn & 1, p.status, p.wait_limit_ns)) {
                     ok = false;
@@ -323,22 +362,27 @@ __global__ void __launch_bounds__(kThreads, 1) g128_rows_kernel(const __grid_con
             const bool whole = blocks == kblocks;
             i += blocks;
             block = 0;
-            if (++strip == strips) strip = 0, ++unit;
+            if (++strip == strips) {
+                strip = 0;
+                if (i < count) u = unit_at(++unit);
+            }
             if (i < count) prepare();  // (its loads are on their way meanwhile)
-            const auto store = [&](int r, float v) {
-                if (r >= rows || col >= p.N) return;
-                uint16_t bits;
-                if constexpr (BF16) bits = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                else bits = __half_as_ushort(__float2half_rn(v));
-                static_cast<uint16_t *>(p.y)[static_cast<size_t>(row0 + r) * p.N + col] = bits;
+            // Rows r and r + 1 of this lane's column: two neighbouring columns of one row
+            // a lane, 64 bytes of each row a store (N is a multiple of 8).
+            const auto store = [&](int r, float a, float b) {
+                const bool odd = lane & 1;
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                const int row = r + odd, col = col0 + (lane & ~1);
+                if (row < rows && col < p.N)
+                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.y) + static_cast<size_t>(row0 + row) * p.N + col) =
+                        pack2<BF16>(odd ? pair_of(other, b) : pair_of(a, other));
             };
             if (whole) {
 #pragma unroll
                 for (int j = 0; j < kOwn / 2; ++j) {
                     float a, b;
                     split(sum[j], a, b);
-                    store(2 * j, a);
-                    store(2 * j + 1, b);
+                    if (2 * j < rows) store(2 * j, a, b);
                 }
             } else {
                 const int owner = owner_of(first), shares = owner_of(first + kblocks - 1) - owner + 1;
@@ -357,16 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1) g128_rows_kernel(const __grid_con
                 epilogue_sync();
                 if (C.arrived == shares - 1) {
                     __threadfence();
-                    if (rows > 0) {
-                        float v[kOwn] = {};
-                        for (int k = owner; k < owner + shares; ++k) {
-                            const float *const from = share_of(k, owner) + at;
+                    // Two shares are asked for together, and added in order.  (The instructions of
+                    // more, which every CTA fetches for this once, cost more than they save.)
+                    float v[kOwn] = {};
+                    for (int k = 0; k < shares; k += 2) {
+                        const float *const a = share_of(owner + k, owner) + at;
+                        const float *const b = share_of(owner + min(k + 1, shares - 1), owner) + at;
+                        float x[kOwn], y[kOwn];
 #pragma unroll
-                            for (int j = 0; j < kOwn; ++j) v[j] += j < rows ? __ldcg(from + j * kCols) : 0.0f;
+                        for (int j = 0; j < kOwn; ++j) {
+                            x[j] = j < rows ? __ldcg(a + j * kCols) : 0.0f;
+                            y[j] = j < rows && k + 1 < shares ? __ldcg(b + j * kCols) : 0.0f;
                         }
 #pragma unroll
-                        for (int j = 0; j < kOwn; ++j) store(j, v[j]);
+                        for (int j = 0; j < kOwn; ++j) v[j] = v[j] + x[j] + y[j];
                     }
+#pragma unroll
+                    for (int j = 0; j < kOwn; j += 2)
+                        if (j < rows) store(j, v[j], v[j + 1]);
                 }
                 epilogue_sync();  // C.arrived has been read
             }
@@ -391,6 +443,11 @@ cudaError_t launch_type(const G128Launch &p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_g128_stage(const G128Stage &p, cudaStream_t stream) {
+    const int blocks = std::max(1, std::min((p.A + kStageWarps - 1) / kStageWarps, 4 * kG128Ctas));
+    return launch_pdl(g128_stage_kernel, blocks, kStageWarps * 32, 0, 0, stream, p);
+}
 
 cudaError_t launch_g128_rows(const G128Launch &p, bool bf16, cudaStream_t stream) {
     return bf16 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);

@@ -35,12 +35,9 @@ struct MoeChoice {
     const float *logits, *bias;
     int32_t *experts;  // [T, K], or NULL
     float *weights;    // likewise
-    int2 *chosen;      // [T, K]: expert and weight, by launch_moe_choose; NULL: each product chooses for itself
+    int2 *chosen;      // [T, K]: expert and weight, for the products
 };
-// Tokens up to which each product makes the choice, in all of its CTAs.
-constexpr int kMoeFewTokens = 8;
 cudaError_t launch_moe_choose(const MoeChoice &c, cudaStream_t stream);
-
 
 struct MoeRowsLaunch {
     MoeChoice choice;

@@ -93,7 +93,7 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
     a2av::MoeRowsLaunch g;
     std::memset(&g, 0, sizeof g);
     g.choice = a2av::MoeChoice{d.T, d.E, d.K, d.score, d.renormalise != 0, d.scale, r.logits, bias, experts, weights,
-                                d.T > a2av::kMoeFewTokens ? reinterpret_cast<int2 *>(chosen) : nullptr};
+                                reinterpret_cast<int2 *>(chosen)};
     g.H = static_cast<int32_t>(d.H);
     g.N = static_cast<int32_t>(d.N);
     g.residual = residual;
@@ -113,7 +113,7 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
         return A2AV_ERR_CUDA;
     if (a2av::launch_moe_router(r, bf16, d.router_dtype == A2AV_FP32, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     if (d.T == 0) return A2AV_OK;  // (the status is stored)
-    if (g.choice.chosen && a2av::launch_moe_choose(g.choice, stream) != cudaSuccess) return A2AV_ERR_CUDA;
+    if (a2av::launch_moe_choose(g.choice, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     if (a2av::launch_moe_gated(g, bf16, d.act, stream) != cudaSuccess) return A2AV_ERR_CUDA;
     return a2av::launch_moe_down(o, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }

@@ -1,5 +1,5 @@
-// The router's logits of the expert layer for a few tokens: l[t][e] = sum over h
-// of x[t][h] router[e][h].
+// The router of the expert layer for a few tokens: the logits l[t][e] = sum over h
+// of x[t][h] router[e][h], and the choice of experts from them.
 //
 // A warp holds four experts' and four tokens' rows (one and one for a single
 // token) against each other, or a part of them: `split` warps of a block take
@@ -8,7 +8,6 @@
 // latency for few tokens, by the reads of the rows from L2 for many.
 #include "activation.cuh"
 #include "moe.h"
-#include "moe_plan.cuh"
 #include "pdl.cuh"
 #include "rows.cuh"
 
@@ -133,8 +132,84 @@ cudaError_t launch_type(const MoeRouterLaunch &p, cudaStream_t stream) {
                : launch_pdl(moe_router_kernel<BF16, R32, 4, 4>, grid, kRouterThreads, 0, 0, stream, p, split);
 }
 
-// The choice, a warp a token: for more tokens than a CTA has warps (64 tokens over
-// 256 experts, one after the other in every CTA, would take 18 us).
+// A float as an integer of the same order; NaN below everything, -0 as 0.
+__device__ __forceinline__ uint32_t moe_order(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    if (v != v) return 0;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// One warp chooses a token's experts from its logits: lane l looks after experts
+// l, l + 32, ..., in descending order, and the lanes' first ones are compared K
+// times.  Lane k < K has the k-th choice and its weight.
+__device__ __forceinline__ void moe_choose(const MoeChoice &c, const float *logits, int lane, int &expert, float &weight) {
+    constexpr int N = kMoeExperts / 32;
+    const float low = -__uint_as_float(0x7f800000u);
+    float l[N];
+    float top = low;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        l[i] = lane + 32 * i < c.E ? logits[lane + 32 * i] : low;
+        top = fmaxf(top, l[i]);
+    }
+    float total = 1.0f;
+    if (c.score == A2AV_SCORE_SOFTMAX) {
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane + 32 * i < c.E) total += expf(l[i] - top);
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    }
+    const auto score = [&](float v) {
+        return c.score == A2AV_SCORE_SOFTMAX ? expf(v - top) / total : 1.0f / (1.0f + expf(-v));
+    };
+    // A key (0: no expert; what is there is above, since the order of a NaN is 0 and
+    // that of an infinity below the largest integer), and the logit's number.
+    uint32_t key[N];
+    int at[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int e = lane + 32 * i;
+        at[i] = i;
+        key[i] = e < c.E ? moe_order(c.bias ? score(l[i]) + __ldg(c.bias + e) : l[i]) + 1 : 0;
+    }
+    // Insertion by neighbours: descending, equal keys stay in the experts' order.
+#pragma unroll
+    for (int pass = 1; pass < N; ++pass) {
+        if (32 * pass >= c.E) break;
+#pragma unroll
+        for (int i = pass; i > 0; --i) {
+            if (key[i] > key[i - 1]) {
+                const uint32_t k = key[i];
+                const int n = at[i];
+                key[i] = key[i - 1], at[i] = at[i - 1];
+                key[i - 1] = k, at[i - 1] = n;
+            }
+        }
+    }
+    float logit = 0.0f;
+    expert = 0;
+    for (int k = 0; k < c.K; ++k) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, key[0]);
+        const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, key[0] == most ? lane + 32 * at[0] : 0x7fffffff));
+        if (lane == k) expert = e;
+        if (lane == e % 32) {
+#pragma unroll
+            for (int i = 1; i < N; ++i) key[i - 1] = key[i], at[i - 1] = at[i];
+            key[N - 1] = 0;
+        }
+    }
+    // (The logit again, from where it was read.)
+    if (lane < c.K) logit = logits[expert];
+    const float mine = lane < c.K ? score(logit) : 0.0f;
+    float sum = mine;
+    for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    weight = (c.renormalise ? mine / sum : mine) * c.scale;
+}
+
+// The choice, a warp a token.  (In the products' CTAs, each for itself, it took as
+// long for one token, and 18 us for 64 over 256 experts.)
 __global__ void __launch_bounds__(32) moe_choose_kernel(const MoeChoice c) {
     __shared__ float logits[kMoeExperts];
     const int t = blockIdx.x, lane = threadIdx.x;

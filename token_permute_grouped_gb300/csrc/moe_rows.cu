@@ -26,9 +26,15 @@
 // several CTAs share has its sums put into the workspace by each; the last of
 // them to come adds all in order: the same result every time, whoever it is.
 //
-// For few tokens a CTA takes half of an SM's shared memory, so that the second
-// kernel's CTAs stand beside the first's: their weights do not depend on h, and
-// are in their stages when the first kernel ends.
+// The second kernel's weights do not depend on h, and fill the stages of a CTA as
+// soon as the first kernel's have left its SM.  (Half of an SM's shared memory each,
+// so that they stand beside each other from the start, was no faster for one token
+// over 32 experts of 2048 x 1024, and 5 to 11% slower for 16 to 32.)
+//
+// Measured with the router's two kernels (weights from HBM, us; in brackets what the
+// weights of all experts would take at a plain copy's 6.68 TB/s): 1 token, 4 of 32
+// experts of 2048 x 1024 27; 32 tokens 91 [60]; 1 token, 6 of 64 of 2048 x 1408 36,
+// 32 tokens 188 [166]; 1 token, 2 of 8 of 4096 x 4096 49, 32 tokens 157 [121].
 // Per CTA: warps 0, 6 and 7 load, warp 1 issues the MMAs, warps 2-5 are the
 // epilogue (all eight make the plan).  Every wait is bounded.
 #include <algorithm>
@@ -56,8 +62,7 @@ constexpr int kMaxStages = 10;
 constexpr int kBK = 64;                       // contraction elements a stage
 constexpr uint32_t kAtom = kBK * 128;         // 64 k-rows x 64 columns of weights
 constexpr uint32_t kWBytes = 2 * kAtom;
-constexpr size_t kHalfSmem = 114688, kFullSmem = 231424;  // two CTAs an SM, or one
-constexpr int kHalfTokens = 32;               // up to which two are to fit
+constexpr size_t kSmem = 231424;
 static_assert(kThreads >= kMoeExperts, "a thread an expert in the plan");
 
 struct Control {
@@ -80,9 +85,9 @@ struct Shape {
     static constexpr uint32_t kStage = kWBytes + kParts * kXAtom;
     static constexpr uint32_t kAccCols = kMats * R;  // of an accumulator, of which there are two
     static constexpr uint32_t kTmemCols = 2 * kAccCols;
-    static int stages(int T, size_t smem) {
+    static int stages(int T) {
         const size_t part = DOWN ? static_cast<size_t>(T) * 512 : 0;  // the tokens' sums
-        return static_cast<int>(std::min<size_t>(kMaxStages, (smem - 1024 - kControlBytes - part) / kStage));
+        return static_cast<int>(std::min<size_t>(kMaxStages, (kSmem - 1024 - kControlBytes - part) / kStage));
     }
 };
 
@@ -123,7 +128,7 @@ __device__ __forceinline__ bool epilogue_all(bool yes) {
 }
 
 template <bool BF16, bool DOWN, int ACT, int R>
-__global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_constant__ MoeRowsLaunch p) {
+__global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_constant__ MoeRowsLaunch p) {
     using S = Shape<DOWN, R>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -160,20 +165,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
         prefetch_tensormap(&p.tmX);
         if (!DOWN) prefetch_tensormap(&p.tmA[1]);
     }
-    // The logits (or the choice) are there: the first kernel waits for them, and lets
-    // the second one start only behind that.  While it waits it makes a plan of
-    // nothing, which brings the instructions in: its first loads wait for the plan.
-    float *const logits = reinterpret_cast<float *>(base_ptr);  // (no stage is filled yet)
-    for (int pass = DOWN ? 1 : 0; pass < 2; ++pass) {
-        if (pass == 1 && !DOWN) {
-            pdl_wait();
-            pdl_trigger();
-        }
-        if (!p.choice.chosen)
-            for (int i = threadIdx.x; i < T * p.choice.E; i += kThreads) logits[i] = pass == 1 ? __ldcg(p.choice.logits + i) : 0.0f;
-        if (pass == 1 || !p.choice.chosen) moe_plan(p.choice, plan, logits, DOWN ? R : kMoeTokens, pass == 1 && !DOWN && blockIdx.x == 0);
+    // The choice is there: the first kernel waits for it, and lets the second one start
+    // only behind that.
+    if (!DOWN) {
+        pdl_wait();
+        pdl_trigger();
     }
-    fence_proxy_async_smem();  // (TMA writes over the logits)
+    moe_plan(p.choice, plan, DOWN ? R : kMoeTokens);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -392,21 +390,22 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
                 }
                 released();
                 if (!whole && last_of(owner, count)) {
-                    for (int g = 0; g < w.rows; g += 4) {
-                        float gate[4] = {0, 0, 0, 0}, up[4] = {0, 0, 0, 0};
-                        for (int k = owner; k < owner + count; ++k) {
-                            const float *at = share_of(k, owner) + q * 32 + lane + g * 256;
+                    // Four shares are asked for together, and added in order.  (The instructions of
+                    // more, which every CTA fetches for this once, cost more than they save.)
+                    for (int r = 0; r < w.rows; ++r) {
+                        float gate = 0.0f, up = 0.0f;
+                        for (int k = 0; k < count; k += 4) {
+                            float a[4], b[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (g + i < w.rows) {
-                                    gate[i] += __ldcg(at + i * 256);
-                                    up[i] += __ldcg(at + i * 256 + 128);
-                                }
+                            for (int h = 0; h < 4; ++h) {
+                                const float *at = share_of(owner + min(k + h, count - 1), owner) + q * 32 + lane + r * 256;
+                                a[h] = k + h < count ? __ldcg(at) : 0.0f;
+                                b[h] = k + h < count ? __ldcg(at + 128) : 0.0f;
                             }
-                        }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (g + i < w.rows) finish(g + i, gate[i], up[i]);
+                            for (int h = 0; h < 4; ++h) gate += a[h], up += b[h];
+                        }
+                        finish(r, gate, up);
                     }
                 }
                 c.unit = ++c.job / strips;
@@ -445,24 +444,42 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
                     for (int t = 0; t < T; ++t) share[t * 128] = column[t * 128];
                     mine = last_of(owner, count);
                 }
-                for (int i = tid; mine && i < T * 32; i += kEpiWarps * 32) {
+                // Four columns of a row, from their sums.
+                const auto finish = [&](int i, f32x2 lo, f32x2 hi) {
                     const int r = i / 32, col = i % 32 * 4;
-                    if (col0 + col >= cols) continue;
-                    f32x2 s[2] = {0, 0};
-                    for (int k = owner; k < owner + count; ++k) {
-                        const float4 b = whole ? *reinterpret_cast<const float4 *>(part + r * 128 + col)
-                                               : __ldcg(reinterpret_cast<const float4 *>(share_of(k, owner) + r * 128 + col));
-                        s[0] = add2(s[0], pair_of(b.x, b.y));
-                        s[1] = add2(s[1], pair_of(b.z, b.w));
-                    }
+                    if (col0 + col >= cols) return;
                     const size_t o = static_cast<size_t>(r) * p.H + col0 + col;
                     if (p.residual) {
                         const uint2 res = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + o);
-                        s[0] = add2(s[0], unpack2<BF16>(res.x));
-                        s[1] = add2(s[1], unpack2<BF16>(res.y));
+                        lo = add2(lo, unpack2<BF16>(res.x));
+                        hi = add2(hi, unpack2<BF16>(res.y));
                     }
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) =
-                        make_uint2(pack2<BF16>(s[0]), pack2<BF16>(s[1]));
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + o) = make_uint2(pack2<BF16>(lo), pack2<BF16>(hi));
+                };
+                constexpr int kAll = kEpiWarps * 32;
+                if (whole) {
+                    for (int i = tid; i < T * 32; i += kAll) {
+                        const float4 b = reinterpret_cast<const float4 *>(part)[i];
+                        finish(i, pair_of(b.x, b.y), pair_of(b.z, b.w));
+                    }
+                } else if (mine) {
+                    // (as above)
+                    for (int i = tid; i < T * 32; i += kAll) {
+                        f32x2 lo = 0, hi = 0;
+                        for (int k = 0; k < count; k += 4) {
+                            float4 v[4];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h)
+                                v[h] = k + h < count ? __ldcg(reinterpret_cast<const float4 *>(share_of(owner + k + h, owner)) + i)
+                                                     : make_float4(0, 0, 0, 0);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                lo = add2(lo, pair_of(v[h].x, v[h].y));
+                                hi = add2(hi, pair_of(v[h].z, v[h].w));
+                            }
+                        }
+                        finish(i, lo, hi);
+                    }
                 }
                 epilogue_sync();  // the sums have been read
             }
@@ -481,16 +498,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_rows_kernel(const __grid_cons
 template <bool BF16, bool DOWN, int ACT, int R>
 cudaError_t launch_rows(MoeRowsLaunch &p, cudaStream_t stream) {
     auto kern = moe_rows_kernel<BF16, DOWN, ACT, R>;
-    const size_t smem = p.choice.T <= kHalfTokens ? kHalfSmem : kFullSmem;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFullSmem));
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    p.stages = Shape<DOWN, R>::stages(p.choice.T, smem);
-    return launch_pdl(kern, dim3(kMoeCtas), dim3(kThreads), smem, 0, stream, p);
+    p.stages = Shape<DOWN, R>::stages(p.choice.T);
+    return launch_pdl(kern, dim3(kMoeCtas), dim3(kThreads), kSmem, 0, stream, p);
 }
 
-// Rows multiplied: all tokens, or a unit's: what the fullest expert is expected
-// to have, so that one pass over its weights is usual.
+// Rows multiplied: all tokens, or a unit's: what the fullest expert is expected to
+// have, so that one pass over its weights is usual.  (Always 64, us: 8 tokens over
+// 64 experts of 2048 x 1408 165 against 120; always 16 in the second kernel: 64
+// tokens over 8 experts of 4096 x 4096 207 against 180.)
 template <bool BF16, bool DOWN, int ACT>
 cudaError_t launch_unit(MoeRowsLaunch &p, cudaStream_t stream) {
     const int R = moe_unit_rows(p.choice.T, p.choice.E, p.choice.K, DOWN);

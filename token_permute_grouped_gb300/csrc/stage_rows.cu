@@ -83,14 +83,12 @@ __global__ void __launch_bounds__(kStageThreads) stage_rows_kernel(const StageRo
     __shared__ int32_t dst_sums[kStageWarps];
     pdl_wait();
     // Cleared before the kernel behind this one can set bits of it.
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) *p.status = 0;
-        for (int i = threadIdx.x; i < p.zeros; i += kStageThreads) p.zero[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        *p.status = 0;
         __threadfence();
-        __syncthreads();
     }
+    if (blockIdx.x == 0) __syncthreads();
     pdl_trigger();
-    if (!p.dst) return;
     const bool good = block_segments(p.recvCounts, p.W, p.e, p.A, table, sums, dst_sums);
     if (!good) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status, kStatusBadCounts);
@@ -118,7 +116,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_rows_kernel(const StageRo
 }  // namespace
 
 cudaError_t launch_stage_rows(const StageRowsLaunch &p, int sms, cudaStream_t stream) {
-    const int64_t items = p.dst ? static_cast<int64_t>(p.A) * ((p.H1 / 8 + 32 * kPieceVecs - 1) / (32 * kPieceVecs)) : 0;
+    const int64_t items = static_cast<int64_t>(p.A) * ((p.H1 / 8 + 32 * kPieceVecs - 1) / (32 * kPieceVecs));
     const int64_t blocks = std::min<int64_t>((items + kStageWarps - 1) / kStageWarps, static_cast<int64_t>(sms) * kStageBlocks);
     return launch_pdl(stage_rows_kernel, static_cast<unsigned>(std::max<int64_t>(blocks, 1)), kStageThreads, 0, 0, stream,
                       p);
