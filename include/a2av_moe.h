@@ -20,7 +20,8 @@
  *
  * Element type T: bf16 or fp16.  Logits, scores, weights and sums are fp32; the
  * block's values go to the second product as two summands of T, so that y's
- * error is that of its own rounding.  Without a bias the choice is made on the
+ * error is that of its own rounding (fp16: values beyond its range lose digits,
+ * those beyond twice its range are infinite).  Without a bias the choice is made on the
  * logits themselves.  A NaN logit is chosen last; a token's NaN or infinity
  * reaches no other token.
  *

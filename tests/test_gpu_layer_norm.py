@@ -234,3 +234,15 @@ def test_training_step_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_squares_that_overflow_about_zero_only():
+    # +-1.1e18 about 0.45e18: 256 squares sum to 3.6e38 about 0, beyond fp32, and to 3.1e38 about the mean.
+    x = torch.full((2, 256), 1.55e18)
+    x[:, ::2] = -0.65e18
+    x, gamma, beta = x.to(torch.bfloat16), rnd(12, 256), rnd(13, 256)
+    f = L.layer_norm(x, None, gamma, beta, 1e-5)
+    assert float((x.double() ** 2).sum(1).max()) > torch.finfo(torch.float32).max
+    assert float(((x.double() - f["mean"][:, None]) ** 2).sum(1).max()) < torch.finfo(torch.float32).max
+    check(f, binding.a2av_layer_norm(dev(x), dev(gamma), dev(beta), eps=1e-5, want_stats=True, want_y=True), None, "mx",
+          residual=False)

@@ -87,7 +87,9 @@ size_t staged_bytes(const a2av_gmm_g128_desc *d) {
     return d->W > 1 ? round256(static_cast<size_t>(d->A) * d->H1) : 0;
 }
 
-// Mean rows of a (source, expert) run from which whole halves are read in place.
+// Mean rows of a (source, expert) run from which whole halves are read in place
+// (us, in place / all copied; 8 sources, 8 experts of 2048 x 2816, runs of 64: 35 /
+// 33, 96: 56 / 51, 128: 73 / 72; of 7168 x 2048, 256: 217 / 241).
 constexpr int64_t kLongRun = 96;
 
 }  // namespace
@@ -153,6 +155,9 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
         return a2av::launch_g128_rows(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
     }
     const int64_t row_tiles = ceil_div(d.A, 256);
+    // Columns of a tile: 128 where those tiles are one wave (us, 128 / 256: 128 rows of
+    // 1024 x 1024 6.2 / 8.8, 512 of 2048 x 2048 9.5 / 11.3, 300 over 4 experts of 4096 x
+    // 2048 19 / 21; 500 over 16 of 2048 x 2816 38 / 34, 1000 over 32 of 4096 x 1536 79 / 55).
     g.bn = (row_tiles + d.e / 2) * ceil_div(d.N1, 128) <= dev->clusters ? 128 : 256;
     const void *rows = ataOut_q;
     if (d.W > 1 && d.A > 0) {

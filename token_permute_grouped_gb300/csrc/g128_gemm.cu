@@ -17,6 +17,12 @@
 // A warp that loads or issues goes along as a whole and one lane issues, which
 // leaves the operands in uniform registers: a branch on the lane costs two to four
 // times the slots.  Every wait is bounded, as in the other GEMMs.
+//
+// Bound by the scaling: a K block's 256 x 256 products cost a pair's tensor cores
+// 512 clocks and each lane 64 packed FMAs, loads of the same from TMEM and a wait.
+// 34,502 rows of 7168 x 4096 from 32 sources take 717 to 837 us (2.4 to 2.8
+// PFLOP/s, the power limit in force), 56 of them the copying of rows; the product
+// with scales in the tensor cores (a2av_gmm_mx_run) takes 650 to 700 for the shape.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -99,21 +105,6 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// This warp's loads have arrived; r is used only behind this.
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-    asm volatile(""  // (behind the wait as well: an asm takes 30 operands)
-                 : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
-
-
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -123,6 +114,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
+// This warp's loads have arrived; r is used only behind this.
 __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),

@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
         if (!(fabsf(mu_lo) < inf)) mu_lo = 0.0f;  // (of an infinite sum)
         const float mean = mu;
         // The squares about the mean are those about 0 less H mu^2 = mu total, each in
-        // two parts.  Where that is more than a quarter of what is left, the values are
-        // taken about the mean, and the squares summed anew.
+        // two parts.  Where that is more than a quarter of what is left, or the squares
+        // about 0 overflow, the values are taken about the mean, and the squares summed anew.
         const float m = mu * total.x, m_lo = fmaf(mu, total.x, -m) + (mu * total.y + mu_lo * total.x);
-        if (squares.x - m > 4.0f * m) {
+        if (squares.x < inf && squares.x - m > 4.0f * m) {
             two_sum(squares.x, squares.y, -m, -m_lo);
         } else {
             sq2 = 0;
@@ -446,8 +446,10 @@ __global__ void __launch_bounds__(32 * kSlices) column_sums_kernel(const float *
 // Blocks of the gradient and threads of one, one block an SM (as the RMS norm's gradient, rms_norm.cu).
 constexpr int kGradBlocks = 152;
 constexpr int kGradThreads = 512;
-// Resident threads an SM that the norm's grid is made for: 64 registers a thread allow 1024.
-constexpr int kNormThreadsPerSm = 1024;
+// Threads an SM that the norm's grid is made for (us, 1024 / 2048): codes of 12,288 x
+// 7168 93 / 100, of 32,768 x 512 both 18; rows only, 4096 x 2048 14 / 9.6, 16,384 x
+// 1024 18 / 15.4.  (512: 115, 22, 18 and 29.)
+constexpr int kCodeThreadsPerSm = 1024, kPlainThreadsPerSm = 2048;
 
 struct GradShape {
     int vpt, threads, rows;  // vectors a thread, threads a row, rows a block
@@ -466,9 +468,12 @@ cudaError_t launch_norm_type(const LayerNormLaunch &p, int kind, int sms, cudaSt
     const int vecs = p.H / 8;
     const auto go = [&](auto launch, int vpt) {
         const int threads = threads_for(vecs, vpt);
-        return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, kNormThreadsPerSm / threads)), stream);
+        const int per_sm = kind == kQuantNone ? kPlainThreadsPerSm : kCodeThreadsPerSm;
+        return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, per_sm / threads)), stream);
     };
-    // A vector a thread where an SM has one row at most, and no next row's values to hold.
+    // A vector a thread where an SM has one row at most, and no next row's values to hold
+    // (us, one vector / two: 1 x 7168 2.5 / 2.7, 1 x 2048 1.7 / 2.2, 128 x 7168 3.2 / 3.9;
+    // with more rows 1024 x 4096 9.0 / 7.2, 12,288 x 7168 123 / 93).
     if (p.rows <= sms && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
     if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2>, 2);
     if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4>, 4);

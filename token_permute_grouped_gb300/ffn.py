@@ -22,7 +22,8 @@ A decode step of a few tokens on one GPU (`TokenLayer`), with all experts of the
     n, s = norm(x + residual)   a2av_rms_norm or a2av_layer_norm (s: the residual stream)
     y    = s + experts(n)       a2av_moe_run          (router, choice, experts, weighted sum)
 
-Rows of h and y are expert-major (TokenLayer's: the tokens').  Plans hold the workspaces, so one object serves every call of its shape.
+Rows of h and y are expert-major (TokenLayer's: the tokens').  Plans hold the workspaces, so one object serves every call
+of its shape.  G128ExpertBlock, MxExpertBlock and TokenLayer serve; they have no gradients.
 """
 
 from __future__ import annotations
@@ -103,8 +104,8 @@ class G128ExpertBlock:
 
 
 class TokenLayer:
-    """A decode step's norm and expert layer for T tokens (up to 64): y = s + experts(norm(s)), s = x + residual, which is
-    the next layer's residual stream with y taken as its x.  beta given: layer norm; else RMS norm."""
+    """A decode step's norm and expert layer for T tokens (up to 64): y = s + experts(norm(s)), s = x + residual (residual
+    None: x): y is the residual stream behind the layer.  beta given: layer norm; else RMS norm."""
 
     def __init__(self, T, E, K, H, N, dtype=torch.bfloat16, act="silu", score="softmax", renormalise=True, scale=1.0,
                  router_dtype=None, eps=1e-6, device=None):
