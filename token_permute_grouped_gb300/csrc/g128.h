@@ -24,15 +24,15 @@ struct G128Launch {
     int32_t write_status;
     int32_t after_permute;  // launched to overlap the kernel before it, which stages the rows
     int32_t direct_halves;  // halves inside one segment are read in place from ataOut
-    int32_t bn;             // columns of a tile: 256 or 128
-    int32_t grid;           // CTAs, two a cluster
+    int32_t pair;           // tiles of 256 x 256 on two CTAs, or of 128 x 128 on one
+    int32_t grid;           // CTAs
     uint64_t wait_limit_ns;
     // The few-row kernel's:
     float *sums;            // [kG128Ctas][2][kG128UnitRows][128]: shares of jobs that several CTAs have
     int32_t *arrivals;      // [kG128Ctas], 0: of those CTAs, by the first
     CUtensorMap tmA;        // expert-major codes [A, K], box 128 x 128 (few-row kernel: 16) rows
     CUtensorMap tmDirect;   // ataOut codes, likewise
-    CUtensorMap tmB;        // weight codes [e, N, K], box 128 x bn / 2 (few-row kernel: 128) columns
+    CUtensorMap tmB;        // weight codes [e, N, K], box 128 x 128 columns
 };
 cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream);
 int g128_gemm_max_clusters();

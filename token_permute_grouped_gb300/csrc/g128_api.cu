@@ -154,11 +154,16 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
         if (a2av::launch_g128_stage(st, stream) != cudaSuccess) return A2AV_ERR_CUDA;
         return a2av::launch_g128_rows(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
     }
-    const int64_t row_tiles = ceil_div(d.A, 256);
-    // Columns of a tile: 128 where those tiles are one wave (us, 128 / 256: 128 rows of
-    // 1024 x 1024 6.2 / 8.8, 512 of 2048 x 2048 9.5 / 11.3, 300 over 4 experts of 4096 x
-    // 2048 19 / 21; 500 over 16 of 2048 x 2816 38 / 34, 1000 over 32 of 4096 x 1536 79 / 55).
-    g.bn = (row_tiles + d.e / 2) * ceil_div(d.N1, 128) <= dev->clusters ? 128 : 256;
+    const int64_t strips = ceil_div(d.N1, 128);
+    // Waves of single CTAs' tiles and of pairs', each expert's last tile half full: a
+    // pair's takes 1.5 times as long for four times the work, since a single CTA waits
+    // for its operands from L2 (us, single / pairs: 128 rows of 1024 x 1024 5.5 / 8.2,
+    // 512 of 2048 x 2048 8.4 / 12.5, 300 over 4 experts of 4096 x 2048 15 / 20, 1634
+    // over 16 of 2048 x 2816 29 / 35, 1000 over 32 of 4096 x 1536 48 / 54; 2048 over 4 of
+    // 2048 x 1408 21 / 18, 4096 over 8 of 2048 x 2816 48 / 37, 16,384 over 8 143 / 114).
+    const int64_t single = ceil_div((ceil_div(d.A, 128) + d.e / 2) * strips, dev->sms);
+    const int64_t pairs = ceil_div((ceil_div(d.A, 256) + d.e / 2) * ceil_div(strips, 2), dev->clusters);
+    g.pair = 2 * single >= 3 * pairs;
     const void *rows = ataOut_q;
     if (d.W > 1 && d.A > 0) {
         // Expert-major rows: all of them, or only the 128-row halves of a tile that
@@ -177,10 +182,12 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
         if (g.direct_halves && !codes_map(&g.tmDirect, ataOut_q, 1, d.A, d.H1, 128)) return A2AV_ERR_CUDA;
     }
     if (d.A > 0 && (!codes_map(&g.tmA, rows, 1, d.A, d.H1, 128) ||
-                    !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, static_cast<uint32_t>(g.bn / 2))))
+                    !codes_map(&g.tmB, gmmWeight_q, d.e, d.N1, d.H1, 128)))
         return A2AV_ERR_CUDA;
-    const int64_t tiles = (row_tiles + d.e) * ceil_div(d.N1, g.bn);
-    g.grid = static_cast<int32_t>(2 * std::max<int64_t>(1, std::min<int64_t>(dev->clusters, tiles)));
+    // (At most one tile more an expert than its rows fill.)
+    const int64_t tiles = g.pair ? (ceil_div(d.A, 256) + d.e) * ceil_div(strips, 2) : (ceil_div(d.A, 128) + d.e) * strips;
+    const int64_t units = std::max<int64_t>(1, std::min<int64_t>(g.pair ? dev->clusters : dev->sms, tiles));
+    g.grid = static_cast<int32_t>(g.pair ? 2 * units : units);
     return a2av::launch_g128_gemm(g, bf16, stream) == cudaSuccess ? A2AV_OK : A2AV_ERR_CUDA;
 }
 

@@ -1,5 +1,6 @@
 // Grouped GEMM of 8-bit rows with a float32 scale per 128 codes, on tcgen05
-// tensor cores (sm_103a): tiles of 256 rows x 256 (or 128) columns on CTA pairs.
+// tensor cores (sm_103a): tiles of 256 rows x 256 columns on CTA pairs, or of 128 x
+// 128 on single CTAs where there are few.
 //
 //   y[i][n] = sum over b of xs[i][b] ws[n / 128][b] sum over k in b of x[i][k] w[n][k]
 //
@@ -10,8 +11,8 @@
 // into another accumulator.  A lane's row has one scale and a warp's 128 columns
 // one, so a block costs a lane one product and 64 packed FMAs.
 //
-// Per CTA: warps 0 and 2 load (a stage is one K block: 16 KB of rows, 8 or 16 KB
-// of weights, 128-byte swizzle), warp 1 issues the MMAs (even CTA), warps 4-11 sum
+// Per CTA: warps 0 and 2 load (a stage is one K block: 16 KB of rows, 16 KB of
+// weights, 128-byte swizzle), warp 1 issues the MMAs (a pair's even CTA), warps 4-11 sum
 // and store, two for each TMEM lane quarter, half of the columns each.  They take
 // the registers that the first four warps leave.
 // A warp that loads or issues goes along as a whole and one lane issues, which
@@ -36,7 +37,6 @@ namespace a2av {
 namespace {
 
 constexpr int BM = 128;             // rows of a CTA
-constexpr int TILE_M = 2 * BM;
 constexpr int BK = 128;             // codes of a K block, which has one scale
 constexpr int kMmaWarp = 1;
 constexpr int kLoadWarpB = 2;
@@ -48,13 +48,15 @@ constexpr int kRegsAtLaunch = 168, kRegsFew = 56, kRegsMany = 224;
 static_assert(kEpiWarp0 * kRegsFew + kEpiWarps * kRegsMany <= (kEpiWarp0 + kEpiWarps) * kRegsAtLaunch, "registers of a CTA");
 constexpr uint32_t kTmemCols = 512;
 
-template <int BN>
+constexpr int kStages = 6;
+constexpr uint32_t kA = BM * BK, kB = 128 * BK, kStageBytes = kA + kB;
+
+template <bool PAIR>
 struct Shape {
-    static constexpr uint32_t kA = BM * BK, kB = BN / 2 * BK;
-    static constexpr uint32_t kStageBytes = kA + kB;
-    static constexpr int kStages = BN == 256 ? 6 : 8;
-    static constexpr int kAccs = kTmemCols / BN;  // accumulators
-    static constexpr int kCols = BN / 2;          // columns of an epilogue warp
+    static constexpr int kCtas = PAIR ? 2 : 1;
+    static constexpr int M = kCtas * BM, N = kCtas * 128;  // of a tile
+    static constexpr int kAccs = kTmemCols / N;            // accumulators
+    static constexpr int kCols = N / 2;                    // columns of an epilogue warp
 };
 
 constexpr uint32_t kTurnBytes = 32 * 64;  // of an epilogue warp: 32 x 32 results
@@ -63,7 +65,7 @@ struct Group {
     int32_t row0, rows, tile_start;
 };
 struct Control {
-    uint64_t full[8], empty[8];
+    uint64_t full[kStages], empty[kStages];
     uint64_t tfull[4], tempty[4];
     uint32_t tmem_base;
     int32_t abort;
@@ -73,11 +75,8 @@ struct Control {
 };
 constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
-template <int BN>
-constexpr size_t smem_bytes() {
-    return 1024 + Shape<BN>::kStages * Shape<BN>::kStageBytes + kEpiWarps * kTurnBytes + kControlBytes;
-}
-static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory per CTA");
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kTurnBytes + kControlBytes;
+static_assert(kSmem <= 232448, "shared memory per CTA");
 
 struct Tile {
     int g, m, n;
@@ -95,14 +94,30 @@ __device__ __forceinline__ uint32_t instr_desc_f8(uint32_t qtype, uint32_t M, ui
     return (1u << 4) | (qtype << 7) | (qtype << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// The barrier of a tile's CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void sync_tile() {
+    if constexpr (PAIR) pair::sync_all();
+    else __syncthreads();
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -142,20 +157,20 @@ __device__ __forceinline__ bool wait_in_line(int32_t *abort_flag, uint32_t bar, 
     return __all_sync(0xffffffffu, ok);
 }
 
-template <bool BF16, int BN>
+template <bool BF16, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_constant__ G128Launch p) {
-    using S = Shape<BN>;
+    using S = Shape<PAIR>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *base_ptr = smem_raw + (base - raw);
-    const uint32_t turn0 = base + S::kStages * S::kStageBytes;
-    Control &C = *reinterpret_cast<Control *>(base_ptr + S::kStages * S::kStageBytes + kEpiWarps * kTurnBytes);
+    const uint32_t turn0 = base + kStages * kStageBytes;
+    Control &C = *reinterpret_cast<Control *>(base_ptr + kStages * kStageBytes + kEpiWarps * kTurnBytes);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const uint32_t rank = pair::cluster_rank();
-    const int unit = blockIdx.x / 2, nunits = gridDim.x / 2;
-    const int tn = (p.N + BN - 1) / BN, kblocks = p.K / BK;
+    const uint32_t rank = PAIR ? pair::cluster_rank() : 0;
+    const int unit = blockIdx.x / S::kCtas, nunits = gridDim.x / S::kCtas;
+    const int tn = (p.N + S::N - 1) / S::N, kblocks = p.K / BK;
 
     if (warp == 0) {
         // (A kernel that this one overlaps has waited for all before it.)
@@ -165,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
         if (lane < p.e) {
             row0 = C.seg.dst[lane * p.W];
             rows = C.seg.dst[(lane + 1) * p.W] - row0;
-            tiles = good ? blocks_of(rows, TILE_M) * tn : 0;
+            tiles = good ? blocks_of(rows, S::M) * tn : 0;
         }
         int inc = tiles;
 #pragma unroll
@@ -184,16 +199,21 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
             }
         }
     } else if (warp == kMmaWarp) {
-        pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
+        if constexpr (PAIR) {
+            pair::tmem_alloc_pair(smem_u32(&C.tmem_base), kTmemCols);
+        } else {
+            tmem_alloc(smem_u32(&C.tmem_base), kTmemCols);
+            tmem_relinquish();
+        }
     } else if (warp == kEpiWarp0) {
         if (lane == 0) {
-            for (int s = 0; s < S::kStages; ++s) {
+            for (int s = 0; s < kStages; ++s) {
                 mbar_init(smem_u32(&C.full[s]), 2);
                 mbar_init(smem_u32(&C.empty[s]), 1);
             }
             for (int a = 0; a < S::kAccs; ++a) {
                 mbar_init(smem_u32(&C.tfull[a]), 1);
-                mbar_init(smem_u32(&C.tempty[a]), 2 * kEpiWarps);
+                mbar_init(smem_u32(&C.tempty[a]), S::kCtas * kEpiWarps);
             }
             fence_barrier_init();
         }
@@ -203,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
         if (p.direct_halves) prefetch_tensormap(&p.tmDirect);
     }
     tc_fence_before_sync();
-    pair::sync_all();
+    sync_tile<PAIR>();
     tc_fence_after_sync();
 
     const int total = __shfl_sync(0xffffffffu, C.total_tiles, 0);
@@ -222,17 +242,17 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
         // =========================================================== producers: rows, weights
         give_up_registers();
         const bool rows = warp == 0, leader = elect_one();
-        const uint32_t bytes = rows ? S::kA : S::kB, to = base + (rows ? 0 : S::kA);
+        const uint32_t bytes = rows ? kA : kB, to = base + (rows ? 0 : kA);
         Place at;
         bool ok = true, all_there = !p.after_permute || !rows;
         for (int t = unit; t < total && ok; t += nunits) {
             const Tile w = tile_at(C, t, tn);
             const CUtensorMap *map = &p.tmB;
-            int y = w.n * BN + static_cast<int>(rank) * (BN / 2), z = w.g;
+            int y = w.n * S::N + static_cast<int>(rank) * 128, z = w.g;
             if (rows) {
                 const int g_end = C.g[w.g].row0 + C.g[w.g].rows;
                 // This CTA's first row; without a row of its own, any one (nothing of it is stored).
-                const int from = w.m * TILE_M + static_cast<int>(rank) * BM;
+                const int from = w.m * S::M + static_cast<int>(rank) * BM;
                 const bool live = from < C.g[w.g].rows;
                 y = C.g[w.g].row0 + (live ? from : 0);
                 z = 0;
@@ -245,16 +265,17 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
                     all_there = true;
                 }
             }
-            for (int kb = 0; kb < kblocks; ++kb, at.next(S::kStages)) {
+            for (int kb = 0; kb < kblocks; ++kb, at.next(kStages)) {
                 if (at.turn > 0 && !wait_in_line(&C.abort, empty0 + 8 * at.s, (at.turn & 1) ^ 1, p.status,
                                                           p.wait_limit_ns)) {
                     ok = false;
                     break;
                 }
-                const uint32_t own = full0 + 8 * at.s, bar = pair::map_to_rank(own, 0);
+                const uint32_t own = full0 + 8 * at.s;
                 if (leader) {
-                    if (rank == 0) mbar_arrive_expect_tx(own, 2 * bytes);
-                    pair::load_3d(to + at.s * S::kStageBytes, map, bar, kb * BK, y, z);
+                    if (rank == 0) mbar_arrive_expect_tx(own, S::kCtas * bytes);
+                    if constexpr (PAIR) pair::load_3d(to + at.s * kStageBytes, map, pair::map_to_rank(own, 0), kb * BK, y, z);
+                    else tma_load_3d(to + at.s * kStageBytes, map, own, kb * BK, y, z);
                 }
                 __syncwarp();
             }
@@ -264,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
             if (!all_there) pdl_wait();  // (a kernel's end implies that of all before it)
         }
         // The stages that were filled have been read.
-        for (int i = 0; i < S::kStages && ok; ++i) {
+        for (int i = 0; i < kStages && ok; ++i) {
             const int turns = at.s > i ? at.turn + 1 : at.turn;  // fills of stage i
             if (turns > 0)
                 ok = wait_in_line(&C.abort, empty0 + 8 * i, (turns - 1) & 1, p.status, p.wait_limit_ns);
@@ -275,27 +296,32 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
         give_up_registers();
         if (rank == 0) {
             const bool leader = elect_one();
-            const uint32_t idesc = instr_desc_f8(static_cast<uint32_t>(p.qtype), TILE_M, BN);
+            const uint32_t idesc = instr_desc_f8(static_cast<uint32_t>(p.qtype), S::M, S::N);
             const uint64_t a_desc0 = smem_desc(base, 16, 1024, kSwizzle128B);
-            const uint64_t b_desc0 = smem_desc(base + S::kA, 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(base + kA, 16, 1024, kSwizzle128B);
             const uint32_t tmem = __shfl_sync(0xffffffffu, C.tmem_base, 0);
             Place at, acc;
             bool ok = true;
             for (int t = unit; t < total && ok; t += nunits) {
-                for (int kb = 0; kb < kblocks; ++kb, at.next(S::kStages), acc.next(S::kAccs)) {
+                for (int kb = 0; kb < kblocks; ++kb, at.next(kStages), acc.next(S::kAccs)) {
                     if (!wait_in_line(&C.abort, full0 + 8 * at.s, at.turn & 1, p.status, p.wait_limit_ns) ||
                         !wait_in_line(&C.abort, tempty0 + 8 * acc.s, (acc.turn & 1) ^ 1, p.status, p.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint64_t off = static_cast<uint32_t>(at.s * S::kStageBytes) >> 4;
+                    const uint64_t off = static_cast<uint32_t>(at.s * kStageBytes) >> 4;
                     if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
-                            mma_f8_pair(tmem + acc.s * BN, a_desc0 + off + 2 * kk, b_desc0 + off + 2 * kk, idesc, kk > 0);
-                        pair::commit(empty0 + 8 * at.s);
-                        pair::commit(tfull0 + 8 * acc.s);
+                            mma_f8<PAIR>(tmem + acc.s * S::N, a_desc0 + off + 2 * kk, b_desc0 + off + 2 * kk, idesc, kk > 0);
+                        if constexpr (PAIR) {
+                            pair::commit(empty0 + 8 * at.s);
+                            pair::commit(tfull0 + 8 * acc.s);
+                        } else {
+                            mma_commit(empty0 + 8 * at.s);
+                            mma_commit(tfull0 + 8 * acc.s);
+                        }
                     }
                     __syncwarp();
                 }
@@ -317,11 +343,11 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
         // The scales of a tile's first blocks, asked for ahead of the tile.
         const auto prepare = [&](int t) {
             const Tile w = tile_at(C, t, tn);
-            const int r = w.m * TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
+            const int r = w.m * S::M + static_cast<int>(rank) * BM + q * 32 + lane;
             valid = r < C.g[w.g].rows;
             const int src = valid ? source_row(C.seg, p.W, p.e, C.g[w.g].row0 + r) : 0;
             xs = p.xs + static_cast<size_t>(src) * kblocks;
-            const int block = min((w.n * BN + part * S::kCols) / 128, scale_rows - 1);
+            const int block = min((w.n * S::N + part * S::kCols) / 128, scale_rows - 1);
             ws = p.ws + (static_cast<size_t>(w.g) * scale_rows + block) * kblocks;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -347,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
                     xn[1] = xs[kb + 2];
                     wn[1] = ws[kb + 2];
                 }
-                const uint32_t from = t_base + acc.s * BN, empty = pair::map_to_rank(tempty0 + 8 * acc.s, 0);
+                const uint32_t from = t_base + acc.s * S::N, empty = PAIR ? pair::map_to_rank(tempty0 + 8 * acc.s, 0) : tempty0 + 8 * acc.s;
                 if (!wait_in_line(&C.abort, tfull0 + 8 * acc.s, acc.turn & 1, p.status, p.wait_limit_ns)) {
                     ok = false;
                     break;
@@ -372,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
             }
             if (!ok) break;
             const Tile w = tile_at(C, t, tn);
-            const int row0 = C.g[w.g].row0 + w.m * TILE_M + static_cast<int>(rank) * BM + q * 32;
+            const int row0 = C.g[w.g].row0 + w.m * S::M + static_cast<int>(rank) * BM + q * 32;
             const int rows = __popc(__ballot_sync(0xffffffffu, row_valid));  // (the first of the 32)
-            const int col0 = w.n * BN + part * S::kCols;
+            const int col0 = w.n * S::N + part * S::kCols;
             if (t + nunits < total) prepare(t + nunits);
             // Each 32 x 32 block is turned around in this warp's 2 KB (64-byte rows, the
             // 16-byte chunk index XORed with (row / 2) % 4), so that a store takes 64 bytes
@@ -402,30 +428,30 @@ __global__ void __launch_bounds__(kThreads, 1) g128_gemm_kernel(const __grid_con
 
     __syncwarp();
     tc_fence_before_sync();
-    pair::sync_all();
+    sync_tile<PAIR>();
     if (warp == kMmaWarp) {
         tc_fence_after_sync();
-        pair::tmem_free_pair(C.tmem_base, kTmemCols);
+        if constexpr (PAIR) pair::tmem_free_pair(C.tmem_base, kTmemCols);
+        else tmem_dealloc(C.tmem_base, kTmemCols);
     }
 }
 
-template <bool BF16, int BN>
+template <bool BF16, bool PAIR>
 cudaError_t launch_shape(const G128Launch &p, cudaStream_t stream) {
-    auto kern = g128_gemm_kernel<BF16, BN>;
-    const cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<BN>()));
+    auto kern = g128_gemm_kernel<BF16, PAIR>;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    return launch_pdl(kern, p.grid, kThreads, smem_bytes<BN>(), 2, stream, p);
+    return launch_pdl(kern, p.grid, kThreads, kSmem, PAIR ? 2 : 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_g128_gemm(const G128Launch &p, bool bf16, cudaStream_t stream) {
-    if (p.bn == 256) return bf16 ? launch_shape<true, 256>(p, stream) : launch_shape<false, 256>(p, stream);
-    return bf16 ? launch_shape<true, 128>(p, stream) : launch_shape<false, 128>(p, stream);
+    if (p.pair) return bf16 ? launch_shape<true, true>(p, stream) : launch_shape<false, true>(p, stream);
+    return bf16 ? launch_shape<true, false>(p, stream) : launch_shape<false, false>(p, stream);
 }
 
-// Both widths need nearly all of an SM's shared memory: one CTA an SM.
-int g128_gemm_max_clusters() { return max_clusters(g128_gemm_kernel<true, 256>, kThreads, smem_bytes<256>(), 2); }
+// (Nearly all of an SM's shared memory: one CTA an SM.)
+int g128_gemm_max_clusters() { return max_clusters(g128_gemm_kernel<true, true>, kThreads, kSmem, 2); }
 
 }  // namespace a2av
