@@ -256,3 +256,27 @@ def test_random_shapes(seed):
     s = inputs(100 + seed, T, E, H, N, dtype)
     plan = binding.MoePlan(T, E, K, H, N, dtype, act, score, renorm)
     check(call(plan, s, bias, residual), s, K, act, dtype, bias, residual, score=score, renormalise=renorm)
+
+
+@pytest.mark.parametrize("T", [8, 9, 16, 17, 51, 64])
+def test_jobs_of_many_shares(T):
+    # A long contraction over a few columns, then a short one over many: what several CTAs have of a job is added, by
+    # one of them and (second product, above 8 tokens) by a kernel behind it.
+    s = inputs(21, T, 4, 3288, 192, torch.float16)
+    plan = binding.MoePlan(T, 4, 4, 3288, 192, torch.float16, act="gelu_tanh")
+    for residual in (True, False):
+        r = call(plan, s, residual=residual)
+        check(r, s, 4, "gelu_tanh", torch.float16, residual=residual)
+    d = {k: v.cuda() for k, v in s.items()}
+    want = plan.run(d["x"], d["router"], d["gate"], d["up"], d["down"], residual=d["x"])
+    y = d["x"].clone()  # x, the residual and the result in one
+    got = plan.run(y, d["router"], d["gate"], d["up"], d["down"], residual=y, out=binding.MoeOut(y, want.experts, want.weights))
+    assert got.y.data_ptr() == y.data_ptr() and torch.equal(y, want.y)
+
+
+@pytest.mark.parametrize("T,H", [(26, 384), (64, 136), (12, 8)])
+def test_few_columns_of_many_experts(T, H):
+    # All CTAs share the second product's one to three jobs.
+    s = inputs(22, T, 49, H, 384, torch.bfloat16)
+    plan = binding.MoePlan(T, 49, 7, H, 384)
+    check(call(plan, s), s, 7, "silu", torch.bfloat16)

@@ -48,6 +48,8 @@ struct MoeRowsLaunch {
     int32_t *status;
     uint64_t wait_limit_ns;
     int32_t stages;      // set by the launch
+    int32_t joined;      // likewise: the second product's shares are added by a kernel behind it
+    int32_t *units;      // of the second product, for that kernel
     float *sums;         // [kMoeCtas][2][T][256 or 128]: shares of jobs that several CTAs have
     int32_t *arrivals;   // [kMoeCtas], 0: of those CTAs, by the first
     CUtensorMap tmA[2];  // gate and up [E][H][N], or down [E][N][H] (the first): box 64 columns x 64

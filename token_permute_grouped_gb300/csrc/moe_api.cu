@@ -105,6 +105,7 @@ a2av_status a2av_moe_run(const a2av_moe_desc *desc, const void *x, const void *r
     g.wait_limit_ns = kWaitLimitNs;
     a2av::MoeRowsLaunch o = g;
     o.arrivals += a2av::kMoeCtas;
+    o.units = r.status + 1;
     if (d.T > 0 && (!tile_map(&g.tmA[0], gate, d.E, d.H, d.N, bf16, 64, 1) ||
                     !tile_map(&g.tmA[1], up, d.E, d.H, d.N, bf16, 64, 1) ||
                     !tile_map(&g.tmX, x, 1, d.T, d.H, bf16, a2av::moe_unit_rows(d.T, d.E, d.K, false), 1) ||

@@ -24,7 +24,8 @@
 // How many experts are reached is known on the device only, so the K blocks of
 // all jobs, one behind the other, are cut into one equal piece a CTA.  A job that
 // several CTAs share has its sums put into the workspace by each; the last of
-// them to come adds all in order: the same result every time, whoever it is.
+// them to come adds all in order: the same result every time, whoever it is.  For
+// many tokens the second kernel's shares are added by a third one, in the same order.
 //
 // The second kernel's weights do not depend on h, and fill the stages of a CTA as
 // soon as the first kernel's have left its SM.  (Half of an SM's shared memory each,
@@ -33,8 +34,8 @@
 //
 // Measured with the router's two kernels (weights from HBM, us; in brackets what the
 // weights of all experts would take at a plain copy's 6.68 TB/s): 1 token, 4 of 32
-// experts of 2048 x 1024 27; 32 tokens 91 [60]; 1 token, 6 of 64 of 2048 x 1408 36,
-// 32 tokens 188 [166]; 1 token, 2 of 8 of 4096 x 4096 49, 32 tokens 157 [121].
+// experts of 2048 x 1024 27; 32 tokens 82 [60]; 1 token, 6 of 64 of 2048 x 1408 37,
+// 32 tokens 178 [166]; 1 token, 2 of 8 of 4096 x 4096 49, 32 tokens 148 [121].
 // Per CTA: warps 0, 6 and 7 load, warp 1 issues the MMAs, warps 2-5 are the
 // epilogue (all eight make the plan).  Every wait is bounded.
 #include <algorithm>
@@ -52,6 +53,11 @@ namespace a2av {
 namespace {
 
 constexpr int kThreads = 8 * 32;
+// Tokens up to which the last CTA of a job of the second kernel adds its shares; above,
+// a kernel behind it (us, last CTA / kernel: 1 token, 7 of 49 experts of 384 x 384 20 /
+// 27, 4 of 32 of 2048 x 1024 27.5 / 28.5; 8 tokens 32 / 36, 55 / 59; 16 tokens 47 / 41,
+// 83 / 80.5; 64 tokens 90 / 50, 113 / 96.5).
+constexpr int kAloneTokens = 8;
 constexpr int kMmaWarp = 1;
 constexpr int kEpiWarp0 = 2;
 constexpr int kEpiWarps = 4;
@@ -127,6 +133,23 @@ __device__ __forceinline__ bool epilogue_all(bool yes) {
     return all != 0;
 }
 
+// CTAs among which the K blocks of all jobs are cut: a CTA has one at least, so
+// that a job's shares are those of consecutive CTAs.  The first kernel's shares are
+// added by one CTA, about 0.02 us for a row of each, and a K block takes a CTA 0.32
+// us: more CTAs a job than make the sum of both least are not used.  (With all, 16
+// tokens at each of 4 experts of 3288 x 192: 48 us against 39.)
+template <bool DOWN>
+__device__ __forceinline__ int moe_ctas(const MoeChoice &c, int grid, int units, int strips, int kblocks) {
+    const int64_t total = static_cast<int64_t>(units) * strips * kblocks;
+    int ctas = static_cast<int>(min(static_cast<int64_t>(grid), total));
+    if (!DOWN) {
+        const float rows = static_cast<float>(c.T * c.K) / static_cast<float>(units);  // of a job
+        const float shares = fmaxf(1.0f, sqrtf(16.0f * static_cast<float>(kblocks) / rows));
+        ctas = static_cast<int>(fminf(static_cast<float>(ctas), ceilf(static_cast<float>(units * strips) * shares)));
+    }
+    return ctas;
+}
+
 template <bool BF16, bool DOWN, int ACT, int R>
 __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_constant__ MoeRowsLaunch p) {
     using S = Shape<DOWN, R>;
@@ -180,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
     // The K blocks of all jobs, and this CTA's.
     const int length = DOWN ? units * kblocks : kblocks;  // of a job
     const int64_t total = static_cast<int64_t>(DOWN ? strips : units * strips) * length;
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total)), me = blockIdx.x;
+    const int ctas = moe_ctas<DOWN>(p.choice, gridDim.x, units, strips, kblocks), me = blockIdx.x;
     const auto begin_of = [&](int cta) { return static_cast<int>(total * cta / ctas); };
     const auto owner_of = [&](int step) { return static_cast<int>(((step + 1ll) * ctas - 1) / total); };
     const int begin = me < ctas ? begin_of(me) : 0, end = me < ctas ? begin_of(me + 1) : 0;
@@ -206,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
             if (++s == n) s = 0, ++turn;
         }
     };
+
+    if (DOWN && me == 0 && threadIdx.x == 0) *p.units = units;  // (for the kernel that joins)
 
     if (warp == 0 || warp >= kLoadWarp1) {
         // =========================================================== producers
@@ -390,22 +415,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                 }
                 released();
                 if (!whole && last_of(owner, count)) {
-                    // Four shares are asked for together, and added in order.  (The instructions of
-                    // more, which every CTA fetches for this once, cost more than they save.)
-                    for (int r = 0; r < w.rows; ++r) {
-                        float gate = 0.0f, up = 0.0f;
+                    // Four shares (of G rows) are asked for together, and added in order.
+                    constexpr int G = R == 16 ? 1 : 4;
+                    for (int r = 0; r < w.rows; r += G) {
+                        float gate[G] = {}, up[G] = {};
                         for (int k = 0; k < count; k += 4) {
-                            float a[4], b[4];
+                            float a[4][G], b[4][G];
 #pragma unroll
                             for (int h = 0; h < 4; ++h) {
                                 const float *at = share_of(owner + min(k + h, count - 1), owner) + q * 32 + lane + r * 256;
-                                a[h] = k + h < count ? __ldcg(at) : 0.0f;
-                                b[h] = k + h < count ? __ldcg(at + 128) : 0.0f;
+#pragma unroll
+                                for (int g = 0; g < G; ++g) {
+                                    const bool there = k + h < count && r + g < w.rows;
+                                    a[h][g] = there ? __ldcg(at + g * 256) : 0.0f;
+                                    b[h][g] = there ? __ldcg(at + g * 256 + 128) : 0.0f;
+                                }
                             }
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) gate += a[h], up += b[h];
+                            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                                for (int g = 0; g < G; ++g) gate[g] += a[h][g], up[g] += b[h][g];
                         }
-                        finish(r, gate, up);
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            if (r + g < w.rows) finish(r + g, gate[g], up[g]);
                     }
                 }
                 c.unit = ++c.job / strips;
@@ -442,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                     epilogue_sync();
                 } else {
                     for (int t = 0; t < T; ++t) share[t * 128] = column[t * 128];
-                    mine = last_of(owner, count);
+                    mine = !p.joined && last_of(owner, count);
                 }
                 // Four columns of a row, from their sums.
                 const auto finish = [&](int i, f32x2 lo, f32x2 hi) {
@@ -495,6 +528,49 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
     }
 }
 
+// y from the shares of the second kernel's jobs, four columns of a row a thread: all
+// of the GPU reads them at once, where the last CTA of a job would take a
+// microsecond for every 14 KB.
+constexpr int kJoinThreads = 128;
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) moe_join_kernel(const MoeRowsLaunch p) {
+    const int vec = blockIdx.x * kJoinThreads + threadIdx.x, row = blockIdx.y, job = vec / 32;
+    const size_t o = static_cast<size_t>(row) * (p.H / 4) + vec;  // of four columns
+    pdl_trigger();
+    pdl_wait();
+    if (4 * vec >= p.H) return;
+    const int units = *p.units, kblocks = (p.N + kBK - 1) / kBK, strips = (p.H + 127) / 128;
+    const int ctas = moe_ctas<true>(p.choice, kMoeCtas, units, strips, kblocks);
+    const int64_t length = static_cast<int64_t>(units) * kblocks, total = length * strips;
+    const auto owner_of = [&](int64_t step) { return static_cast<int>(((step + 1) * ctas - 1) / total); };
+    const int owner = owner_of(job * length), count = owner_of((job + 1) * length - 1) - owner + 1;
+    if (count == 1) return;  // (stored where it was made)
+    const size_t slot = static_cast<size_t>(p.choice.T) * 32;
+    const float4 *at = reinterpret_cast<const float4 *>(p.sums) + (2 * static_cast<size_t>(owner) + 1) * slot +
+                       static_cast<size_t>(row) * 32 + vec % 32;
+    f32x2 lo = 0, hi = 0;
+    for (int k = 0; k < count; k += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            // (the first CTA's share is its last one, the others' their first)
+            const float4 *from = at + (k + h == 0 ? 0 : (2 * static_cast<size_t>(k + h) - 1) * slot);
+            v[h] = k + h < count ? __ldcg(from) : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            lo = add2(lo, pair_of(v[h].x, v[h].y));
+            hi = add2(hi, pair_of(v[h].z, v[h].w));
+        }
+    }
+    if (p.residual) {
+        const uint2 res = static_cast<const uint2 *>(p.residual)[o];
+        lo = add2(lo, unpack2<BF16>(res.x));
+        hi = add2(hi, unpack2<BF16>(res.y));
+    }
+    static_cast<uint2 *>(p.y)[o] = make_uint2(pack2<BF16>(lo), pack2<BF16>(hi));
+}
+
 template <bool BF16, bool DOWN, int ACT, int R>
 cudaError_t launch_rows(MoeRowsLaunch &p, cudaStream_t stream) {
     auto kern = moe_rows_kernel<BF16, DOWN, ACT, R>;
@@ -533,7 +609,12 @@ cudaError_t launch_moe_gated(MoeRowsLaunch p, bool bf16, int act, cudaStream_t s
 }
 
 cudaError_t launch_moe_down(MoeRowsLaunch p, bool bf16, cudaStream_t stream) {
-    return bf16 ? launch_unit<true, true, A2AV_ACT_SILU>(p, stream) : launch_unit<false, true, A2AV_ACT_SILU>(p, stream);
+    p.joined = p.choice.T > kAloneTokens;
+    const cudaError_t err =
+        bf16 ? launch_unit<true, true, A2AV_ACT_SILU>(p, stream) : launch_unit<false, true, A2AV_ACT_SILU>(p, stream);
+    if (err != cudaSuccess || !p.joined) return err;
+    const dim3 grid((p.H / 4 + kJoinThreads - 1) / kJoinThreads, p.choice.T);
+    return launch_pdl(bf16 ? moe_join_kernel<true> : moe_join_kernel<false>, grid, kJoinThreads, 0, 0, stream, p);
 }
 
 }  // namespace a2av
