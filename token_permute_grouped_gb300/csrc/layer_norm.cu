@@ -10,8 +10,10 @@
 // values are requested before the current one is reduced.  Values and squares are
 // summed in one reduction; where the mean is more than half of the deviation, the
 // squares are summed again about the mean, from what the registers hold, so that
-// a row's offset costs no digits.  (12,288 x 7168 bf16 rows to codes: 127 us with
-// both reductions in every row.)
+// a row's offset costs no digits.  With codes the instructions count as much as HBM:
+// gamma and beta wait in shared memory as fp32 (109 us against 115.6 for mx codes).
+// 12,288 x 7168 bf16 rows with a residual: to mx codes 107 us, to codes per 128 100
+// (6.1 TB/s, 92% of a copy's rate; 127 with a reduction a sum in every row).
 #include <algorithm>
 
 #include "activation.cuh"
@@ -83,13 +85,32 @@ __device__ __forceinline__ float inv_root(float v_hi, float v_part, float eps, f
     return r;
 }
 
+// a + b, b of two 16-bit elements: one instruction each, without a conversion first
+// (mx codes of 12,288 x 7168 118.5 -> 115.6 us; without codes HBM is the bound, and
+// packed additions were 2% faster).
+template <bool BF16>
+__device__ __forceinline__ f32x2 add_elements(f32x2 a, uint32_t b) {
+    float x, y;
+    split(a, x, y);
+    if constexpr (BF16)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+            : "+f"(x), "+f"(y)
+            : "r"(b));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+            : "+f"(x), "+f"(y)
+            : "r"(b));
+    return pair_of(x, y);
+}
+
 // VPT: vectors of 8 values a thread holds.  KIND: the 8-bit output.
 template <bool BF16, int VPT, int KIND>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch p) {
     using Q = Quant<KIND>;
-    constexpr bool PRE = VPT <= 2;
+    constexpr bool PRE = VPT <= 2, WIDE = VPT == 2 && Q::kAny;
     __shared__ float4 slots[2][32];  // of both sums, by row
     __shared__ float2 again[32];     // of the squares about the mean
+    extern __shared__ float4 wide[];  // gamma and beta: four planes of a vector's values 0-3 and 4-7
     const int vecs = p.H / 8, T = blockDim.x, t = threadIdx.x;
     const uint4 *gamma = static_cast<const uint4 *>(p.gamma), *beta = static_cast<const uint4 *>(p.beta);
     uint4 raw[VPT], res[VPT];
@@ -113,6 +134,26 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
     pdl_trigger();
     pdl_wait();
     if (PRE) load(blockIdx.x);
+    if (WIDE) {  // (a thread reads what it has written)
+        const auto put = [&](const uint4 *from, float4 *to, int v) {
+            f32x2 f[4] = {0, 0, 0, 0};
+            if (from) unpack8<BF16>(__ldg(from + v), f);
+            split(f[0], to[v].x, to[v].y), split(f[1], to[v].z, to[v].w);
+            split(f[2], to[vecs + v].x, to[vecs + v].y), split(f[3], to[vecs + v].z, to[vecs + v].w);
+        };
+        for (int v = t; v < vecs; v += T) {
+            put(gamma, wide, v);
+            put(beta, wide + 2 * vecs, v);
+        }
+    }
+    const auto weights = [&](const uint4 *from, const float4 *in, int v, f32x2 (&f)[4]) {
+        if (WIDE) {
+            const float4 a = in[v], b = in[vecs + v];
+            f[0] = pair_of(a.x, a.y), f[1] = pair_of(a.z, a.w), f[2] = pair_of(b.x, b.y), f[3] = pair_of(b.z, b.w);
+        } else if (from) {
+            unpack8<BF16>(__ldg(from + v), f);
+        }
+    };
     for (int row = blockIdx.x; row < p.rows; row = row < last ? row + step : p.rows, flip ^= 1) {
         const size_t out0 = static_cast<size_t>(row) * vecs;
         if (!PRE) load(row);
@@ -124,10 +165,17 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
             if (t + k * T < vecs) {
                 unpack8<BF16>(raw[k], s[k]);
                 if (p.residual) {
-                    f32x2 f[4];
-                    unpack8<BF16>(res[k], f);
+                    if constexpr (Q::kAny) {
+                        s[k][0] = add_elements<BF16>(s[k][0], res[k].x);
+                        s[k][1] = add_elements<BF16>(s[k][1], res[k].y);
+                        s[k][2] = add_elements<BF16>(s[k][2], res[k].z);
+                        s[k][3] = add_elements<BF16>(s[k][3], res[k].w);
+                    } else {
+                        f32x2 f[4];
+                        unpack8<BF16>(res[k], f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[k][i] = add2(s[k][i], f[i]);
+                        for (int i = 0; i < 4; ++i) s[k][i] = add2(s[k][i], f[i]);
+                    }
                 }
             }
         }
@@ -135,10 +183,14 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
         f32x2 sum2 = 0, sq2 = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            if (p.h && t + k * T < vecs) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
             sum2 = add2(sum2, add2(add2(s[k][0], s[k][1]), add2(s[k][2], s[k][3])));
 #pragma unroll
             for (int i = 0; i < 4; ++i) sq2 = fma2(s[k][i], s[k][i], sq2);
+        }
+        if (p.h) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (t + k * T < vecs) static_cast<uint4 *>(p.h)[out0 + t + k * T] = pack8<BF16>(s[k]);
         }
         float sum, odd, sq, sq_odd;
         split(sum2, sum, odd);
@@ -188,8 +240,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
             for (int i = 0; i < 4; ++i) y[k][i] = 0;
             if (v < vecs) {
                 f32x2 g[4], b[4] = {0, 0, 0, 0};
-                unpack8<BF16>(__ldg(gamma + v), g);
-                if (beta) unpack8<BF16>(__ldg(beta + v), b);
+                weights(gamma, wide, v, g);
+                weights(beta, wide + 2 * vecs, v, b);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[k][i] = fma2(fma2(s[k][i], scale, shift), g[i], b[i]);
                 if (p.y) static_cast<uint4 *>(p.y)[out0 + v] = pack8<BF16>(y[k]);
@@ -236,12 +288,21 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
     }
 }
 
+constexpr int kMaxWide = 16384 * 8;  // the widest row of two vectors a thread
+
 template <bool BF16, int VPT>
 cudaError_t launch_norm_vpt(const LayerNormLaunch &p, int kind, int threads, int grid, cudaStream_t stream) {
+    const size_t smem = VPT == 2 && kind != kQuantNone ? static_cast<size_t>(p.H) * 8 : 0;
+    const auto go = [&](auto kern) {
+        if (smem > 48 * 1024) {
+            const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWide);
+            if (err != cudaSuccess) return err;
+        }
+        return launch_pdl(kern, grid, threads, smem, 0, stream, p);
+    };
     switch (kind) {
-#define A2AV_KIND(...)                                                                             \
-    case __VA_ARGS__:                                                                              \
-        return launch_pdl(layer_norm_kernel<BF16, VPT, __VA_ARGS__>, grid, threads, 0, 0, stream, p)
+#define A2AV_KIND(...) \
+    case __VA_ARGS__: return go(layer_norm_kernel<BF16, VPT, __VA_ARGS__>)
         A2AV_KIND(kQuantNone);
         A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E4M3FN));
         A2AV_KIND(quant_kind(A2AV_QMODE_MX, A2AV_Q_E5M2));
@@ -471,10 +532,11 @@ cudaError_t launch_norm_type(const LayerNormLaunch &p, int kind, int sms, cudaSt
         const int per_sm = kind == kQuantNone ? kPlainThreadsPerSm : kCodeThreadsPerSm;
         return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, per_sm / threads)), stream);
     };
-    // A vector a thread where an SM has one row at most, and no next row's values to hold
-    // (us, one vector / two: 1 x 7168 2.5 / 2.7, 1 x 2048 1.7 / 2.2, 128 x 7168 3.2 / 3.9;
-    // with more rows 1024 x 4096 9.0 / 7.2, 12,288 x 7168 123 / 93).
-    if (p.rows <= sms && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
+    // A vector a thread where all rows are on the SMs at once, and there are no next
+    // rows' values to hold (us, one vector / two: 1 x 7168 2.5 / 2.7, 128 x 7168 3.2 /
+    // 3.9, 300 x 4096 3.3 / 4.4, 600 x 2048 3.3 / 4.6, 2000 x 512 3.2 / 4.1; with more
+    // rows 1024 x 4096 9.0 / 7.2, 12,288 x 7168 123 / 93).
+    if (static_cast<int64_t>(p.rows) * threads_for(vecs, 1) <= static_cast<int64_t>(sms) * 1024 && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
     if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2>, 2);
     if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4>, 4);
     return go(launch_norm_vpt<BF16, 8>, 8);
