@@ -246,3 +246,14 @@ def test_squares_that_overflow_about_zero_only():
     assert float(((x.double() - f["mean"][:, None]) ** 2).sum(1).max()) < torch.finfo(torch.float32).max
     check(f, binding.a2av_layer_norm(dev(x), dev(gamma), dev(beta), eps=1e-5, want_stats=True, want_y=True), None, "mx",
           residual=False)
+
+
+@pytest.mark.parametrize("qtype,mode", [("e4m3fn", "mx"), ("int8", "group128")])
+@pytest.mark.parametrize("rows,H", [(700, 7168), (170, 16384), (200, 8192), (153, 8192), (2500, 512)])
+def test_codes_around_the_limits_of_the_wide_weights(rows, H, qtype, mode):
+    # One vector a thread while all rows are resident, then two with gamma and beta in shared memory, up to 128 KB.
+    x, res = rnd(31, rows, H), rnd(32, rows, H)
+    gamma, beta = rnd(33, H), rnd(34, H)
+    for b in (beta, None):
+        r = binding.a2av_layer_norm(dev(x), dev(gamma), dev(b), dev(res), eps=1e-5, qtype=qtype, mode=mode)
+        check(L.layer_norm(x, res, gamma, b, 1e-5), r, qtype, mode, want_y=False)

@@ -280,3 +280,27 @@ def test_few_columns_of_many_experts(T, H):
     s = inputs(22, T, 49, H, 384, torch.bfloat16)
     plan = binding.MoePlan(T, 49, 7, H, 384)
     check(call(plan, s), s, 7, "silu", torch.bfloat16)
+
+
+def test_two_plans_of_many_tokens_at_once_and_replayed():
+    """Above 8 tokens a kernel behind the second product adds the shares: two streams at a time, and a graph of both."""
+    T, E, K, H, N = 33, 24, 3, 264, 520
+    plans = [binding.MoePlan(T, E, K, H, N) for _ in range(2)]
+    hosts = [inputs(23 + i, T, E, H, N, torch.bfloat16) for i in range(2)]
+    want = [call(plans[i], hosts[i]) for i in range(2)]
+    dev = [{k: v.cuda() for k, v in s.items()} for s in hosts]
+    run = lambda i, **kw: plans[i].run(dev[i]["x"], dev[i]["router"], dev[i]["gate"], dev[i]["up"], dev[i]["down"],
+                                       residual=dev[i]["residual"], **kw)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    outs = [[run(i, stream=streams[i]) for i in range(2)] for _ in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[i].y, want[i].y) for o in outs for i in range(2))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        got = [run(0), run(1), run(0)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g.y, want[i].y) for g, i in zip(got, (0, 1, 0)))
