@@ -21,7 +21,7 @@
 //
 // Bound by the scaling: a K block's 256 x 256 products cost a pair's tensor cores
 // 512 clocks and each lane 64 packed FMAs, loads of the same from TMEM and a wait.
-// 34,502 rows of 7168 x 4096 from 32 sources take 717 to 837 us (2.4 to 2.8
+// 34,502 rows of 7168 x 4096 from 32 sources take 717 to 856 us (2.4 to 2.8
 // PFLOP/s, the power limit in force), 56 of them the copying of rows; the product
 // with scales in the tensor cores (a2av_gmm_mx_run) takes 650 to 700 for the shape.
 #include <algorithm>

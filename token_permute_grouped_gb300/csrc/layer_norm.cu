@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(32 * kSlices) column_sums_kernel(const float *
 constexpr int kGradBlocks = 152;
 constexpr int kGradThreads = 512;
 // Threads an SM that the norm's grid is made for (us, 1024 / 2048): codes of 12,288 x
-// 7168 93 / 100, of 32,768 x 512 both 18; rows only, 4096 x 2048 14 / 9.6, 16,384 x
+// 7168 88 / 94.5, of 32,768 x 512 16 / 19; rows only, 4096 x 2048 14 / 9.6, 16,384 x
 // 1024 18 / 15.4.  (512: 115, 22, 18 and 29.)
 constexpr int kCodeThreadsPerSm = 1024, kPlainThreadsPerSm = 2048;
 
@@ -535,7 +535,7 @@ cudaError_t launch_norm_type(const LayerNormLaunch &p, int kind, int sms, cudaSt
     // A vector a thread where all rows are on the SMs at once, and there are no next
     // rows' values to hold (us, one vector / two: 1 x 7168 2.5 / 2.7, 128 x 7168 3.2 /
     // 3.9, 300 x 4096 3.3 / 4.4, 600 x 2048 3.3 / 4.6, 2000 x 512 3.2 / 4.1; with more
-    // rows 1024 x 4096 9.0 / 7.2, 12,288 x 7168 123 / 93).
+    // rows 1024 x 4096 8.5 / 7.6, 12,288 x 7168 125 / 88).
     if (static_cast<int64_t>(p.rows) * threads_for(vecs, 1) <= static_cast<int64_t>(sms) * 1024 && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
     if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2>, 2);
     if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4>, 4);
