@@ -43,7 +43,7 @@ struct MoeRowsLaunch {
     MoeChoice choice;
     int32_t H, N;
     const void *residual;
-    void *h;             // [2][T * K][N]: the gated block's values, expert after expert, in two summands
+    void *h;             // [2][T * K][N]: the gated block's values, expert after expert, in two summands (value_parts)
     void *y;
     int32_t *status;
     uint64_t wait_limit_ns;

@@ -18,8 +18,7 @@
 //           each.  A unit's product starts its TMEM accumulator afresh, and is
 //           added with the tokens' weights to sums [T][128] in shared memory:
 //           what an expert computes reaches its own tokens only.  h comes as two
-//           summands of the element type, each multiplied into the same
-//           accumulator.
+//           summands of the element type (value_parts).
 //
 // How many experts are reached is known on the device only, so the K blocks of
 // all jobs, one behind the other, are cut into one equal piece a CTA.  A job that
@@ -81,15 +80,41 @@ struct Control {
 };
 constexpr size_t kControlBytes = (sizeof(Control) + 1023) / 1024 * 1024;
 
+// A value of the gated block as two summands of the element type for the second
+// product, which has the other factor in that type.  bf16: value = h + l, into one
+// accumulator (two_parts.cuh: 2^-15 of the value and less).  fp16: value = 2 h + l / 1024,
+// into an accumulator each, which are added as fp32: one scale for both would take
+// values below 1e-4 for multiples of fp16's least, 6e-8.  So a value is held to 2^-22 of
+// it or 2^-35, from 0 to twice fp16's range, and is infinite beyond.  h is 0 for 0 only:
+// an infinite weight makes h's sum infinite or NaN, which is then the product's (l may
+// have the other sign).
+constexpr float kHigh = 2.0f, kLow = 1.0f / 1024.0f;
+template <bool BF16>
+__device__ __forceinline__ void value_parts(float v, uint32_t &h, uint32_t &l) {
+    if constexpr (BF16) {
+        two_parts<true>(v, h, l);
+    } else {
+        h = __half_as_ushort(__float2half_rn(v / kHigh));
+        if ((h & 0x7fffu) == 0 && v != 0.0f) h = v < 0.0f ? 0x8001u : 1u;
+        const float high = kHigh * __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+        l = (h & 0x7fffu) < 0x7c00u ? __half_as_ushort(__float2half_rn((v - high) / kLow)) : 0u;
+    }
+}
+__device__ __forceinline__ float sum_of_parts(float h, float l) {
+    return fabsf(h) < __uint_as_float(0x7f800000u) ? fmaf(kHigh, h, kLow * l) : h;
+}
+
 // A stage's rows: R of 64 elements, twice where they come as two summands.  A K
-// block is a stage of each matrix.
-template <bool DOWN, int R>
+// block is a stage of each matrix.  The gate's and the up projection's products have an
+// accumulator each, and so have fp16's summands.
+template <bool BF16, bool DOWN, int R>
 struct Shape {
     static constexpr int kMats = DOWN ? 1 : 2;
     static constexpr int kParts = DOWN ? 2 : 1;
+    static constexpr bool kApart = DOWN && !BF16;
     static constexpr uint32_t kXAtom = R * 128;
     static constexpr uint32_t kStage = kWBytes + kParts * kXAtom;
-    static constexpr uint32_t kAccCols = kMats * R;  // of an accumulator, of which there are two
+    static constexpr uint32_t kAccCols = (kApart ? 2 : kMats) * R;  // of a set of accumulators, of which there are two
     static constexpr uint32_t kTmemCols = 2 * kAccCols;
     static int stages(int T) {
         const size_t part = DOWN ? static_cast<size_t>(T) * 512 : 0;  // the tokens' sums
@@ -105,6 +130,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// This warp's loads have arrived; r is used only behind this.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 // One column.
@@ -152,7 +186,7 @@ __device__ __forceinline__ int moe_ctas(const MoeChoice &c, int grid, int units,
 
 template <bool BF16, bool DOWN, int ACT, int R>
 __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_constant__ MoeRowsLaunch p) {
-    using S = Shape<DOWN, R>;
+    using S = Shape<BF16, DOWN, R>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -319,8 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                         if (kk < ksteps) {
 #pragma unroll
                             for (int q = 0; q < S::kParts; ++q)
-                                mma_f16(tmem + acc * S::kAccCols + m * R, a_desc0 + off + 128 * kk,
-                                        b_desc0 + off + ((q * S::kXAtom + kk * 32) >> 4), idesc, !starts || kk > 0 || q > 0);
+                                mma_f16(tmem + acc * S::kAccCols + (S::kApart ? q : m) * R, a_desc0 + off + 128 * kk,
+                                        b_desc0 + off + ((q * S::kXAtom + kk * 32) >> 4), idesc,
+                                        !starts || kk > 0 || (!S::kApart && q > 0));
                         }
                     }
                     mma_commit(empty0 + 8 * at.s);
@@ -383,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                     float f, unused;
                     a2av::split(mul2(act_value<ACT>(pair_of(gate, 0.0f)), pair_of(up, 0.0f)), f, unused);
                     uint32_t h, l;
-                    two_parts<BF16>(f, h, l);
+                    value_parts<BF16>(f, h, l);
                     uint16_t *to = static_cast<uint16_t *>(p.h) + static_cast<size_t>(w.first + r) * p.N + col;
                     to[0] = static_cast<uint16_t>(h);
                     to[static_cast<size_t>(T) * topk * p.N] = static_cast<uint16_t>(l);
@@ -451,15 +486,21 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
 #pragma unroll
                     for (int g = 0; g < R; g += 16) {
                         if (g < w.rows) {
-                            uint32_t r[16];
+                            uint32_t r[16], low[16];
                             tmem_ld16(t_base + (seg & 1) * S::kAccCols + g, r);
-                            tmem_ld_wait();
+                            if constexpr (S::kApart) {
+                                tmem_ld16(t_base + (seg & 1) * S::kAccCols + R + g, low);
+                                tmem_ld16_wait(low);
+                            }
+                            tmem_ld16_wait(r);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 if (g + i < w.rows) {
                                     const int pair = plan.pairs[w.first + g + i];
                                     float *to = column + pair / topk * 128;
-                                    *to = fmaf(plan.weight[pair], __uint_as_float(r[i]), *to);
+                                    float d = __uint_as_float(r[i]);
+                                    if constexpr (S::kApart) d = sum_of_parts(d, __uint_as_float(low[i]));
+                                    *to = fmaf(plan.weight[pair], d, *to);
                                 }
                             }
                         }
@@ -576,7 +617,7 @@ cudaError_t launch_rows(MoeRowsLaunch &p, cudaStream_t stream) {
     auto kern = moe_rows_kernel<BF16, DOWN, ACT, R>;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    p.stages = Shape<DOWN, R>::stages(p.choice.T);
+    p.stages = Shape<BF16, DOWN, R>::stages(p.choice.T);
     return launch_pdl(kern, dim3(kMoeCtas), dim3(kThreads), kSmem, 0, stream, p);
 }
 
