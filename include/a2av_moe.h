@@ -7,6 +7,7 @@
  *     p = softmax(l) or 1 / (1 + e^-l)
  *     experts = the K largest of p + bias            (ties: the lowest index)
  *     w = p of the chosen, over their sum where `renormalise` is set, times scale
+ *         (a ratio of scores, however small they are)
  *     y = residual + sum over k of w_k (act(x Wg_k) * (x Wu_k)) Wd_k
  *
  * Each expert's weights are read once for the tokens that chose it.  Larger

@@ -202,7 +202,18 @@ __device__ __forceinline__ void moe_choose(const MoeChoice &c, const float *logi
     }
     // (The logit again, from where it was read.)
     if (lane < c.K) logit = logits[expert];
-    const float mine = lane < c.K ? score(logit) : 0.0f;
+    float mine = lane < c.K ? score(logit) : 0.0f;
+    if (c.renormalise) {
+        // Of the scores only their ratios are left, taken relative to the largest chosen
+        // logit m: all of them may lie below fp32's range (sigmoid below -88; softmax where
+        // the bias chose), and their sum would be 0.  sigmoid(v) = e^v / (1 + e^v).
+        float m = lane < c.K ? logit : low;
+        for (int off = 4; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        float ratio = expf(logit - m);
+        if (c.score == A2AV_SCORE_SOFTMAX) ratio = total == total ? ratio : total;  // (a NaN or +infinity among all logits)
+        else ratio = m < 0.0f ? ratio / (1.0f + expf(logit)) : mine;
+        if (lane < c.K) mine = ratio;
+    }
     float sum = mine;
     for (int off = 4; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     weight = (c.renormalise ? mine / sum : mine) * c.scale;
