@@ -141,9 +141,18 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// One column.
+// One column, and the wait behind which a group of them is used.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t &r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld1_wait(uint32_t (&r)[kGroup][2]) {
+    static_assert(kGroup == 8, "as many registers below");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[1][0]), "+r"(r[1][1]), "+r"(r[2][0]), "+r"(r[2][1]),
+                   "+r"(r[3][0]), "+r"(r[3][1]), "+r"(r[4][0]), "+r"(r[4][1]), "+r"(r[5][0]), "+r"(r[5][1]),
+                   "+r"(r[6][0]), "+r"(r[6][1]), "+r"(r[7][0]), "+r"(r[7][1])
+                 :
+                 : "memory");
 }
 
 // A K block among all jobs'.
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                 };
                 if (!filled()) break;
                 for (int g = 0; g < w.rows; g += kGroup) {
-                    uint32_t v[kGroup][2];
+                    uint32_t v[kGroup][2] = {};
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) {
                         if (g + i < w.rows) {
@@ -434,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_rows_kernel(const __grid_cons
                             tmem_ld1(at + R, v[i][1]);
                         }
                     }
-                    tmem_ld_wait();
+                    tmem_ld1_wait(v);
 #pragma unroll
                     for (int i = 0; i < kGroup; ++i) {
                         if (g + i < w.rows) {
