@@ -120,7 +120,8 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
  *
  * Outputs, strides, codes, in-place h, limits and alignments as for
  * a2av_rms_norm; beta [H] T, mean [rows] float32.  The squares are summed about
- * the mean; a row whose squares overflow fp32 gets rstd 0.
+ * the mean; a row whose squares overflow fp32 gets rstd 0, one whose sum does has
+ * an infinite mean and no y.
  */
 typedef struct {
     int64_t rows, H;

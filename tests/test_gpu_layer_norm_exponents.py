@@ -96,3 +96,28 @@ def test_exponents_within_a_few_units_of_a_power_of_two(rows, H, repeat, dt, qty
         assert not bad.any(), (int(bad.sum()), int((bad & close)[0::2].sum()), int((bad & close)[1::2].sum()), off[bad][:4].tolist())
     # rows of both kinds have such blocks, and plain fp32 puts some of each on the wrong side
     assert min(blocks.values()) > 40 and min(plain_wrong.values()) > 4, (blocks, plain_wrong)
+
+
+@pytest.mark.parametrize("M", [0, 1, 3, 40, 300, 700, 1000, 1900])
+@pytest.mark.parametrize("spread", [1, 4, 30])
+def test_statistics_of_rows_at_any_distance_from_zero(M, spread):
+    """Whole numbers around M: values, sums and the mean of a power of two of them are exact in fp32.  A thread's sum of up to
+    16 squares is rounded 17 times, half a unit of fp32 each: 2^-20 of the variance, 2^-21 of rstd.  The same rows in
+    several calls, one with a value that differs in a thousand."""
+    rng = np.random.default_rng([M, spread])
+    x = M + rng.integers(-spread, spread + 1, (40, 2048)).astype(np.float64)
+    x[20:] = M
+    x[20:, 77] = M + spread
+    want, s = torch.from_numpy(x), torch.from_numpy(x).half()
+    gamma = torch.ones(2048, dtype=torch.float16, device="cuda")
+    f = L.layer_norm(s, None, gamma.cpu(), None, EPS)
+    assert torch.equal(f["s"], want)
+    for qtype, mode in ((None, "mx"), ("e4m3fn", "mx"), ("e4m3fn", "group128")):
+        for repeat in (1, 40):
+            r = binding.a2av_layer_norm(s.cuda().repeat(repeat, 1), gamma, None, None, EPS, qtype, mode, want_y=True, want_stats=True)
+            mean, rstd = (t.cpu().double().view(repeat, 40) for t in (r.mean, r.rstd))
+            assert bool(((mean - f["mean"]).abs() <= 2.0 ** -24 * f["mean"].abs()).all())
+            assert bool(((rstd - f["rstd"]).abs() <= 2.0 ** -20 * f["rstd"]).all())
+            y = r.y.cpu().double().view(repeat, 40, 2048)
+            err = 2.0 ** -20 * f["y"].abs() + 2.0 ** -22
+            assert bool(((y - f["y"]).abs() <= err * (1 + 2.0 ** -11) + 2.0 ** -11 * f["y"].abs() + 2.0 ** -24).all())

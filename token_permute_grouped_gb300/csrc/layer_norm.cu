@@ -9,8 +9,8 @@
 // the registers of one block between its sums and the scaling, the next row's
 // values are requested before the current one is reduced.  Values and squares are
 // summed in one reduction; where the mean is more than half of the deviation, the
-// squares are summed again about the mean, from what the registers hold, so that
-// a row's offset costs no digits.  With codes the instructions count as much as HBM:
+// squares are summed again about a short value next to the mean, from what the
+// registers hold, so that a row's offset costs no digits.  With codes the instructions count as much as HBM:
 // gamma and beta wait in shared memory as fp32 (109 us against 115.6 for mx codes).
 // 12,288 x 7168 bf16 rows with a residual: to mx codes 107 us, to codes per 128 100
 // (6.1 TB/s, 92% of a copy's rate; 127 with a reduction a sum in every row).
@@ -203,25 +203,34 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
         const float mean = mu;
         // The squares about the mean are those about 0 less H mu^2 = mu total, each in
         // two parts.  Where that is more than a quarter of what is left, or the squares
-        // about 0 overflow, the values are taken about the mean, and the squares summed anew.
+        // about 0 overflow, the values are taken about c, and the squares summed anew.  c
+        // is the mean's first 12 bits: a 16-bit value's difference from it is exact, and
+        // mu - c below a quarter of the deviation, as the mean was before; or, in rows
+        // that are a thousand times nearer to their mean than to 0, the mean in fp32.
         const float m = mu * total.x, m_lo = fmaf(mu, total.x, -m) + (mu * total.y + mu_lo * total.x);
-        if (squares.x < inf && squares.x - m > 4.0f * m) {
+        const float left = squares.x - m;
+        if (squares.x < inf && left > 4.0f * m) {
             two_sum(squares.x, squares.y, -m, -m_lo);
         } else {
+            const uint32_t bits = squares.x < inf && left > 0x1p-18f * m ? 0xfffff000u : 0xffffffffu;
+            const float c = __uint_as_float(__float_as_uint(mu) & bits);
             sq2 = 0;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 if (t + k * T < vecs) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        s[k][i] = add2(add2(s[k][i], both(-mu)), both(-mu_lo));
+                        s[k][i] = add2(s[k][i], both(-c));
                         sq2 = fma2(s[k][i], s[k][i], sq2);
                     }
                 }
             }
-            mu = mu_lo = 0.0f;
+            mu = fabsf(mu) < inf ? mu - c : 0.0f;
             split(sq2, sq, sq_odd);
             squares = row_sum(sq + sq_odd, again, t, T, 0);
+            const float d2 = mu * mu, e = H * d2;  // H (mu - c)^2, likewise (mu - c is of 12 bits, its square exact)
+            if (e > 0.0f) two_sum(squares.x, squares.y, -e, -fmaf(2.0f * H * mu, mu_lo, fmaf(H, d2, -e)));
+            if (squares.x < 0.0f) squares = make_float2(0.0f, 0.0f);
         }
         float var_lo, rstd_lo;
         const float var = mean_of(squares, H, inv, var_lo);
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
             if (p.rstd) p.rstd[row] = rstd;
         }
         if (!Q::kAny && !p.y) continue;
-        const f32x2 scale = both(rstd), shift = both(-fmaf(mu, rstd, mu_lo * rstd));  // (mu is below half of the deviation)
+        const f32x2 scale = both(rstd), shift = both(-fmaf(mu, rstd, mu_lo * rstd));  // (mu is below half of the deviation here)
         f32x2 y[VPT][4];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -249,7 +258,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
         }
         if constexpr (Q::kAny) {
             // y's roundings and those of the mean and of rstd, each with its error: near pw,
-            // the difference of the sum's head from it is exact.
+            // the difference of the sum's head from it is exact.  (What stays are the roundings
+            // of a thread's sums of values and squares.)
             const auto reaches = [&](int k, float pw) {
                 const int v = t + k * T;
                 if (v >= vecs) return false;
