@@ -517,9 +517,10 @@ __global__ void __launch_bounds__(32 * kSlices) column_sums_kernel(const float *
 // Blocks of the gradient and threads of one, one block an SM (as the RMS norm's gradient, rms_norm.cu).
 constexpr int kGradBlocks = 152;
 constexpr int kGradThreads = 512;
-// Threads an SM that the norm's grid is made for (us, 1024 / 2048): codes of 12,288 x
-// 7168 88 / 94.5, of 32,768 x 512 16 / 19; rows only, 4096 x 2048 14 / 9.6, 16,384 x
-// 1024 18 / 15.4.  (512: 115, 22, 18 and 29.)
+// Threads an SM that the norm's grid is made for (us, 1024 / 2048, without a residual):
+// codes per 128 of 12,288 x 7168 88 / 94.5, of 32,768 x 512 16 / 19; rows only, 4096 x
+// 2048 14 / 9.6, 16,384 x 1024 18 / 15.4.  (512: 115, 22, 18 and 29.)  2048 are not
+// resident at 64 registers a thread: blocks that wait start as soon as others end.
 constexpr int kCodeThreadsPerSm = 1024, kPlainThreadsPerSm = 2048;
 
 struct GradShape {
@@ -542,11 +543,14 @@ cudaError_t launch_norm_type(const LayerNormLaunch &p, int kind, int sms, cudaSt
         const int per_sm = kind == kQuantNone ? kPlainThreadsPerSm : kCodeThreadsPerSm;
         return launch(p, kind, threads, std::min(p.rows, sms * std::max(1, per_sm / threads)), stream);
     };
-    // A vector a thread where all rows are on the SMs at once, and there are no next
-    // rows' values to hold (us, one vector / two: 1 x 7168 2.5 / 2.7, 128 x 7168 3.2 /
-    // 3.9, 300 x 4096 3.3 / 4.4, 600 x 2048 3.3 / 4.6, 2000 x 512 3.2 / 4.1; with more
-    // rows 1024 x 4096 8.5 / 7.6, 12,288 x 7168 125 / 88).
-    if (static_cast<int64_t>(p.rows) * threads_for(vecs, 1) <= static_cast<int64_t>(sms) * 1024 && vecs <= 1024) return go(launch_norm_vpt<BF16, 1>, 1);
+    // A vector a thread where all rows are on the SMs at once (its 64 registers leave an
+    // SM 1024 threads), and there are no next rows' values to hold.  Without a residual, us,
+    // one vector / two: codes per 128 of 1 x 7168 2.5 / 2.7, 128 x 7168 3.2 / 3.9, 152 x
+    // 5376 2.8 / 2.9, 304 x 4096 3.1 / 3.3, 600 x 2048 3.3 / 4.6, 2000 x 512 3.2 / 4.1, rows
+    // only, 300 x 4096 3.0 / 3.5; past the limit codes 153 x 5376 4.0 / 4.0, 305 x 4096 3.8 /
+    // 4.5, 400 x 4096 5.0 / 5.0, 1024 x 4096 8.5 / 7.6, 12,288 x 7168 125 / 87, rows only, 153
+    // x 5376 4.2 / 3.1, 200 x 5376 5.2 / 3.5, 400 x 4096 4.6 / 3.9.
+    if (vecs <= 1024 && p.rows <= sms * (1024 / threads_for(vecs, 1))) return go(launch_norm_vpt<BF16, 1>, 1);
     if (vecs <= 2048) return go(launch_norm_vpt<BF16, 2>, 2);
     if (vecs <= 4096) return go(launch_norm_vpt<BF16, 4>, 4);
     return go(launch_norm_vpt<BF16, 8>, 8);
