@@ -87,10 +87,12 @@ size_t staged_bytes(const a2av_gmm_g128_desc *d) {
     return d->W > 1 ? round256(static_cast<size_t>(d->A) * d->H1) : 0;
 }
 
-// Mean rows of a (source, expert) run from which whole halves are read in place
-// (us, in place / all copied; 8 sources, 8 experts of 2048 x 2816, runs of 64: 35 /
-// 33, 96: 56 / 51, 128: 73 / 72; of 7168 x 2048, 256: 217 / 241).
-constexpr int64_t kLongRun = 96;
+// Mean rows of a (source, expert) run from which whole halves are read in place (us, in
+// place / all copied, medians of ten: 8 sources, 8 experts of 2048 x 2816, runs of 64: 35 /
+// 33.5, 96: 53 / 49, 128: 70 / 69, 160: 82 / 81, 192: 89 / 87, 256: 111 / 109; 16 sources, 8
+// of 4096 x 2048, 128: 150 / 154; 4 of 4096 x 4096, 192: 195 / 200; 8 of 7168 x 2048, 256:
+// 224 / 242; 8 of 7168 x 4096, 32 sources, 135: 827 / 814, 8 sources, 539: 764 / 812).
+constexpr int64_t kLongRun = 192;
 
 }  // namespace
 
