@@ -120,8 +120,9 @@ a2av_status a2av_rms_norm_backward(int64_t rows, int64_t H, int32_t dtype, const
  *
  * Outputs, strides, codes, in-place h, limits and alignments as for
  * a2av_rms_norm; beta [H] T, mean [rows] float32.  The squares are summed about
- * the mean; a row whose squares overflow fp32 gets rstd 0, one whose sum does has
- * an infinite mean and no y.
+ * the mean.  They and the sums are fp32: a row whose squares overflow gets rstd 0,
+ * one whose sum does an infinite mean and NaN for y; squares below fp32's range
+ * are 0 (which eps covers, unless it is 0).
  */
 typedef struct {
     int64_t rows, H;

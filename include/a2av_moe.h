@@ -11,7 +11,11 @@
  *     y = residual + sum over k of w_k (act(x Wg_k) * (x Wu_k)) Wd_k
  *
  * Each expert's weights are read once for the tokens that chose it.  Larger
- * batches go through a2av_gated_run and a2av_gmm_run.
+ * batches go through a2av_gated_run and a2av_gmm_run.  A call has four or five
+ * kernels whose start and end take 20 to 30 us however small the experts are: for
+ * less than about 30 MB of weights and more than a few tokens those two products,
+ * with a router of the caller's own, may be the better path (64 tokens, 4 of 4
+ * experts of 3288 x 192: 70 us, the two products 30).
  *
  *   x, residual, y [T, H] T (residual may be NULL: 0; y may be x or residual)
  *   router [E, H] T or float32; bias [E] float32 (may be NULL; it takes part in

@@ -12,8 +12,12 @@
 // squares are summed again about a short value next to the mean, from what the
 // registers hold, so that a row's offset costs no digits.  With codes the instructions count as much as HBM:
 // gamma and beta wait in shared memory as fp32 (109 us against 115.6 for mx codes).
-// 12,288 x 7168 bf16 rows with a residual: to mx codes 107 us, to codes per 128 100
-// (6.1 TB/s, 92% of a copy's rate; 127 with a reduction a sum in every row).
+// 12,288 x 7168 bf16 rows with a residual: to mx codes 106 us, to codes per 128 99
+// (6.2 TB/s, 93% of a copy's rate; 127 with a reduction a sum in every row); in rows
+// that are summed again 137 and 122.  Without a residual, 43% of the bytes, 94 and 86:
+// bound by the instructions.  Above 16,384 values a row, four or eight vectors a thread,
+// registers are spilled: 2048 x 20,480 to codes per 128 97, 1024 x 65,408 450 (40 and 70
+// at a copy's rate).
 #include <algorithm>
 
 #include "activation.cuh"
@@ -563,10 +567,12 @@ cudaError_t launch_layer_norm(const LayerNormLaunch &p, bool bf16, int kind, int
 }
 
 // Up to so many turns of their rows by the blocks of one cluster, whose sums are
-// then all of them: one launch, no workspace.  An eager call is bound by the host
-// there, and takes 20 us instead of 28 (61 rows of 4096).  On the GPU, in a graph
-// (us, cluster / two kernels): 32 x 2048 5.6 / 5.1, 16 x 7168 6.8 / 7.1, 61 x 4096
-// 8.4 / 5.9, 256 x 1024 9.2 / 6.5; four turns of 8 blocks 9.9 / 5.9.
+// then all of them: one launch, no workspace.  The rule is made for eager calls, which
+// are bound by the host there: 19 to 21 us against 24 to 26 at all these sizes.  On the
+// GPU, in a graph, the two kernels would be faster but for few wide rows (us, cluster /
+// two kernels): 9 x 2048 5.0 / 5.0, 32 x 2048 5.6 / 5.1, 128 x 2048 8.2 / 5.6, 16 x 4096
+// 5.7 / 5.5, 61 x 4096 8.5 / 5.8, 16 x 7168 6.6 / 6.8, 32 x 7168 8.3 / 6.9, 256 x 1024 8.8 /
+// 6.2; four turns of 8 blocks, 61 x 4096, 9.9.
 constexpr int kClusterBlocks = 16, kClusterTurns = 2;
 constexpr int64_t kClusterWidth = 8192;  // the sums of a block in 64 KB
 

@@ -33,8 +33,8 @@
 //
 // Measured with the router's two kernels (weights from HBM, us; in brackets what the
 // weights of all experts would take at a plain copy's 6.68 TB/s): 1 token, 4 of 32
-// experts of 2048 x 1024 27; 32 tokens 82 [60]; 1 token, 6 of 64 of 2048 x 1408 37,
-// 32 tokens 178 [166]; 1 token, 2 of 8 of 4096 x 4096 49, 32 tokens 148 [121].
+// experts of 2048 x 1024 27; 32 tokens 82 to 87 [60]; 1 token, 6 of 64 of 2048 x 1408 37,
+// 32 tokens 178 [166]; 1 token, 2 of 8 of 4096 x 4096 50, 32 tokens 150 [121].
 // Per CTA: warps 0, 6 and 7 load, warp 1 issues the MMAs, warps 2-5 are the
 // epilogue (all eight make the plan).  Every wait is bounded.
 #include <algorithm>
@@ -53,9 +53,9 @@ namespace {
 
 constexpr int kThreads = 8 * 32;
 // Tokens up to which the last CTA of a job of the second kernel adds its shares; above,
-// a kernel behind it (us, last CTA / kernel: 1 token, 7 of 49 experts of 384 x 384 20 /
-// 27, 4 of 32 of 2048 x 1024 27.5 / 28.5; 8 tokens 32 / 36, 55 / 59; 16 tokens 47 / 41,
-// 83 / 80.5; 64 tokens 90 / 50, 113 / 96.5).
+// a kernel behind it (us, last CTA / kernel: 1 token, 7 of 49 experts of 384 x 384 19 /
+// 24, 4 of 32 of 2048 x 1024 27 / 28; 8 tokens 31.5 / 40, 59 / 61; 16 tokens 45 / 40, 78 /
+// 80; 64 tokens 89 / 48, 102 / 91).
 constexpr int kAloneTokens = 8;
 constexpr int kMmaWarp = 1;
 constexpr int kEpiWarp0 = 2;
