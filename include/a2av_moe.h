@@ -28,8 +28,8 @@
  * to 2^-15 of it (bf16) or to 2^-22 of it or 2^-35, whichever is larger (fp16;
  * values beyond twice fp16's range are infinite).  So y's error is that of its own
  * rounding, in fp16 unless down or scale are large enough to bring values about
- * 2^-35 into it.  Without a bias the choice is made on the logits themselves.  A NaN logit is chosen last; a token's NaN or infinity
- * reaches no other token.
+ * 2^-35 into it.  Without a bias the choice is made on the logits themselves.  A
+ * NaN logit is chosen last; a token's NaN or infinity reaches no other token.
  *
  * Limits: 0 <= T <= 64, 1 <= E <= 256, 1 <= K <= 8, K <= E, 0 < H, N < 65536 and
  * multiples of 8; T tensors, router and bias 16-byte, experts and weights 4-byte

@@ -158,10 +158,11 @@ a2av_status a2av_gmm_g128_run(const a2av_gmm_g128_desc *desc, const void *ataOut
     }
     const int64_t strips = ceil_div(d.N1, 128);
     // Waves of single CTAs' tiles and of pairs', each expert's last tile half full: a
-    // pair's takes 1.5 times as long for four times the work (us, single / pairs: 128 rows of 1024 x 1024 5.5 / 8.2,
-    // 512 of 2048 x 2048 8.4 / 12.5, 300 over 4 experts of 4096 x 2048 15 / 20, 1634
-    // over 16 of 2048 x 2816 29 / 35, 1000 over 32 of 4096 x 1536 48 / 54; 2048 over 4 of
-    // 2048 x 1408 21 / 18, 4096 over 8 of 2048 x 2816 48 / 37, 16,384 over 8 143 / 114).
+    // pair's takes 1.5 times as long for four times the work (us, single / pairs: 128 rows
+    // of 1024 x 1024 5.5 / 8.2, 512 of 2048 x 2048 8.4 / 12.5, 300 over 4 experts of 4096 x
+    // 2048 15 / 20, 1634 over 16 of 2048 x 2816 29 / 35, 1000 over 32 of 4096 x 1536 48 /
+    // 54; 2048 over 4 of 2048 x 1408 21 / 18, 4096 over 8 of 2048 x 2816 48 / 37, 16,384 over
+    // 8 143 / 114).
     const int64_t single = ceil_div((ceil_div(d.A, 128) + d.e / 2) * strips, dev->sms);
     const int64_t pairs = ceil_div((ceil_div(d.A, 256) + d.e / 2) * ceil_div(strips, 2), dev->clusters);
     g.pair = 2 * single >= 3 * pairs;

@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormLaunch 
         // two parts.  Where that is more than a quarter of what is left, or the squares
         // about 0 overflow, the values are taken about c, and the squares summed anew.  c
         // is the mean's first 12 bits: a 16-bit value's difference from it is exact, and
-        // mu - c below a quarter of the deviation, as the mean was before; or, in rows
-        // that are a thousand times nearer to their mean than to 0, the mean in fp32.
+        // mu - c below a quarter of the deviation; or, where the mean is over 500 times the
+        // deviation (or the squares about 0 overflow), the mean in fp32.
         const float m = mu * total.x, m_lo = fmaf(mu, total.x, -m) + (mu * total.y + mu_lo * total.x);
         const float left = squares.x - m;
         if (squares.x < inf && left > 4.0f * m) {
